@@ -694,12 +694,14 @@ int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, con
         add_chunk(row, std::max(m * C, sp.w), std::min((m + 1) * C, sp.n), m * C, q, k,
                   slot_base, merge_base);
     } else {
-      // k equal page-aligned parts, so no short remainder chunk launches last
+      // k equal page-aligned parts, so no short remainder chunk launches last.  Every part gets a
+      // page at least (the merge counts k of them): k <= ceil(a / ps), so the parts before the
+      // last end below n also where parts shorter than a page were rounded up
       const int64_t a = sp.n - sp.w;
       int64_t b = sp.w, tile0 = sp.w / ps * ps, q = 0;
       for (int64_t m = 1; m <= k; ++m) {
-        const int64_t e = m == k ? sp.n : (sp.w + a * m / k) / ps * ps;
-        if (e <= b) continue;
+        const int64_t e =
+            m == k ? sp.n : std::max((sp.w + a * m / k) / ps * ps, (b / ps + 1) * ps);
         add_chunk(row, b, e, tile0, q++, k, slot_base, merge_base);
         b = e;
         tile0 = e;
