@@ -21,7 +21,17 @@
  *     "host" pointers are ordinary CPU memory.  Every buffer is owned by the caller.
  *   - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream).
  *   - dtype codes: PKD_DTYPE_F16 (IEEE half), PKD_DTYPE_BF16, PKD_DTYPE_E4M3 (fp8 e4m3fn,
- *     KV only).
+ *     KV only), PKD_DTYPE_E2M1 (4 bits, KV only).
+ *
+ * The 4-bit cache (PKD_DTYPE_E2M1).  A K or V row of head_dim values is held as head_dim / 2
+ * code bytes, value 2i in the low half of byte i, and head_dim / 16 scale bytes: value d is
+ * e2m1(code d) * e4m3(scale d / 16), times the call's k_scale or v_scale.  Codes and scales are
+ * two pools of one layout, [.., head_dim / 2] and [.., head_dim / 16] bytes, with strides of
+ * their own.  The e2m1 values of codes 0..7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign.
+ * A row is written (pkd_append) with scale = e4m3(amax / (6 * k_scale)) over each 16 values and
+ * code = e2m1(x / (k_scale * scale)), both rounded to nearest with ties to even from the exact
+ * quotient and held to the type's largest value; a block that holds a NaN gets a NaN scale, so
+ * that it reads back as NaNs.
  *
  * Semantics (the page fixes the shapes; these readings fill what it leaves open):
  *   kv_len[i] = page_size * (indptr[i+1] - indptr[i] - 1) + last_page_len[i]  (0 if the
@@ -53,10 +63,12 @@ extern "C" {
 /* Bits of the device status word (pkd_check_status). */
 #define PKD_STATUS_TIMEOUT 1u  /* a pipeline wait ran out: the kernel gave up, outputs incomplete */
 #define PKD_STATUS_BAD_PAGE 2u /* a page id outside [0, num_pages) was read (as zeros) */
+#define PKD_STATUS_BAD_TOKEN 4u /* pkd_append / pkd_gather skipped a row that has no slot */
 
 #define PKD_DTYPE_F16 0
 #define PKD_DTYPE_BF16 1
 #define PKD_DTYPE_E4M3 2
+#define PKD_DTYPE_E2M1 3 /* 4-bit KV only: two values a byte, an e4m3 scale per 16 values */
 
 #define PKD_LAYOUT_NHD 0 /* page block [page_size, num_kv_heads, head_dim] */
 #define PKD_LAYOUT_HND 1 /* page block [num_kv_heads, page_size, head_dim] */
@@ -102,13 +114,14 @@ int pkd_reset_workspace(pkd_handle* h, void* float_ws, size_t float_ws_bytes, vo
  *     PKD_STATUS_BAD_PAGE in the status word; pkd_check_page_table checks a host copy of
  *     the table up front.
  *   num_qo_heads must be a multiple of num_kv_heads.  head_dim in {64, 128, 256}
- *   (e4m3 KV: {128, 256}).  page_size a power of two in [8, 256].
+ *   (e4m3 KV: {128, 256}).  page_size a power of two in [8, 256].  E2M1 KV runs on the
+ *   tensor-core kernel alone, without ROPE_LLAMA (keys are rotated as they are appended).
  *   sm_scale: NaN selects 1/sqrt(head_dim).  logits_soft_cap <= 0: no cap.
  *   window_left < 0: no window.  fixed_split_size > 0: split every request into chunks of
  *   that many pages counted from its first page, so the result of a request does not depend
  *   on the rest of the batch; disable_split_kv != 0: one chunk per request; otherwise a
  *   heuristic sizes chunks to fill the GPU.
- *   q_dtype / o_dtype: F16 or BF16, equal; kv_dtype: q_dtype or E4M3.
+ *   q_dtype / o_dtype: F16 or BF16, equal; kv_dtype: q_dtype, E4M3 or E2M1.
  *   use_tensor_cores: PKD_KERNEL_AUTO, PKD_KERNEL_CUDA_CORE or PKD_KERNEL_TENSOR_CORE.
  *   q_len_per_req >= 1 (the page's run(q_len_per_req), fixed here because the work list
  *     depends on it): query tokens per request.  They are the request's last positions:
@@ -162,6 +175,22 @@ int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* 
                   int64_t num_pages, const int64_t kv_strides[3], float q_scale,
                   float k_scale, float v_scale, void* o, float* lse, void* stream,
                   void* ev_start, void* ev_end);
+
+/*
+ * Run a plan whose kv_dtype is PKD_DTYPE_E2M1 (pkd_run refuses it, and this call refuses every
+ * other plan).  Arguments as in pkd_run_timed, and the scale pools:
+ *   k_base / v_base, kv_strides: the code pools; strides in bytes, multiples of 16 as above.
+ *   k_scales / v_scales (device), scale_strides[3]: scale byte (page, slot, head, block) of K / V
+ *     lives at base + page*scale_strides[0] + slot*scale_strides[1] + head*scale_strides[2] +
+ *     block.  Strides in bytes, in any order; bases and strides are multiples of head_dim / 16
+ *     (4, 8 or 16 bytes: a token's scales are one copy).
+ * A slot outside a request's attended tokens may hold anything, NaN scales among it.
+ */
+int pkd_run_scaled(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
+                   int64_t num_pages, const int64_t kv_strides[3], const void* k_scales,
+                   const void* v_scales, const int64_t scale_strides[3], float q_scale,
+                   float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
+                   void* ev_end);
 
 /*
  * Programmatic dependent launch (the page's run(enable_pdl=...)), on by default.  When on, the
@@ -354,6 +383,160 @@ int pkd_set_wait_limit(pkd_handle* h, uint64_t limit_ns);
  */
 int pkd_check_page_table(const int32_t* indptr_host, int batch, const int32_t* indices_host,
                          int64_t num_indices, int64_t num_pages);
+
+/*
+ * ---------------------------------------------------------------- operators on a page cache
+ *
+ * The calls below fill, read back and move the pools that decode reads.  They take no handle and
+ * keep nothing: each is one launch (pkd_copy_pages: one per PKD_COPY_PAIRS pairs and
+ * PKD_COPY_POOLS pools) on `stream`, asynchronous, capturable in a CUDA graph, with page tables
+ * and token lists read on the device.
+ */
+
+/* One layer's pool of K and V and the page table of its sequences. */
+typedef struct pkd_paged_pool {
+  void* k; /* element (page, slot, head, d) of K at k + (page*strides[0] + slot*strides[1] + */
+  void* v; /* head*strides[2] + d) elements; E2M1: code bytes, strides in bytes */
+  void* k_scales; /* E2M1: scale bytes, scale_strides in bytes; else NULL */
+  void* v_scales;
+  int64_t num_pages;
+  int64_t strides[3];
+  int64_t scale_strides[3];
+  const int32_t* indptr;  /* device [batch + 1]: sequence b owns indices[indptr[b] .. indptr[b+1]) */
+  const int32_t* indices; /* device [num_indices]: physical page ids */
+  int64_t num_indices;
+  int32_t batch;
+  int32_t dtype; /* PKD_DTYPE_* of the cache */
+  int32_t num_kv_heads;
+  int32_t head_dim;  /* 64, 128 or 256 */
+  int32_t page_size; /* a power of two in [1, 2^20] */
+  float k_scale;     /* value = stored value * k_scale (v_scale): positive, finite, 1 if unused */
+  float v_scale;
+  int32_t reserved;
+} pkd_paged_pool;
+
+/*
+ * Append token rows to a cache, with the norm of each query and key head and the position
+ * rotation in the same pass.  Row t of q / k / v belongs to sequence batch_indices[t] at
+ * position positions[t].  For every head of q and of k:
+ *   x *= 1 / sqrt(mean(x^2) + eps) * weight        if q_weight (k_weight) is not NULL
+ *   the pairs of the first rotary_dim dims, (i, i + rotary_dim / 2) or with interleaved
+ *   (2i, 2i + 1), turn: (a, b) -> (a cos - b sin, b cos + a sin), cos = cos_sin[p][i],
+ *   sin = cos_sin[p][rotary_dim / 2 + i], p = rope_positions[t] (NULL: positions[t])
+ * q goes to q_out, rounded once; k and v go to slot positions[t] % page_size of page
+ * indices[indptr[b] + positions[t] / page_size], divided by k_scale / v_scale and rounded once to
+ * the cache's type: 16-bit caches of the input's type to nearest, E4M3 to nearest within +-448,
+ * E2M1 as described at the top.  The codes of E4M3 and E2M1 are those of exact arithmetic.
+ * Sums and products are held in 32 bits (64 where a code's rounding is in doubt).
+ *   - A row whose batch index is negative is padding: nothing of it is read or written.
+ *   - A row with no slot (batch index >= batch, position negative or past the sequence's pages)
+ *     writes no k and v and sets PKD_STATUS_BAD_TOKEN; a page id outside [0, num_pages) likewise,
+ *     with PKD_STATUS_BAD_PAGE.  Its q is still written.  A rotation position outside
+ *     [0, cos_sin_rows) leaves the whole row out, with PKD_STATUS_BAD_TOKEN.
+ *   - Two rows of one call must not have the same slot (nor one sequence share a page that it
+ *     appends to with another: see pkd_pages_fork).
+ * q may be NULL (num_qo_heads 0), and k with v NULL (only q is normed and rotated).  q_out may be
+ * q itself.  All of q, k, v, q_out: in_dtype F16 or BF16, head_dim contiguous, 16-byte aligned,
+ * strides {token, head} in elements, multiples of 8.  Weights: head_dim values of in_dtype, or
+ * float32 with weight_f32; 16-byte aligned.  rotary_dim: 0 or a multiple of 16 up to head_dim;
+ * cos_sin float32 [cos_sin_rows, rotary_dim], contiguous, 16-byte aligned.
+ * status (device, NULL to leave out) receives the PKD_STATUS_* bits by OR; nothing clears it.
+ */
+typedef struct pkd_append_args {
+  pkd_paged_pool pool;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_strides[2];
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+  int64_t q_out_strides[2];
+  const int32_t* batch_indices;  /* device [num_tokens] */
+  const int32_t* positions;      /* device [num_tokens] */
+  const int32_t* rope_positions; /* device [num_tokens] or NULL */
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  int64_t cos_sin_rows;
+  uint32_t* status;
+  int64_t num_tokens;
+  double eps;
+  int32_t num_qo_heads;
+  int32_t in_dtype;
+  int32_t weight_f32;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t reserved;
+} pkd_append_args;
+int pkd_append(const pkd_append_args* args, void* stream);
+
+/*
+ * Read token rows of a cache back: row t of k_out and v_out receives what slot positions[t] of
+ * sequence batch_indices[t] holds, times k_scale / v_scale, rounded once to out_dtype (F16 or
+ * BF16; for a 16-bit cache its own type).  Rows of padding (negative batch index) and rows with no
+ * slot are left as they were, the latter with a status bit as in pkd_append.
+ * k_out / v_out: head_dim contiguous, 16-byte aligned, strides {token, head} in elements,
+ * multiples of 8; either may be NULL.  A row may be listed any number of times.
+ */
+typedef struct pkd_gather_args {
+  pkd_paged_pool pool;
+  void* k_out;
+  void* v_out;
+  int64_t k_out_strides[2];
+  int64_t v_out_strides[2];
+  const int32_t* batch_indices;
+  const int32_t* positions;
+  uint32_t* status;
+  int64_t num_tokens;
+  int32_t out_dtype;
+  int32_t reserved;
+} pkd_gather_args;
+int pkd_gather(const pkd_gather_args* args, void* stream);
+
+/*
+ * Copy pages dst_pages[i] <- src_pages[i] in every one of n_pools pools (every layer's K, V and
+ * scales): page p of pool j is the page_bytes[j] bytes at bases[j] + p * page_strides[j].
+ * src_pages / dst_pages: host arrays, travelling with the launch (nothing is uploaded, and they
+ * are free again when the call returns).  Every id must lie in [0, num_pages), a destination may
+ * appear once and may be no source: the copies run at the same time.  page_strides[j] >=
+ * page_bytes[j].  INVALID_ARG otherwise, and nothing is copied.
+ */
+#define PKD_COPY_PAIRS 2048
+#define PKD_COPY_POOLS 256
+int pkd_copy_pages(void* const* bases, const int64_t* page_strides, const int64_t* page_bytes,
+                   int n_pools, int64_t num_pages, const int32_t* src_pages,
+                   const int32_t* dst_pages, int64_t n_pairs, void* stream);
+
+/*
+ * Bookkeeping of a pool's pages (host memory only; no CUDA call): which pages are free and how
+ * many sequences share each one.  Free pages are handed out lowest id first.  Calls on one
+ * pkd_pages object must not overlap.
+ *   pkd_pages_alloc   n free pages into out, each then used once; INVALID_ARG if fewer are free
+ *                     (out is then left alone).
+ *   pkd_pages_free    one use less of each of the n pages (a page listed twice loses two); a page
+ *                     without uses is free.  INVALID_ARG if a page is not in use so often; nothing
+ *                     changes then.
+ *   pkd_pages_fork    a second sequence with the first kv_len tokens of one that owns `pages`
+ *                     (n_pages, ceil(kv_len / page_size) of them needed): out receives its page
+ *                     ids.  Full pages are shared (one use more); a partly filled last page is
+ *                     replaced by a fresh one, and *copy_src / *copy_dst receive the pair to copy
+ *                     (pkd_copy_pages) before either sequence appends; -1 where none is needed.
+ *   pkd_pages_compact moves the pages in use to the lowest ids: src / dst (room for num_pages
+ *                     each) receive *n_moves pairs to copy, highest sources into lowest free
+ *                     destinations, and remap[num_pages] every page's new id (its own if it stays
+ *                     or is free).  The caller copies, then rewrites its page tables with remap.
+ *   pkd_pages_count   *n_free free pages; uses (room for num_pages, or NULL) every page's uses.
+ */
+typedef struct pkd_pages pkd_pages;
+int pkd_pages_create(pkd_pages** out, int64_t num_pages);
+int pkd_pages_destroy(pkd_pages* p);
+int pkd_pages_alloc(pkd_pages* p, int64_t n, int32_t* out);
+int pkd_pages_free(pkd_pages* p, const int32_t* pages, int64_t n);
+int pkd_pages_fork(pkd_pages* p, const int32_t* pages, int64_t n_pages, int64_t kv_len,
+                   int page_size, int32_t* out, int32_t* copy_src, int32_t* copy_dst);
+int pkd_pages_compact(pkd_pages* p, int32_t* src, int32_t* dst, int64_t* n_moves, int32_t* remap);
+int pkd_pages_count(pkd_pages* p, int64_t* n_free, int32_t* uses);
 
 /*
  * pkd_decode_noalloc -- plan + run in one call, using only scratch memory built into the

@@ -22,10 +22,10 @@ ERRORS = {
     -5: "PKD_ERR_UNSUPPORTED",
     -6: "PKD_ERR_DEVICE",
 }
-DTYPE_F16, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
+DTYPE_F16, DTYPE_BF16, DTYPE_E4M3, DTYPE_E2M1 = 0, 1, 2, 3
 LAYOUT_NHD, LAYOUT_HND = 0, 1
 KERNEL_AUTO, KERNEL_CUDA_CORE, KERNEL_TENSOR_CORE = -1, 0, 1
-STATUS_TIMEOUT, STATUS_BAD_PAGE = 1, 2
+STATUS_TIMEOUT, STATUS_BAD_PAGE, STATUS_BAD_TOKEN = 1, 2, 4
 
 # every symbol include/pkd.h declares, with its ctypes signature (pointers, host or device, pass
 # as addresses)
@@ -42,6 +42,20 @@ SIGNATURES = {
                          _vp, _vp, _vp]),
     "pkd_run_timed": (_c_int, [_vp, _vp, _vp, _vp, ctypes.c_int64, _i64p, _c_float, _c_float,
                                _c_float, _vp, _vp, _vp, _vp, _vp]),
+    "pkd_run_scaled": (_c_int, [_vp, _vp, _vp, _vp, ctypes.c_int64, _i64p, _vp, _vp, _i64p, _c_float,
+                                _c_float, _c_float, _vp, _vp, _vp, _vp, _vp]),
+    # the argument structs travel as packed bytes (cache.py)
+    "pkd_append": (_c_int, [ctypes.c_char_p, _vp]),
+    "pkd_gather": (_c_int, [ctypes.c_char_p, _vp]),
+    "pkd_copy_pages": (_c_int, [_vp, _vp, _vp, _c_int, ctypes.c_int64, _vp, _vp, ctypes.c_int64, _vp]),
+    "pkd_pages_create": (_c_int, [ctypes.POINTER(_vp), ctypes.c_int64]),
+    "pkd_pages_destroy": (_c_int, [_vp]),
+    "pkd_pages_alloc": (_c_int, [_vp, ctypes.c_int64, _vp]),
+    "pkd_pages_free": (_c_int, [_vp, _vp, ctypes.c_int64]),
+    "pkd_pages_fork": (_c_int, [_vp, _vp, ctypes.c_int64, ctypes.c_int64, _c_int, _vp,
+                                ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
+    "pkd_pages_compact": (_c_int, [_vp, _vp, _vp, _i64p, _vp]),
+    "pkd_pages_count": (_c_int, [_vp, _i64p, _vp]),
     "pkd_destroy": (_c_int, [_vp]),
     "pkd_last_error": (ctypes.c_char_p, []),
     "pkd_workspace_bytes": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,

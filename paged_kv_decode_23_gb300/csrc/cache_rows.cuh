@@ -1,0 +1,132 @@
+// cache_rows.cuh -- device code shared by the kernels that write and read rows of a paged cache:
+// rows of head_dim values spread over head_dim / 8 lanes, eight consecutive values a lane.
+#pragma once
+
+#include "cache_ops.cuh"
+#include "pkd_device.cuh"
+
+namespace pkd {
+namespace rows {
+
+using dev::pack2;
+using dev::unpack2;
+
+enum CacheKind { kSame16 = 0, kFp8 = 1, kFp4 = 2 };
+
+// Bytes of eight values in a cache of kind KV.
+template <int KV>
+__host__ __device__ constexpr int bytes8() { return KV == kSame16 ? 16 : KV == kFp8 ? 8 : 4; }
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const float2 a = unpack2<T>(v.x), b = unpack2<T>(v.y), c = unpack2<T>(v.z), d = unpack2<T>(v.w);
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]),
+                    pack2<T>(x[6], x[7]));
+}
+
+// Where a token's rows live: the page id and the slot in it.
+struct Slot {
+  int64_t page;
+  int slot;
+  uint32_t status;  // 0, or the PKD_STATUS_* bit that says why there is none
+};
+
+// Bounds-checked walk of the page table; reads nothing outside indptr[0 .. batch] and
+// indices[0 .. num_indices).
+__device__ __forceinline__ Slot find_slot(const pkd_paged_pool& p, int page_log, int b, int pos) {
+  Slot s{0, pos & ((1 << page_log) - 1), PKD_STATUS_BAD_TOKEN};
+  if (b < 0 || b >= p.batch || pos < 0) return s;
+  const int64_t first = __ldg(p.indptr + b), end = __ldg(p.indptr + b + 1);
+  const int64_t at = first + (pos >> page_log);
+  if (first < 0 || at >= end || at >= p.num_indices) return s;
+  s.page = __ldg(p.indices + at);
+  s.status = s.page >= 0 && s.page < p.num_pages ? 0u : PKD_STATUS_BAD_PAGE;
+  return s;
+}
+
+// Address of eight values (lane gl of the row) of one head in the K or V pool.
+template <int KV>
+__device__ __forceinline__ char* row_addr(void* base, const int64_t (&st)[3], const Slot& s, int head,
+                                          int gl) {
+  constexpr int kUnit = KV == kSame16 ? 2 : 1;  // bytes a stride unit
+  return static_cast<char*>(base) +
+         (s.page * st[0] + (int64_t)s.slot * st[1] + (int64_t)head * st[2]) * kUnit +
+         gl * bytes8<KV>();
+}
+__device__ __forceinline__ uint8_t* scale_addr(void* base, const int64_t (&st)[3], const Slot& s,
+                                               int head, int gl) {
+  return static_cast<uint8_t*>(base) + s.page * st[0] + (int64_t)s.slot * st[1] +
+         (int64_t)head * st[2] + (gl >> 1);
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+// Codes of two values >= 0 (or NaN), nearest with ties to even, at most the type's largest: of
+// `lo` in the low half of the result, of `hi` above it (8 bits each in e4m3, 4 in e2m1).
+template <int KV>
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+  if constexpr (KV == kFp8) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+  } else {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t, z;\n\tmov.b16 {z, t}, 0;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+        "mov.b32 %0, {t, z, z, z};\n\t}"
+        : "=r"(r)
+        : "f"(hi), "f"(lo));
+    return r;
+  }
+}
+template <int KV>
+__device__ __forceinline__ float code_value(uint32_t code) {
+  if constexpr (KV == kFp8) return e4m3_value(code);
+  // e2m1, from its definition: codes 0 and 1 are 0 and 0.5, else (1 + m / 2) 2^(e - 1)
+  const uint32_t e = code >> 1, m = code & 1;
+  return e == 0 ? 0.5f * m : __uint_as_float((e + 126u) << 23 | m << 22);
+}
+
+// A double as a float whose last bit is set if anything was cut off (rounding to odd): a further
+// rounding to nearest, to a type of at most 22 bits, then gives what the double itself rounds to.
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = __double2float_rz(x);
+  return (double)f != x && f == f && fabsf(f) < __int_as_float(0x7f800000)
+             ? __uint_as_float(__float_as_uint(f) | 1u)
+             : f;
+}
+
+// The code nearest to a / (m * unit), m a value of few bits and a >= 0, known only through the
+// approximation t of that quotient with |t - quotient| <= e.
+//   exact:  a is exact; the doubt is settled by the sign of a - mid * m * unit, mid being the
+//           border between the two codes (one rounding in an FMA keeps a sign), ties to even.
+//   else:   *doubt is set when the codes of t - e and t + e differ.
+template <int KV>
+__device__ __forceinline__ uint32_t nearest_code(float a, float t, float e, float m, float unit,
+                                                 bool exact, bool* doubt) {
+  constexpr int kBits = KV == kFp8 ? 8 : 4;
+  t = t > 1e30f ? 1e30f : t;  // (keeps a NaN)
+  e = fminf(e, 1e30f);
+  const float low = t - e;
+  const uint32_t c = codes2<KV>(low < 0.f ? 0.f : low, t + e);
+  const uint32_t lo = c & ((1u << kBits) - 1), hi = (c >> kBits) & ((1u << kBits) - 1);
+  if (lo == hi) return lo;
+  if (!exact) {
+    *doubt = true;
+    return lo;
+  }
+  const float mid = 0.5f * (code_value<KV>(lo) + code_value<KV>(hi));
+  const float r = fmaf(-(mid * m), unit, a);
+  return r > 0.f || (r == 0.f && (hi & 1) == 0) ? hi : lo;
+}
+
+}  // namespace rows
+}  // namespace pkd

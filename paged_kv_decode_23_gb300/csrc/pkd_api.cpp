@@ -46,6 +46,7 @@ void init_registry() {
     register_decode_rope(g_decode);
     register_decode_rope_cc(g_decode);
     register_decode_rope_cc_e4m3(g_decode);
+    register_decode_e2m1(g_decode);
     register_mla(g_mla);
     register_mla_tc(g_mla);
   });
@@ -218,14 +219,19 @@ int staging_release(pkd_handle* h, int slot, cudaStream_t s) {
 
 // 4-D TMA view of one K or V pool: dims (d, head, slot, page) for NHD and (d, slot, head, page)
 // for HND, i.e. ordered by increasing stride; a box is 128 bytes of d by `box_rows` slots of
-// one head of one page, landing 128-byte swizzled in shared memory.
+// one head of one page, landing 128-byte swizzled in shared memory.  An E2M1 pool is a pool of
+// head_dim / 2 code bytes a row, with boxes of 64 bytes of them (all 32 at head_dim 64) and the
+// swizzle of that width.
 int make_kv_tensor_map(CUtensorMap* map, const void* base, int kv_dtype, int head_dim, int page_size,
                        int num_kv_heads, int64_t num_pages, const int64_t strides[3], int layout,
                        int box_rows) {
   std::string why;
   EncodeTiledFn enc = get_encode_fn(&why);
   if (!enc) return fail(PKD_ERR_CUDA, why);
-  const int elt = kv_dtype == kE4M3 ? 1 : 2;
+  const bool fp4 = kv_dtype == kE2M1;
+  const int elt = kv_dtype == kE4M3 || fp4 ? 1 : 2;
+  const int row_elts = fp4 ? head_dim / 2 : head_dim;  // elements of a row
+  const int box_bytes = !fp4 ? 128 : row_elts < 64 ? 32 : 64;
   const CUtensorMapDataType dt = kv_dtype == kF16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : kv_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -247,13 +253,16 @@ int make_kv_tensor_map(CUtensorMap* map, const void* base, int kv_dtype, int hea
     box[1] = (cuuint32_t)box_rows;
     box[2] = 1;
   }
-  dims[0] = (cuuint64_t)head_dim;
+  dims[0] = (cuuint64_t)row_elts;
   dims[3] = (cuuint64_t)num_pages;
   gstr[2] = (cuuint64_t)page_b;
-  box[0] = (cuuint32_t)(128 / elt);
+  box[0] = (cuuint32_t)(box_bytes / elt);
   box[3] = 1;
+  const CUtensorMapSwizzle swizzle = box_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                       : CU_TENSOR_MAP_SWIZZLE_32B;
   CUresult r = enc(map, dt, 4, const_cast<void*>(base), dims, gstr, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     char buf[256];
@@ -495,8 +504,11 @@ int pkd_plan(pkd_handle* h, const int32_t* indptr_host, const int32_t* last_page
   if (q_dtype != PKD_DTYPE_F16 && q_dtype != PKD_DTYPE_BF16)
     return fail(PKD_ERR_INVALID_ARG, "q_dtype must be F16 or BF16");
   if (o_dtype != q_dtype) return fail(PKD_ERR_UNSUPPORTED, "o_dtype must equal q_dtype");
-  if (kv_dtype != q_dtype && kv_dtype != PKD_DTYPE_E4M3)
-    return fail(PKD_ERR_UNSUPPORTED, "kv_dtype must equal q_dtype or be E4M3");
+  if (kv_dtype != q_dtype && kv_dtype != PKD_DTYPE_E4M3 && kv_dtype != PKD_DTYPE_E2M1)
+    return fail(PKD_ERR_UNSUPPORTED, "kv_dtype must equal q_dtype or be E4M3 or E2M1");
+  if (kv_dtype == PKD_DTYPE_E2M1 && pos_encoding_mode == PKD_POS_ROPE_LLAMA)
+    return fail(PKD_ERR_UNSUPPORTED,
+                "ROPE_LLAMA is not built for E2M1 KV (rotate the keys as they are appended)");
   if (batch > 0 && !indices_dev) return fail(PKD_ERR_INVALID_ARG, "indices_dev is null");
   if (batch > 0 && num_indices < (int64_t)indptr_host[batch])
     return fail(PKD_ERR_INVALID_ARG, "indices holds fewer than indptr[batch] page ids");
@@ -699,14 +711,26 @@ int cached_kv_tensor_map(pkd_handle* h, CUtensorMap* map, const void* base, int6
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
-                  int64_t num_pages, const int64_t kv_strides[3], float q_scale, float k_scale,
-                  float v_scale, void* o, float* lse, void* stream, void* ev_start, void* ev_end) {
+// The scale pools of an E2M1 run (pkd_run_scaled).
+struct ScalePools {
+  const void* k;
+  const void* v;
+  const int64_t* strides;
+};
+
+// pkd_run_timed (sf null) and pkd_run_scaled.
+int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
+               int64_t num_pages, const int64_t kv_strides[3], const ScalePools* sf, float q_scale,
+               float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
+               void* ev_end) {
   if (!h) return fail(PKD_ERR_INVALID_ARG, "handle is null");
   if (!h->planned || h->mla)
     return fail(PKD_ERR_NOT_PLANNED, "pkd_run called before a successful pkd_plan");
+  if ((h->kv_dtype == kE2M1) != (sf != nullptr))
+    return fail(PKD_ERR_INVALID_ARG,
+                "a plan with E2M1 KV runs with pkd_run_scaled, every other plan without scale pools");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (h->n_tasks == 0 && !h->graph) return PKD_OK;  // empty batch
   if (!q || !k_base || !v_base || !o || !kv_strides)
@@ -715,11 +739,11 @@ int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* 
     return fail(PKD_ERR_INVALID_ARG, "num_pages must lie in [1, 2^31]");
   if (!aligned(k_base, 16) || !aligned(v_base, 16) || !aligned(q, 16) || !aligned(o, 16))
     return fail(PKD_ERR_INVALID_ARG, "q, o and the K/V bases must be 16-byte aligned");
-  const int elt = h->kv_dtype == kE4M3 ? 1 : 2;
+  const int elt = h->kv_dtype == kE4M3 || sf ? 1 : 2;
   for (int i = 0; i < 3; ++i)
     if (kv_strides[i] <= 0 || (kv_strides[i] * elt) % 16 != 0)
       return fail(PKD_ERR_INVALID_ARG, "kv strides must be positive multiples of 16 bytes");
-  const int64_t D = h->head_dim;
+  const int64_t D = sf ? h->head_dim / 2 : h->head_dim;  // elements of a row
   const bool nhd = h->layout == PKD_LAYOUT_NHD;
   const int64_t inner = nhd ? kv_strides[2] : kv_strides[1];  // stride of the faster of slot/head
   const int64_t outer = nhd ? kv_strides[1] : kv_strides[2];
@@ -730,8 +754,27 @@ int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* 
                 "kv strides do not match the handle's layout (NHD: page > slot > head >= "
                 "head_dim; HND: page > head > slot >= head_dim, without overlap)");
 
-  DecodeParams prm;
-  std::memset(&prm, 0, sizeof prm);
+  if (sf) {
+    const int64_t sb = h->head_dim / 16;
+    if (!sf->k || !sf->v || !sf->strides)
+      return fail(PKD_ERR_INVALID_ARG, "null k_scales / v_scales / scale_strides");
+    if (!aligned(sf->k, sb) || !aligned(sf->v, sb))
+      return fail(PKD_ERR_INVALID_ARG, "the scale pools must be aligned to head_dim / 16 bytes");
+    for (int i = 0; i < 3; ++i)
+      if (sf->strides[i] <= 0 || sf->strides[i] % sb != 0)
+        return fail(PKD_ERR_INVALID_ARG,
+                    "scale strides must be positive multiples of head_dim / 16 bytes");
+  }
+
+  // the E2M1 kernels take the decode parameters followed by their scale pools
+  DecodeE2m1Params prm_all;
+  std::memset(static_cast<void*>(&prm_all), 0, sizeof prm_all);
+  DecodeParams& prm = prm_all;
+  if (sf) {
+    prm_all.k_sf = static_cast<const uint8_t*>(sf->k);
+    prm_all.v_sf = static_cast<const uint8_t*>(sf->v);
+    for (int i = 0; i < 3; ++i) prm_all.sf_stride[i] = sf->strides[i];
+  }
   const int tile = h->kernel->tile_tokens;
   const int box_rows = h->page_size < tile ? h->page_size : tile;
   int rc = cached_kv_tensor_map(h, &prm.tmap_k, k_base, num_pages, kv_strides, box_rows);
@@ -799,6 +842,27 @@ int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* 
 
   // split (row, kv head, slice) units are merged by the CTA that finishes their last chunk
   return PKD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
+                  int64_t num_pages, const int64_t kv_strides[3], float q_scale, float k_scale,
+                  float v_scale, void* o, float* lse, void* stream, void* ev_start, void* ev_end) {
+  return run_decode(h, q, k_base, v_base, num_pages, kv_strides, nullptr, q_scale, k_scale, v_scale,
+                    o, lse, stream, ev_start, ev_end);
+}
+
+int pkd_run_scaled(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
+                   int64_t num_pages, const int64_t kv_strides[3], const void* k_scales,
+                   const void* v_scales, const int64_t scale_strides[3], float q_scale,
+                   float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
+                   void* ev_end) {
+  const ScalePools sf{k_scales, v_scales, scale_strides};
+  return run_decode(h, q, k_base, v_base, num_pages, kv_strides, &sf, q_scale, k_scale, v_scale, o,
+                    lse, stream, ev_start, ev_end);
 }
 
 int pkd_run(pkd_handle* h, const void* q, const void* k_base, const void* v_base,

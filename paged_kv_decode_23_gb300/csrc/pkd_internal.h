@@ -59,7 +59,7 @@ static_assert(sizeof(DecodeTask) == 48, "DecodeTask is 12 int32");
 // Rows of one partial slot: the qo heads of one task (a slice holds at most 8).
 constexpr int kSlotHeads = 8;
 
-enum DType { kF16 = 0, kBF16 = 1, kE4M3 = 2 };
+enum DType { kF16 = 0, kBF16 = 1, kE4M3 = 2, kE2M1 = 3 };
 
 // Default (and largest) limit of a kernel's pipeline waits, in ns of the global timer.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
@@ -107,6 +107,15 @@ struct DecodeParams {
   float v_scale;
 };
 
+// The parameters of a kernel over a 4-bit cache: K and V maps over the code pools, and the e4m3
+// scale of (page, slot, head, block) at base + page*sf_stride[0] + slot*sf_stride[1] +
+// head*sf_stride[2] + block.
+struct DecodeE2m1Params : DecodeParams {
+  const uint8_t* k_sf;
+  const uint8_t* v_sf;
+  int64_t sf_stride[3];
+};
+
 // A compiled decode kernel and how to launch it.
 struct DecodeKernel {
   int kind;         // KernelKind
@@ -129,6 +138,7 @@ void register_decode_e4m3(std::vector<DecodeKernel>& out);
 void register_decode_rope(std::vector<DecodeKernel>& out);
 void register_decode_rope_cc(std::vector<DecodeKernel>& out);
 void register_decode_rope_cc_e4m3(std::vector<DecodeKernel>& out);
+void register_decode_e2m1(std::vector<DecodeKernel>& out);
 
 // MLA decode kernel parameters (pkd_mla_run -> mla_decode_kernel).
 struct MlaParams {

@@ -377,8 +377,8 @@ int decode_geometry(const PlanRequest& r, DecodeSchedule* s, const char** err) {
     *err = "num_qo_heads must be a positive multiple of num_kv_heads";
     return kErrInvalidD;
   }
-  if (r.kv_dtype != kF16 && r.kv_dtype != kBF16 && r.kv_dtype != kE4M3) {
-    *err = "kv_dtype must be F16, BF16 or E4M3";
+  if (r.kv_dtype != kF16 && r.kv_dtype != kBF16 && r.kv_dtype != kE4M3 && r.kv_dtype != kE2M1) {
+    *err = "kv_dtype must be F16, BF16, E4M3 or E2M1";
     return kErrInvalidD;
   }
   if (r.head_dim != 64 && r.head_dim != 128 && r.head_dim != 256) {
@@ -387,6 +387,10 @@ int decode_geometry(const PlanRequest& r, DecodeSchedule* s, const char** err) {
   }
   if (r.kv_dtype == kE4M3 && r.head_dim == 64) {
     *err = "e4m3 KV needs head_dim 128 or 256 (rows of whole 128-byte blocks)";
+    return kErrUnsupportedD;
+  }
+  if (r.kv_dtype == kE2M1 && r.use_tensor_cores == 0) {
+    *err = "E2M1 KV runs on the tensor-core kernel alone";
     return kErrUnsupportedD;
   }
   if (r.page_size < 8 || r.page_size > 256 || (r.page_size & (r.page_size - 1)) != 0) {
@@ -432,7 +436,8 @@ int decode_geometry(const PlanRequest& r, DecodeSchedule* s, const char** err) {
     s->heads_per_cta = gp;
   }
   s->gslices = (G + s->heads_per_cta - 1) / s->heads_per_cta;
-  s->tile_tokens = 16384 / (r.head_dim * (r.kv_dtype == kE4M3 ? 1 : 2));
+  s->tile_tokens = 16384 / (r.head_dim * (r.kv_dtype == kE4M3 || r.kv_dtype == kE2M1 ? 1 : 2));
+  if (s->tile_tokens > 128) s->tile_tokens = 128;  // at most 8 consumer warps of 16 tokens
   return 0;
 }
 

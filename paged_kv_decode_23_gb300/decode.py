@@ -17,16 +17,47 @@ import torch
 
 from . import _lib as L
 
+E2M1 = "e2m1"  # the 4-bit KV cache: not every torch has a dtype for it
 _DTYPE_CODE = {torch.float16: L.DTYPE_F16, torch.bfloat16: L.DTYPE_BF16,
-               torch.float8_e4m3fn: L.DTYPE_E4M3}
+               torch.float8_e4m3fn: L.DTYPE_E4M3, E2M1: L.DTYPE_E2M1}
 _STR_DTYPE = {"float16": torch.float16, "half": torch.float16, "bfloat16": torch.bfloat16,
-              "float8_e4m3fn": torch.float8_e4m3fn, "e4m3": torch.float8_e4m3fn}
+              "float8_e4m3fn": torch.float8_e4m3fn, "e4m3": torch.float8_e4m3fn,
+              "float4_e2m1fn_x2": E2M1, E2M1: E2M1}
+# torch dtypes of a 4-bit cache's codes (two a byte) and of its scales
+CODE_DTYPES = tuple(getattr(torch, n) for n in ("uint8", "float4_e2m1fn_x2") if hasattr(torch, n))
+SCALE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _as_dtype(x):
-    if x is None or isinstance(x, torch.dtype):
+    if x is None or (isinstance(x, torch.dtype) and x not in CODE_DTYPES[1:]):
         return x
     return _STR_DTYPE[str(x).replace("torch.", "")]
+
+
+def pool_views(paged_kv_cache, kv_layout: str, what: str = "paged_kv_cache"):
+    """A page pool as ``(k, v, strides, page_size, num_kv_heads)``: k and v address K and V of
+    (page 0, slot 0, head 0), strides are those of (page, slot, head) in elements."""
+    if isinstance(paged_kv_cache, (tuple, list)):
+        k, v = paged_kv_cache
+        st = k.stride()
+        if k.dim() != 4 or k.shape != v.shape or st != v.stride() or k.dtype != v.dtype:
+            raise ValueError(f"{what}: (k, v) must be 4-D tensors of one shape, stride and dtype")
+        shape, kp, vp = k.shape, k.data_ptr(), v.data_ptr()
+        if v.device != k.device:
+            raise ValueError(f"{what}: k and v must be on one device")
+    else:
+        k = paged_kv_cache
+        st, shape = k.stride(), k.shape
+        if len(shape) != 5 or shape[1] != 2:
+            raise ValueError(f"{what} must be [pages, 2, ...]")
+        kp = k.data_ptr()
+        vp = kp + st[1] * k.element_size()
+        st, shape = (st[0], st[2], st[3], st[4]), (shape[0], shape[2], shape[3], shape[4])
+    if st[3] != 1 and shape[3] != 1:
+        raise ValueError(f"{what} must have its last axis contiguous")
+    if kv_layout == "NHD":
+        return kp, vp, (st[0], st[1], st[2]), shape[1], shape[2]
+    return kp, vp, (st[0], st[2], st[1]), shape[2], shape[1]
 
 
 def _host_i32(t) -> np.ndarray:
@@ -167,7 +198,8 @@ class BatchDecodePagedKV:
         here): the request's last positions, each attending causally; q / o then have
         ``batch * q_len_per_req`` rows, request-major.  ``pos_encoding_mode``: "NONE",
         "ROPE_LLAMA" (with ``rope_scale`` / ``rope_theta``, defaults 1 and 1e4) or
-        "ALIBI"."""
+        "ALIBI".  ``kv_data_type``: q's type, float8_e4m3fn, or "e2m1" (torch's float4_e2m1fn_x2)
+        for a cache in 4 bits, which runs on the tensor-core kernel without ROPE_LLAMA."""
         if block_tables is not None or seq_lens is not None:
             raise NotImplementedError("block_tables / seq_lens (the trtllm-gen backend's page "
                                       "table form) are not built; pass indptr / indices / "
@@ -208,6 +240,8 @@ class BatchDecodePagedKV:
     # ------------------------------------------------------------------ run
     def _kv_pointers(self, paged_kv_cache):
         a = self._plan_args
+        if a["kv_dtype"] == E2M1:
+            a = dict(a, head_dim=a["head_dim"] // 2)  # two values a byte
         if isinstance(paged_kv_cache, (tuple, list)):
             k, v = paged_kv_cache
             if k.dim() != 4 or v.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
@@ -240,10 +274,15 @@ class BatchDecodePagedKV:
             v_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
             lse: Optional[torch.Tensor] = None, return_lse: bool = False, stream=None,
             timing_events=None, enable_pdl: Optional[bool] = None,
-            q_len_per_req: Optional[int] = None):
+            q_len_per_req: Optional[int] = None, kv_block_scales=None):
         """Decode attention for the planned batch on one layer's pool: returns ``o`` or
         ``(o, lse)`` (lse: float32 natural log, ``[batch, num_qo_heads]``).  ``enable_pdl``
-        switches programmatic dependent launch for this and later runs (on by default)."""
+        switches programmatic dependent launch for this and later runs (on by default).
+
+        A plan with ``kv_data_type="e2m1"`` (4 bits) takes the codes as ``paged_kv_cache`` (uint8
+        or float4_e2m1fn_x2, last axis head_dim / 2) and their e4m3 scales, one per 16 values, as
+        ``kv_block_scales`` (float8_e4m3fn or uint8, last axis head_dim / 16; a 5-D tensor or a
+        (k, v) pair in the same layout)."""
         a = self._plan_args
         if a is None:
             raise RuntimeError("plan() must be called before run()")
@@ -254,7 +293,7 @@ class BatchDecodePagedKV:
         if tuple(q.shape) != exp_q or q.dtype != a["q_dtype"] or not q.is_contiguous():
             raise ValueError(f"q must be a contiguous {a['q_dtype']} tensor of shape {exp_q}")
         kv, k_ptr, v_ptr, num_pages, strides = self._kv_pointers(paged_kv_cache)
-        if kv.dtype != a["kv_dtype"]:
+        if kv.dtype not in (CODE_DTYPES if a["kv_dtype"] == E2M1 else (a["kv_dtype"],)):
             raise ValueError(f"KV dtype {kv.dtype} does not match the plan ({a['kv_dtype']})")
         if out is None:
             out = torch.empty(exp_q, dtype=a["o_dtype"], device=q.device)
@@ -268,6 +307,27 @@ class BatchDecodePagedKV:
         if enable_pdl is not None:
             L.check(L.lib().pkd_set_pdl(self._h, int(bool(enable_pdl))))
         ev0, ev1 = timing_events if timing_events is not None else (None, None)
+        if (kv_block_scales is not None) != (a["kv_dtype"] == E2M1):
+            raise ValueError("kv_block_scales belongs to a plan with kv_data_type 'e2m1', and such "
+                             "a plan needs it")
+        if kv_block_scales is not None:
+            sf = kv_block_scales[0] if isinstance(kv_block_scales, (tuple, list)) else kv_block_scales
+            ks, vs, sf_strides, ps, hkv = pool_views(kv_block_scales, self.kv_layout, "kv_block_scales")
+            if (sf.dtype not in SCALE_DTYPES or sf.shape[-1] != a["head_dim"] // 16
+                    or (sf.shape[0], ps, hkv) != (num_pages, a["page_size"], a["num_kv_heads"])):
+                raise ValueError("kv_block_scales must be float8_e4m3fn (or uint8) of the cache's "
+                                 "shape with a last axis of head_dim / 16")
+            if not (q.device == kv.device == sf.device == self._float_ws.device):
+                raise ValueError("q, the cache, its scales and the workspace must be on one device")
+            L.check(L.lib().pkd_run_scaled(
+                self._h, q.data_ptr(), k_ptr, v_ptr, num_pages, st, ks, vs,
+                (ctypes.c_int64 * 3)(*sf_strides), 1.0 if q_scale is None else float(q_scale),
+                1.0 if k_scale is None else float(k_scale),
+                1.0 if v_scale is None else float(v_scale), out.data_ptr(),
+                lse.data_ptr() if lse is not None else None, _stream_ptr(stream),
+                ev0.cuda_event if ev0 is not None else None,
+                ev1.cuda_event if ev1 is not None else None))
+            return (out, lse) if return_lse else out
         L.check(L.lib().pkd_run_timed(
             self._h, q.data_ptr(), k_ptr, v_ptr, num_pages, st,
             1.0 if q_scale is None else float(q_scale), 1.0 if k_scale is None else float(k_scale),
