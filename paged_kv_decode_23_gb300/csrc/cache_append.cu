@@ -1,18 +1,22 @@
 // cache_append.cu -- token rows into a paged cache, with the norm of each query and key head and
 // the position rotation in the same pass (pkd_append).
 //
-// A row of one head is spread over head_dim / 8 lanes, eight values (16 bytes) each: the sum of
-// squares is a shuffle tree over those lanes, the rotation partner of the half-split form is the
-// value of another lane (one shuffle), that of the interleaved form is in the lane itself, and a
-// block of the 4-bit cache is two lanes.  A group of lanes takes R heads of one token, R of them
-// loaded before the first is used; cos and sin are read once for them.
+// A row of one head is spread over a group of head_dim / 8 lanes, eight values (16 bytes) each: the
+// sum of squares is a shuffle tree over the group, the rotation partner of the half-split form is
+// the value of another lane (one shuffle), that of the interleaved form is in the lane itself, and
+// a block of the 4-bit cache is two lanes.  A warp takes one token's neighbouring heads, all q, all
+// k or all v, up to R for each of its groups, and loads them before it uses the first; weights,
+// cosines and sines are read once for them, and all that depends on the token is the same in every
+// lane, so that every shuffle is the whole warp's (one over a part of it costs four instructions
+// more).  Pairs of values go through the packed 32-bit FMA.
 //
 // Codes.  A cache of 8 or 4 bits stores the code nearest to the exact quotient, so that neither
-// the order of a sum nor the lanes' roundings can show in it.  t, the quotient in 32 bits, comes
-// with a bound e on its error; where the codes of t - e and t + e agree (all but about one value
-// in 1e5) that is the code.  Otherwise: a value that comes straight from the input (v; k without
-// norm, outside the rotated dims) is exact, and an FMA against the border between the two codes
-// settles it, ties included; a computed value sends its warp through the row once more in 64 bits.
+// the order of a sum nor the lanes' roundings can show in it.  A value that comes straight from
+// the input (v; k without norm, outside the rotated dims) is exact: its quotient is rounded to odd
+// and that to the code.  Ties are common there, one value in eight with a scale of few bits.  A
+// computed value's quotient t has an error bound e: where the codes of t - e and t + e agree (all
+// but about one value in 1e5) that is the code, else its warp goes through its rows once more in
+// 64 bits.
 //
 // Bound: bytes.  Every input byte is read once and every output byte written once; see the
 // figures at the launcher.
@@ -27,11 +31,13 @@ using namespace rows;
 
 struct AppendParams {
   pkd_append_args a;
-  int64_t token0;    // first token of this launch
-  uint32_t items;    // (token, chunk of heads) pairs of this launch
-  uint32_t chunks;   // chunks of a token
-  int heads;         // Hq + 2 Hkv
+  int64_t token0;     // first token of this launch
+  uint32_t items;     // (token, chunk of heads) pairs of this launch, a warp each
+  uint32_t chunks;    // chunks of a token: qc of q, kc of k, kc of v
+  int qc, kc;
   int page_log;
+  float eps;          // a.eps in 32 bits (a conversion per row would take the 64-bit pipe)
+  float k_inv, v_inv;  // 1 / k_scale, 1 / v_scale
 };
 
 // Relative error bound of a computed value against the terms it is summed from: sums of squares
@@ -61,16 +67,15 @@ struct Codes {
   uint32_t scale;    // e2m1: the block's scale byte
 };
 
-// The codes of a computed key row, in 64 bits throughout.  Called by whole warps; `src` null for
-// lanes that have no such row.
+// The codes of a computed key row, in 64 bits throughout.  Called by whole warps.
 template <typename T, int KV, int D>
 __device__ __noinline__ Codes exact_codes(const T* src, const void* weight, int weight_f32,
-                                          const float* cs, int rotary, int interleaved, double eps,
-                                          float unit) {
+                                          const float* cs, int rotary,
+                                          int interleaved, double eps, float unit) {
   constexpr int LANES = D / 8;
   const int lane = threadIdx.x & 31, gl = lane & (LANES - 1);
-  float xf[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (src) unpack8<T>(*(reinterpret_cast<const uint4*>(src) + gl), xf);
+  float xf[8];
+  unpack8<T>(*(reinterpret_cast<const uint4*>(src) + gl), xf);
   double x[8];
   double ss = 0.0;
 #pragma unroll
@@ -80,7 +85,7 @@ __device__ __noinline__ Codes exact_codes(const T* src, const void* weight, int 
   }
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-  if (weight != nullptr && src) {
+  if (weight != nullptr) {
     float w[8];
     load_weight8(weight, weight_f32, gl, std::is_same<T, __nv_bfloat16>::value, w);
     const double r = 1.0 / sqrt(ss / D + eps);
@@ -89,7 +94,7 @@ __device__ __noinline__ Codes exact_codes(const T* src, const void* weight, int 
   }
   if (rotary) {
     const int half = rotary / 2;
-    const bool turned = 8 * gl < rotary && src != nullptr;
+    const bool turned = 8 * gl < rotary;
     if (interleaved) {
       if (turned) {
 #pragma unroll
@@ -147,186 +152,224 @@ __device__ __noinline__ Codes exact_codes(const T* src, const void* weight, int 
 }
 
 // The codes of a row from its values y in 32 bits, each with the sum `err` of the terms it was
-// computed from (unused where `exact`).  Whole warps; *doubt: some code needs exact_codes.
+// computed from (unused where `exact`); inv about 1 / unit.  Whole warps, whose lanes may differ in
+// `exact`; *doubt: some code needs exact_codes.
 template <int KV>
-__device__ __forceinline__ Codes quick_codes(const float (&y)[8], const float (&err)[8], bool exact,
-                                             float unit, bool* doubt) {
+__device__ __forceinline__ Codes quick_codes(const float (&y)[8], const float (&err)[8],
+                                             bool exact, float unit, float inv, bool* doubt) {
   Codes out{0, 0, 0};
-  float m = 1.f, inv = 1.f / unit;
+  float d = unit, dl = 0.f;  // the divisor and what its rounding left
   if constexpr (KV == kFp4) {
     float top = 0.f, off = 0.f;
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       top = fmaxf(top, fabsf(y[i]));
-      off = fmaxf(off, err[i]);
       nan |= y[i] != y[i];
+      if (!exact) off = fmaxf(off, err[i]);
     }
     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    off = fmaxf(off, __shfl_xor_sync(~0u, off, 1));
+    off = fmaxf(off, __shfl_xor_sync(~0u, off, 1));  // (lanes differ in exact)
     nan |= __shfl_xor_sync(~0u, (int)nan, 1) != 0;
-    const float t = top * (inv * 0.16666667f);
-    const float e = t * kQuotErr + (exact ? 0.f : off * (inv * 0.16666667f) * kValueErr);
-    out.scale = nan ? 0x7fu : nearest_code<kFp8>(top, t, e, 6.f, unit, exact, doubt);
-    m = e4m3_value(out.scale);
-    if (!(m > 0.f)) return out;  // a block of zeros (or a NaN's): all codes 0
-    inv = 1.f / (m * unit);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(y[i]);
-    const float t = a * inv;
-    const float e = t * kQuotErr + (exact ? 0.f : err[i] * inv * kValueErr);
-    const uint32_t c = nearest_code<KV>(a, t, e, m, unit, exact, doubt);
-    const uint32_t sign = __float_as_uint(y[i]) >> 31;
-    if constexpr (KV == kFp8) {
-      if (i < 4) out.lo |= (c | sign << 7) << (8 * i);
-      else out.hi |= (c | sign << 7) << (8 * (i - 4));
+    const float sixth = inv * 0.16666667f;
+    if (exact) {
+      const float six = 6.f * unit, t = odd_quotient(top, six, fmaf(6.f, unit, -six), sixth);
+      out.scale = codes2<kFp8>(t, t) & 0xffu;
     } else {
-      out.lo |= (c | sign << 3) << (4 * i);
+      const float t = top * sixth, e = off * sixth * (kValueErr + kQuotErr);
+      const uint32_t c = codes2<kFp8>(t - e, t + e);
+      out.scale = c & 0xffu;
+      *doubt = out.scale != c >> 8;
     }
+    if (nan) out.scale = 0x7fu;
+    const float m = e4m3_value(out.scale);
+    if (!(m > 0.f)) return out;  // a block of zeros (or a NaN's): all codes 0
+    d = m * unit;
+    dl = fmaf(m, unit, -d);
+    inv = rcp(d);
+  }
+  if (exact) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = odd_quotient(y[i], d, dl, inv);
+    const uint2 c = codes8<KV>(t);
+    out.lo = c.x;
+    out.hi = c.y;
+  } else {
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // (+ 0: a negative zero, from a zero head and a negative weight, is no doubt)
+      const float t = fmaf(y[i], inv, 0.f), e = err[i] * inv * (kValueErr + kQuotErr);
+      lo[i] = t - e;
+      hi[i] = t + e;
+    }
+    const uint2 a = codes8<KV>(lo), b = codes8<KV>(hi);
+    out.lo = a.x;
+    out.hi = a.y;
+    *doubt |= a.x != b.x || a.y != b.y;
   }
   return out;
 }
 
 template <typename T, int KV, int D, int R>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, KV == kSame16 ? 3 : 2) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LANES = D / 8;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const pkd_append_args& a = p.a;
+  constexpr int GROUPS = 32 / LANES;
   const int lane = threadIdx.x & 31, gl = lane & (LANES - 1);
-  const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-  const bool in = item < p.items;
-  const uint32_t tok = in ? item / p.chunks : 0;
-  const int c0 = in ? (int)(item - tok * p.chunks) : 0;
+  const uint32_t item = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (item >= p.items) return;  // whole warps from here on, until their last row is stored
+  const uint32_t tok = item / p.chunks;
+  int c = (int)(item - tok * p.chunks);
   const int64_t t = p.token0 + tok;
-  const int hq = a.num_qo_heads, hkv = a.pool.num_kv_heads;
+
+  // this warp's heads [h0, heads) of q, k or v: its group g takes h0 + g, h0 + g + GROUPS, ...
+  const int kind = c < p.qc ? 0 : c < p.qc + p.kc ? 1 : 2;
+  c -= kind == 0 ? 0 : kind == 1 ? p.qc : p.qc + p.kc;
+  const int heads = kind == 0 ? a.num_qo_heads : a.pool.num_kv_heads;
+  const int h0 = c * R * GROUPS + lane / LANES;
+  const int64_t st0 = kind == 0 ? a.q_strides[0] : kind == 1 ? a.k_strides[0] : a.v_strides[0];
+  const int64_t st1 = kind == 0 ? a.q_strides[1] : kind == 1 ? a.k_strides[1] : a.v_strides[1];
+  const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + t * st0;
+  const int b = __ldg(a.batch_indices + t);
+  const int pos = __ldg(a.positions + t);
   const int rotary = a.rotary_dim;
-
-  const int b = in ? __ldg(a.batch_indices + t) : -1;
-  const int pos = in ? __ldg(a.positions + t) : 0;
-  const int rpos = rotary && a.rope_positions && in ? __ldg(a.rope_positions + t) : pos;
-  const bool turnable = !rotary || (rpos >= 0 && rpos < a.cos_sin_rows);
-  const bool live = b >= 0 && turnable;
-
-  // this group's heads c0, c0 + chunks, ...: neighbouring groups read neighbouring rows
-  const T* src[R];
+  const int rpos = rotary && a.rope_positions ? __ldg(a.rope_positions + t) : pos;
   uint4 raw[R];
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int r = c0 + j * (int)p.chunks;
-    src[j] = nullptr;
-    raw[j] = make_uint4(0, 0, 0, 0);
-    if (live && r < p.heads) {
-      if (r < hq) src[j] = static_cast<const T*>(a.q) + t * a.q_strides[0] + r * a.q_strides[1];
-      else if (r < hq + hkv) src[j] = static_cast<const T*>(a.k) + t * a.k_strides[0] + (r - hq) * a.k_strides[1];
-      else src[j] = static_cast<const T*>(a.v) + t * a.v_strides[0] + (r - hq - hkv) * a.v_strides[1];
-      raw[j] = *(reinterpret_cast<const uint4*>(src[j]) + gl);
-    }
+  for (int j = 0; j < R; ++j) {  // (a padding row's values are read and dropped; no head: zeros)
+    const int h = h0 + j * GROUPS;
+    raw[j] = h < heads ? *(reinterpret_cast<const uint4*>(src + h * st1) + gl) : make_uint4(0, 0, 0, 0);
+  }
+  if (b < 0) return;
+  if (rotary && (rpos < 0 || rpos >= a.cos_sin_rows)) {
+    if (lane == 0 && a.status) atomicOr(a.status, PKD_STATUS_BAD_TOKEN);
+    return;
   }
   Slot slot{0, 0, 0};
-  if (live && c0 + (R - 1) * (int)p.chunks >= hq && hkv > 0) slot = find_slot(a.pool, p.page_log, b, pos);
-  if (gl == 0 && a.status) {
-    const uint32_t bits = (b >= 0 && !turnable ? PKD_STATUS_BAD_TOKEN : 0u) | slot.status;
-    if (bits) atomicOr(a.status, bits);
+  if (kind != 0) {
+    slot = find_slot(a.pool, p.page_log, b, pos);
+    if (slot.status) {
+      if (lane == 0 && a.status) atomicOr(a.status, slot.status);
+      return;
+    }
   }
-  float cs[8], sn[8];
+  const bool turned = kind != 2 && 8 * gl < rotary;
+  const void* w = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+  const float unit = kind == 2 ? a.pool.v_scale : a.pool.k_scale, inv = kind == 2 ? p.v_inv : p.k_inv;
   const int half = rotary / 2;
-  const bool turned = live && 8 * gl < rotary;
   const bool first = 8 * gl < half;
-  const float* cs_row = a.cos_sin + (turned || live ? (int64_t)rpos * rotary : 0);
+  const float* cs_row = rotary ? a.cos_sin + (int64_t)rpos * rotary : nullptr;
+  // cosines, and sines with the sign that this lane's values take their partners with
+  float cs[8], sn[8], wv[8];
   if (turned) {
     if (a.interleaved) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(cs_row + 4 * gl));
+      const float4 u = __ldg(reinterpret_cast<const float4*>(cs_row + 4 * gl));
       const float4 s = __ldg(reinterpret_cast<const float4*>(cs_row + half + 4 * gl));
-      cs[0] = cs[1] = c.x; cs[2] = cs[3] = c.y; cs[4] = cs[5] = c.z; cs[6] = cs[7] = c.w;
-      sn[0] = sn[1] = s.x; sn[2] = sn[3] = s.y; sn[4] = sn[5] = s.z; sn[6] = sn[7] = s.w;
+      cs[0] = cs[1] = u.x; cs[2] = cs[3] = u.y; cs[4] = cs[5] = u.z; cs[6] = cs[7] = u.w;
+      sn[1] = s.x; sn[3] = s.y; sn[5] = s.z; sn[7] = s.w;
+      sn[0] = -s.x; sn[2] = -s.y; sn[4] = -s.z; sn[6] = -s.w;
     } else {
       const int i0 = first ? 8 * gl : 8 * gl - half;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(cs_row + i0) + i);
+        const float4 u = __ldg(reinterpret_cast<const float4*>(cs_row + i0) + i);
         const float4 s = __ldg(reinterpret_cast<const float4*>(cs_row + half + i0) + i);
-        cs[4 * i] = c.x; cs[4 * i + 1] = c.y; cs[4 * i + 2] = c.z; cs[4 * i + 3] = c.w;
+        cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
         sn[4 * i] = s.x; sn[4 * i + 1] = s.y; sn[4 * i + 2] = s.z; sn[4 * i + 3] = s.w;
       }
+      if (first)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
   }
+  if (w) load_weight8(w, a.weight_f32, gl, kBf16, wv);
   const int from = (lane - gl) + ((first ? gl + half / 8 : gl - half / 8) & (LANES - 1));
 
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    const int r = c0 + j * (int)p.chunks;
-    const bool is_v = r >= hq + hkv;
-    const void* w = is_v ? nullptr : r < hq ? a.q_weight : a.k_weight;
-    float y[8];
+    const int h = h0 + j * GROUPS;
+    if (h0 - lane / LANES + j * GROUPS >= heads) break;  // the warp's last heads are done
+    const bool live = h < heads;
+    float y[8], err[8];  // err: |terms| that a value is the sum of
     unpack8<T>(raw[j], y);
-    // ---- norm (both weights are given or one of them: the shuffles are the warp's)
-    if (a.q_weight || a.k_weight) {
-      float ss = 0.f;
+    // ---- norm
+    if (w) {
+      float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+      for (int i = 0; i < 8; i += 2) ss = __ffma2_rn(make_float2(y[i], y[i + 1]), make_float2(y[i], y[i + 1]), ss);
+      float sum = ss.x + ss.y;
 #pragma unroll
-      for (int o = 1; o < LANES; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-      if (w && src[j]) {
-        float wv[8];
-        load_weight8(w, a.weight_f32, gl, kBf16, wv);
-        const float rn = rsqrtf(fmaf(ss, 1.f / D, (float)a.eps));
+      for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      const float rn = rsqrtf(fmaf(sum, 1.f / D, p.eps));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * rn * wv[i];
+      for (int i = 0; i < 8; i += 2) {
+        const float2 v = __fmul2_rn(__fmul2_rn(make_float2(y[i], y[i + 1]), make_float2(rn, rn)), make_float2(wv[i], wv[i + 1]));
+        y[i] = v.x;
+        y[i + 1] = v.y;
       }
     }
     // ---- rotation
-    float err[8];  // |terms| that a value is the sum of
+    if (KV != kSame16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) err[i] = fabsf(y[i]);
-    if (rotary) {
+      for (int i = 0; i < 8; ++i) err[i] = fabsf(y[i]);
+    }
+    if (rotary && kind != 2) {
       float other[8];
+      if (a.interleaved) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) other[i] = a.interleaved ? y[i ^ 1] : __shfl_sync(~0u, y[i], from);
-      if (turned && !is_v) {
+        for (int i = 0; i < 8; ++i) other[i] = y[i ^ 1];
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool minus = a.interleaved ? (i & 1) == 0 : first;
-          const float os = other[i] * (minus ? -sn[i] : sn[i]);
-          err[i] = fabsf(y[i] * cs[i]) + fabsf(os);
-          y[i] = fmaf(y[i], cs[i], os);
+        for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(~0u, y[i], from);
+      }
+      if (turned) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float2 os = __fmul2_rn(make_float2(other[i], other[i + 1]), make_float2(sn[i], sn[i + 1]));
+          const float2 cc = make_float2(cs[i], cs[i + 1]);
+          const float2 v = __ffma2_rn(make_float2(y[i], y[i + 1]), cc, os);
+          if (KV != kSame16) {
+            err[i] = fabsf(y[i] * cc.x) + fabsf(os.x);
+            err[i + 1] = fabsf(y[i + 1] * cc.y) + fabsf(os.y);
+          }
+          y[i] = v.x;
+          y[i + 1] = v.y;
         }
       }
     }
-    // ---- q out
-    if (src[j] && r < hq) {
-      T* dst = static_cast<T*>(a.q_out) + t * a.q_out_strides[0] + r * a.q_out_strides[1];
-      *(reinterpret_cast<uint4*>(dst) + gl) = pack8<T>(y);
+    // ---- out
+    if (kind == 0) {
+      T* dst = static_cast<T*>(a.q_out) + t * a.q_out_strides[0] + h * a.q_out_strides[1];
+      if (live) *(reinterpret_cast<uint4*>(dst) + gl) = pack8<T>(y);
+      continue;
     }
-    // ---- k and v into their slots
-    const bool store = src[j] && r >= hq && slot.status == 0;
-    const int head = is_v ? r - hq - hkv : r - hq;
+    char* dst = row_addr<KV>(kind == 2 ? a.pool.v : a.pool.k, a.pool.strides, slot, h, gl);
     if constexpr (KV == kSame16) {
-      if (store)
-        *reinterpret_cast<uint4*>(row_addr<KV>(is_v ? a.pool.v : a.pool.k, a.pool.strides, slot, head, gl)) =
-            pack8<T>(y);
+      if (live) *reinterpret_cast<uint4*>(dst) = kind == 2 ? raw[j] : pack8<T>(y);
     } else {
-      if (__any_sync(~0u, store)) {
-        const float unit = is_v ? a.pool.v_scale : a.pool.k_scale;
-        const bool exact = is_v || (!w && !turned);
-        bool doubt = false;
-        Codes c = quick_codes<KV>(y, err, exact, unit, &doubt);
-        if (__any_sync(~0u, doubt && store)) {
-          const Codes e = exact_codes<T, KV, D>(store && !is_v ? src[j] : nullptr, w, a.weight_f32,
-                                                cs_row, rotary, a.interleaved, a.eps, unit);
-          if (!exact) c = e;
-        }
-        if (store) {
-          char* dst = row_addr<KV>(is_v ? a.pool.v : a.pool.k, a.pool.strides, slot, head, gl);
-          if constexpr (KV == kFp8) *reinterpret_cast<uint2*>(dst) = make_uint2(c.lo, c.hi);
-          else *reinterpret_cast<uint32_t*>(dst) = c.lo;
-          if (KV == kFp4 && (gl & 1) == 0)
-            *scale_addr(is_v ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot, head, gl) =
-                (uint8_t)c.scale;
-        }
+      const bool exact = kind == 2 || (!w && !turned);
+      bool doubt = false;
+      Codes cd = quick_codes<KV>(y, err, exact, unit, inv, &doubt);
+      if (__any_sync(~0u, doubt && live)) {
+        // (a group without a head goes along on the warp's first one)
+        const T* row = src + (live ? h : h0 - lane / LANES) * st1;
+        const Codes e = exact_codes<T, KV, D>(row, w, a.weight_f32, cs_row, rotary, a.interleaved, a.eps, unit);
+        if (!exact) cd = e;
+      }
+      if (live) {
+        if constexpr (KV == kFp8) *reinterpret_cast<uint2*>(dst) = make_uint2(cd.lo, cd.hi);
+        else *reinterpret_cast<uint32_t*>(dst) = cd.lo;
+        if (KV == kFp4 && (gl & 1) == 0)
+          *scale_addr(kind == 2 ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot, h, gl) =
+              (uint8_t)cd.scale;
       }
     }
   }
@@ -334,18 +377,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 
 template <typename T, int KV, int D, int R>
 cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
-  constexpr int LANES = D / 8;
+  constexpr int PER = R * 32 / (D / 8);  // heads of a warp
   AppendParams p;
   p.a = a;
-  p.heads = a.num_qo_heads + 2 * a.pool.num_kv_heads;
-  p.chunks = (uint32_t)(p.heads + R - 1) / R;
-  p.page_log = __builtin_ctz((unsigned)a.pool.page_size);
+  p.eps = (float)a.eps;
+  p.k_inv = 1.f / a.pool.k_scale;
+  p.v_inv = 1.f / a.pool.v_scale;
+  p.qc = (a.num_qo_heads + PER - 1) / PER;
+  p.kc = (a.pool.num_kv_heads + PER - 1) / PER;
+  p.chunks = (uint32_t)(p.qc + 2 * p.kc);
+  p.page_log = a.pool.page_size > 0 ? __builtin_ctz((unsigned)a.pool.page_size) : 0;
   const int64_t slab = (int64_t(1) << 30) / p.chunks;  // tokens a launch counts in 32 bits
   for (int64_t t0 = 0; t0 < a.num_tokens; t0 += slab) {
     const int64_t n = a.num_tokens - t0 < slab ? a.num_tokens - t0 : slab;
     p.token0 = t0;
     p.items = (uint32_t)(n * p.chunks);
-    const unsigned grid = (p.items + kThreads / LANES - 1) / (kThreads / LANES);
+    const unsigned grid = (p.items + kThreads / 32 - 1) / (kThreads / 32);
     cudaError_t e = launch_pdl(append_kernel<T, KV, D, R>, p, grid, kThreads, s);
     if (e != cudaSuccess) return e;
   }
@@ -354,10 +401,10 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
 
 template <typename T, int KV, int D>
 cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
-  // Heads a lane group takes: one while the call leaves SMs idle (a decode step is latency), four
+  // Heads a group takes: one while the call leaves SMs idle (a decode step is latency), several
   // once there is work for every SM several times over.
   const int64_t rows = a.num_tokens * (a.num_qo_heads + 2 * (int64_t)a.pool.num_kv_heads);
-  if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, 4>(a, s);
+  if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, KV == kSame16 ? 4 : 2>(a, s);
   return launch_r<T, KV, D, 1>(a, s);
 }
 

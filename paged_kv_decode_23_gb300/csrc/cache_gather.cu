@@ -1,8 +1,9 @@
 // cache_gather.cu -- listed token rows of a paged cache back as 16-bit rows (pkd_gather).
 //
-// A row of one head is spread over head_dim / 8 lanes, eight values each: 16, 8 or 4 bytes in,
-// 16 bytes out.  A group of lanes takes R rows of one token (its K and V heads), all loaded
-// before the first is used.  Nothing is computed but the widening and one multiply: bytes bound.
+// A row of one head is spread over head_dim / 16 lanes, sixteen values each (of a 4-bit cache one
+// block: eight code bytes and its scale): 32, 16 or 8 bytes in, 32 bytes out.  A group of lanes
+// takes up to R neighbouring heads of one token's K or V, all loaded before the first is used.
+// Nothing is computed but the widening and one multiply: bytes bound, see the launcher.
 #include <type_traits>
 
 #include "cache_rows.cuh"
@@ -15,16 +16,17 @@ using namespace rows;
 struct GatherParams {
   pkd_gather_args a;
   int64_t token0;
-  uint32_t items;
-  uint32_t chunks;
-  int heads;  // kv heads of K and of V together (of the one that is asked for)
+  uint32_t items;   // (token, chunk of heads) pairs of this launch
+  uint32_t chunks;  // chunks of a token: hc of each of K and V that is asked for
+  int hc;
   int page_log;
 };
 
 constexpr int kThreads = 256;
 
+// Eight values of raw (of an e2m1 block: its codes' values without the scale).
 template <typename T, int KV>
-__device__ __forceinline__ void widen8(const uint4& raw, uint32_t scale, float (&x)[8]) {
+__device__ __forceinline__ void widen8(const uint4& raw, float (&x)[8]) {
   if constexpr (KV == kSame16) {
     unpack8<T>(raw, x);
   } else if constexpr (KV == kFp8) {
@@ -40,15 +42,12 @@ __device__ __forceinline__ void widen8(const uint4& raw, uint32_t scale, float (
         : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
         : "r"(raw.x));
     unpack8<__half>(h, x);
-    const float s = e4m3_value(scale);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= s;  // at most 6 bits: exact
   }
 }
 
 template <typename T, int KV, int D, int R>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherParams p) {
-  constexpr int LANES = D / 8;
+  constexpr int LANES = D / 16;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const pkd_gather_args& a = p.a;
@@ -56,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
   if (item >= p.items) return;
   const uint32_t tok = item / p.chunks;
-  const int c0 = (int)(item - tok * p.chunks);
+  int c = (int)(item - tok * p.chunks);
   const int64_t t = p.token0 + tok;
   const int b = __ldg(a.batch_indices + t);
   if (b < 0) return;
@@ -65,54 +64,68 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     if (gl == 0 && a.status) atomicOr(a.status, slot.status);
     return;
   }
-  const int hkv = a.pool.num_kv_heads;
-  uint4 raw[R];
+  const bool is_v = a.k_out == nullptr || c >= p.hc;
+  if (c >= p.hc) c -= p.hc;
+  const int h0 = c * R, n = min(R, a.pool.num_kv_heads - h0);
+  // heads follow each other at fixed strides
+  const char* src = row_addr<KV>(is_v ? a.pool.v : a.pool.k, a.pool.strides, slot, h0, 2 * gl);
+  const int64_t step = a.pool.strides[2] * (KV == kSame16 ? 2 : 1);
+  uint4 raw[R][KV == kSame16 ? 2 : 1];
   uint32_t sf[R];
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    const int r = c0 + j * (int)p.chunks;
-    raw[j] = make_uint4(0, 0, 0, 0);
-    sf[j] = 0;
-    if (r < p.heads) {
-      const bool is_v = a.k_out == nullptr || r >= hkv;
-      const int head = r >= hkv ? r - hkv : r;
-      const char* src = row_addr<KV>(is_v ? a.pool.v : a.pool.k, a.pool.strides, slot, head, gl);
-      if constexpr (KV == kSame16) raw[j] = *reinterpret_cast<const uint4*>(src);
-      else if constexpr (KV == kFp8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(src);
-        raw[j].x = v.x;
-        raw[j].y = v.y;
+    if (j < n) {
+      if constexpr (KV == kSame16) {
+        raw[j][0] = reinterpret_cast<const uint4*>(src + j * step)[0];
+        raw[j][1] = reinterpret_cast<const uint4*>(src + j * step)[1];
+      } else if constexpr (KV == kFp8) {
+        raw[j][0] = *reinterpret_cast<const uint4*>(src + j * step);
       } else {
-        raw[j].x = *reinterpret_cast<const uint32_t*>(src);
-        sf[j] = *scale_addr(is_v ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot,
-                            head, gl);
+        const uint2 v = *reinterpret_cast<const uint2*>(src + j * step);
+        raw[j][0] = make_uint4(v.x, v.y, 0, 0);
       }
     }
   }
+  if constexpr (KV == kFp4) {
+    const uint8_t* at = scale_addr(is_v ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot, h0, 2 * gl);
+#pragma unroll
+    for (int j = 0; j < R; ++j) sf[j] = j < n ? at[j * a.pool.scale_strides[2]] : 0u;
+  }
+  const float unit = is_v ? a.pool.v_scale : a.pool.k_scale;
+  const int64_t o0 = is_v ? a.v_out_strides[0] : a.k_out_strides[0];
+  const int64_t o1 = is_v ? a.v_out_strides[1] : a.k_out_strides[1];
+  T* dst = static_cast<T*>(is_v ? a.v_out : a.k_out) + t * o0 + h0 * o1 + 16 * gl;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    const int r = c0 + j * (int)p.chunks;
-    if (r >= p.heads) continue;
-    const bool is_v = a.k_out == nullptr || r >= hkv;
-    const int head = r >= hkv ? r - hkv : r;
-    const float unit = is_v ? a.pool.v_scale : a.pool.k_scale;
-    float x[8];
-    widen8<T, KV>(raw[j], sf[j], x);
+    if (j >= n) break;
+    // (an e2m1 value times its scale has at most 6 bits: only the last product is rounded)
+    const float s = KV == kFp4 ? e4m3_value(sf[j]) : 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= unit;
-    T* dst = is_v ? static_cast<T*>(a.v_out) + t * a.v_out_strides[0] + head * a.v_out_strides[1]
-                  : static_cast<T*>(a.k_out) + t * a.k_out_strides[0] + head * a.k_out_strides[1];
-    *(reinterpret_cast<uint4*>(dst) + gl) = pack8<T>(x);
+    for (int i = 0; i < 2; ++i) {
+      float x[8];
+      if constexpr (KV == kSame16) widen8<T, KV>(raw[j][i], x);
+      else if constexpr (KV == kFp8) widen8<T, KV>(i ? make_uint4(raw[j][0].z, raw[j][0].w, 0, 0) : raw[j][0], x);
+      else widen8<T, KV>(i ? make_uint4(raw[j][0].y, 0, 0, 0) : raw[j][0], x);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        float2 v = make_float2(x[e], x[e + 1]);
+        if constexpr (KV == kFp4) v = __fmul2_rn(v, make_float2(s, s));
+        v = __fmul2_rn(v, make_float2(unit, unit));
+        x[e] = v.x;
+        x[e + 1] = v.y;
+      }
+      reinterpret_cast<uint4*>(dst + j * o1)[i] = pack8<T>(x);
+    }
   }
 }
 
 template <typename T, int KV, int D, int R>
 cudaError_t launch_r(const pkd_gather_args& a, cudaStream_t s) {
-  constexpr int LANES = D / 8;
+  constexpr int LANES = D / 16;
   GatherParams p;
   p.a = a;
-  p.heads = a.pool.num_kv_heads * ((a.k_out != nullptr) + (a.v_out != nullptr));
-  p.chunks = (uint32_t)(p.heads + R - 1) / R;
+  p.hc = (a.pool.num_kv_heads + R - 1) / R;
+  p.chunks = (uint32_t)(p.hc * ((a.k_out != nullptr) + (a.v_out != nullptr)));
   p.page_log = __builtin_ctz((unsigned)a.pool.page_size);
   const int64_t slab = (int64_t(1) << 30) / p.chunks;  // tokens a launch counts in 32 bits
   for (int64_t t0 = 0; t0 < a.num_tokens; t0 += slab) {

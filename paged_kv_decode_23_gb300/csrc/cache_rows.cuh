@@ -70,7 +70,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-// Codes of two values >= 0 (or NaN), nearest with ties to even, at most the type's largest: of
+// Codes of two values, nearest with ties to even, at most the type's largest, with their signs: of
 // `lo` in the low half of the result, of `hi` above it (8 bits each in e4m3, 4 in e2m1).
 template <int KV>
 __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
@@ -87,14 +87,22 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
     return r;
   }
 }
+// ... and of eight, in order: eight bytes, or eight nibbles in w.x.
 template <int KV>
-__device__ __forceinline__ float code_value(uint32_t code) {
-  if constexpr (KV == kFp8) return e4m3_value(code);
-  // e2m1, from its definition: codes 0 and 1 are 0 and 0.5, else (1 + m / 2) 2^(e - 1)
-  const uint32_t e = code >> 1, m = code & 1;
-  return e == 0 ? 0.5f * m : __uint_as_float((e + 126u) << 23 | m << 22);
+__device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
+  if constexpr (KV == kFp8) {
+    return make_uint2(codes2<KV>(v[0], v[1]) | codes2<KV>(v[2], v[3]) << 16,
+                      codes2<KV>(v[4], v[5]) | codes2<KV>(v[6], v[7]) << 16);
+  } else {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return make_uint2(r, 0u);
+  }
 }
-
 // A double as a float whose last bit is set if anything was cut off (rounding to odd): a further
 // rounding to nearest, to a type of at most 22 bits, then gives what the double itself rounds to.
 __device__ __forceinline__ float to_odd(double x) {
@@ -104,28 +112,29 @@ __device__ __forceinline__ float to_odd(double x) {
              : f;
 }
 
-// The code nearest to a / (m * unit), m a value of few bits and a >= 0, known only through the
-// approximation t of that quotient with |t - quotient| <= e.
-//   exact:  a is exact; the doubt is settled by the sign of a - mid * m * unit, mid being the
-//           border between the two codes (one rounding in an FMA keeps a sign), ties to even.
-//   else:   *doubt is set when the codes of t - e and t + e differ.
-template <int KV>
-__device__ __forceinline__ uint32_t nearest_code(float a, float t, float e, float m, float unit,
-                                                 bool exact, bool* doubt) {
-  constexpr int kBits = KV == kFp8 ? 8 : 4;
-  t = t > 1e30f ? 1e30f : t;  // (keeps a NaN)
-  e = fminf(e, 1e30f);
-  const float low = t - e;
-  const uint32_t c = codes2<KV>(low < 0.f ? 0.f : low, t + e);
-  const uint32_t lo = c & ((1u << kBits) - 1), hi = (c >> kBits) & ((1u << kBits) - 1);
-  if (lo == hi) return lo;
-  if (!exact) {
-    *doubt = true;
-    return lo;
-  }
-  const float mid = 0.5f * (code_value<KV>(lo) + code_value<KV>(hi));
-  const float r = fmaf(-(mid * m), unit, a);
-  return r > 0.f || (r == 0.f && (hi & 1) == 0) ? hi : lo;
+// 1 / x within one unit in the last place, for normal x.
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// a / (d + dl) rounded to odd, so that one more rounding to a type of few bits is that of the exact
+// quotient: a finite, d + dl the exact divisor as a float and the rest it leaves, inv about 1 / d.
+// One Newton step makes t faithful; the remainder then keeps its sign through its two FMAs.
+__device__ __forceinline__ float odd_quotient(float a, float d, float dl, float inv) {
+  const float x = fabsf(a);
+  float t = x * inv;
+  float r = fmaf(-t, dl, fmaf(-t, d, x));
+  t = fmaf(r, inv, t);
+  r = fmaf(-t, dl, fmaf(-t, d, x));
+  uint32_t bits = __float_as_uint(t);
+  if (r < 0.f) --bits;  // truncated ...
+  if (r != 0.f) bits |= 1u;  // ... with what was cut off kept in the last bit
+  // (beyond the range of any code nothing is left to decide; a NaN or an infinity stays one)
+  if (!(x * inv < 1e30f)) bits = __float_as_uint(x * inv);
+  if (x == 0.f) bits = 0u;
+  return __uint_as_float(bits | (__float_as_uint(a) & 0x80000000u));
 }
 
 }  // namespace rows

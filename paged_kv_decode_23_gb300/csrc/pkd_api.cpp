@@ -139,6 +139,7 @@ struct pkd_handle {
   // of every later step) skips the encoding: a map depends only on these fields
   struct TmapEntry {
     const void* base;
+    int64_t kv_stride;  // 4-bit pools: K to V in one map, 0: one of them alone; other pools: 0
     int64_t num_pages;
     int64_t strides[3];
     int kv_dtype, head_dim, page_size, num_kv_heads, layout, box_rows;
@@ -219,19 +220,14 @@ int staging_release(pkd_handle* h, int slot, cudaStream_t s) {
 
 // 4-D TMA view of one K or V pool: dims (d, head, slot, page) for NHD and (d, slot, head, page)
 // for HND, i.e. ordered by increasing stride; a box is 128 bytes of d by `box_rows` slots of
-// one head of one page, landing 128-byte swizzled in shared memory.  An E2M1 pool is a pool of
-// head_dim / 2 code bytes a row, with boxes of 64 bytes of them (all 32 at head_dim 64) and the
-// swizzle of that width.
+// one head of one page, landing 128-byte swizzled in shared memory.
 int make_kv_tensor_map(CUtensorMap* map, const void* base, int kv_dtype, int head_dim, int page_size,
                        int num_kv_heads, int64_t num_pages, const int64_t strides[3], int layout,
                        int box_rows) {
   std::string why;
   EncodeTiledFn enc = get_encode_fn(&why);
   if (!enc) return fail(PKD_ERR_CUDA, why);
-  const bool fp4 = kv_dtype == kE2M1;
-  const int elt = kv_dtype == kE4M3 || fp4 ? 1 : 2;
-  const int row_elts = fp4 ? head_dim / 2 : head_dim;  // elements of a row
-  const int box_bytes = !fp4 ? 128 : row_elts < 64 ? 32 : 64;
+  const int elt = kv_dtype == kE4M3 ? 1 : 2;
   const CUtensorMapDataType dt = kv_dtype == kF16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : kv_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -253,16 +249,13 @@ int make_kv_tensor_map(CUtensorMap* map, const void* base, int kv_dtype, int hea
     box[1] = (cuuint32_t)box_rows;
     box[2] = 1;
   }
-  dims[0] = (cuuint64_t)row_elts;
+  dims[0] = (cuuint64_t)head_dim;
   dims[3] = (cuuint64_t)num_pages;
   gstr[2] = (cuuint64_t)page_b;
-  box[0] = (cuuint32_t)(box_bytes / elt);
+  box[0] = (cuuint32_t)(128 / elt);
   box[3] = 1;
-  const CUtensorMapSwizzle swizzle = box_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                       : CU_TENSOR_MAP_SWIZZLE_32B;
   CUresult r = enc(map, dt, 4, const_cast<void*>(base), dims, gstr, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     char buf[256];
@@ -270,6 +263,44 @@ int make_kv_tensor_map(CUtensorMap* map, const void* base, int kv_dtype, int hea
                   "cuTensorMapEncodeTiled failed (%d) for strides page=%lld slot=%lld head=%lld "
                   "bytes",
                   (int)r, (long long)page_b, (long long)slot_b, (long long)head_b);
+    return fail(PKD_ERR_INVALID_ARG, buf);
+  }
+  return PKD_OK;
+}
+
+// 5-D TMA view of a 4-bit pool's codes: (d, head, slot, K/V, page) for NHD and (d, slot, head, K/V,
+// page) for HND, strides in bytes; a box is the whole row (head_dim / 2 bytes, swizzled at that
+// width) by `box_rows` slots of one head, of both K and V (kv_rows 2, V kv_stride bytes behind K)
+// or of the one that starts at base (kv_rows 1).
+int make_code_tensor_map(CUtensorMap* map, const void* base, int64_t kv_stride, int kv_rows,
+                         int head_dim, int page_size, int num_kv_heads, int64_t num_pages,
+                         const int64_t strides[3], int layout, int box_rows) {
+  std::string why;
+  EncodeTiledFn enc = get_encode_fn(&why);
+  if (!enc) return fail(PKD_ERR_CUDA, why);
+  const int at_slot = layout == PKD_LAYOUT_NHD ? 2 : 1, at_head = 3 - at_slot;
+  cuuint64_t dims[5] = {(cuuint64_t)head_dim / 2, 0, 0, (cuuint64_t)kv_rows, (cuuint64_t)num_pages};
+  cuuint64_t gstr[4] = {0, 0, (cuuint64_t)kv_stride, (cuuint64_t)strides[0]};
+  cuuint32_t box[5] = {(cuuint32_t)head_dim / 2, 1, 1, (cuuint32_t)kv_rows, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  dims[at_slot] = (cuuint64_t)page_size;
+  dims[at_head] = (cuuint64_t)num_kv_heads;
+  gstr[at_slot - 1] = (cuuint64_t)strides[1];
+  gstr[at_head - 1] = (cuuint64_t)strides[2];
+  box[at_slot] = (cuuint32_t)box_rows;
+  const CUtensorMapSwizzle swizzle = head_dim == 256   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                       : CU_TENSOR_MAP_SWIZZLE_32B;
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, gstr, box,
+                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[256];
+    std::snprintf(buf, sizeof buf,
+                  "cuTensorMapEncodeTiled failed (%d) for strides page=%lld slot=%lld head=%lld kv=%lld "
+                  "bytes",
+                  (int)r, (long long)strides[0], (long long)strides[1], (long long)strides[2],
+                  (long long)kv_stride);
     return fail(PKD_ERR_INVALID_ARG, buf);
   }
   return PKD_OK;
@@ -331,7 +362,7 @@ int decode_ctas_per_sm(const DecodeKernel* k, int device, int* out) {
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k->fn, k->threads,
                                                                 (size_t)k->smem_bytes);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-  n = std::max(1, std::min(n, kDecodeCtasPerSm));
+  n = std::max(1, std::min(n, k->max_ctas));
   cache.push_back({{k->fn, device}, n});
   *out = n;
   return PKD_OK;
@@ -450,7 +481,7 @@ int pkd_plan_host(const int32_t* indptr_host, const int32_t* last_page_len_host,
   r.max_items = work_capacity > 0 ? work_capacity : 0;
   ScheduleStore st;
   DecodeSchedule sch;
-  rc = plan_decode(r, (num_sms > 0 ? num_sms : 152) * kDecodeCtasPerSm, st, &sch);
+  rc = plan_decode(r, (num_sms > 0 ? num_sms : 152) * decode_max_ctas(r), st, &sch);
   if (rc) return rc;
   if (n_tasks) *n_tasks = (int)sch.n_tasks;
   if (n_merges) *n_merges = (int)sch.n_merges;
@@ -483,7 +514,7 @@ int pkd_workspace_bytes(const int32_t* indptr_host, const int32_t* last_page_len
   if (rc) return rc;
   ScheduleStore st;
   DecodeSchedule sch;
-  const int ctas = (num_sms > 0 ? num_sms : 152) * kDecodeCtasPerSm;
+  const int ctas = (num_sms > 0 ? num_sms : 152) * decode_max_ctas(r);
   rc = plan_decode(r, ctas, st, &sch);
   if (rc) return rc;
   DecodeWsLayout lay{(size_t)sch.n_tasks, (size_t)sch.n_merges, (size_t)sch.n_slots};
@@ -686,19 +717,23 @@ namespace {
 
 // make_kv_tensor_map through the handle's cache of maps.
 int cached_kv_tensor_map(pkd_handle* h, CUtensorMap* map, const void* base, int64_t num_pages,
-                         const int64_t strides[3], int box_rows) {
+                         const int64_t strides[3], int box_rows, int64_t kv_stride = 0) {
   for (const auto& t : h->tmaps)
-    if (t.base == base && t.num_pages == num_pages && t.strides[0] == strides[0] &&
+    if (t.base == base && t.kv_stride == kv_stride && t.num_pages == num_pages && t.strides[0] == strides[0] &&
         t.strides[1] == strides[1] && t.strides[2] == strides[2] && t.kv_dtype == h->kv_dtype &&
         t.head_dim == h->head_dim && t.page_size == h->page_size &&
         t.num_kv_heads == h->num_kv_heads && t.layout == h->layout && t.box_rows == box_rows) {
       *map = t.map;
       return PKD_OK;
     }
-  int rc = make_kv_tensor_map(map, base, h->kv_dtype, h->head_dim, h->page_size,
-                              h->num_kv_heads, num_pages, strides, h->layout, box_rows);
+  int rc = h->kv_dtype == kE2M1
+               ? make_code_tensor_map(map, base, kv_stride ? kv_stride : strides[0],
+                                      kv_stride ? 2 : 1, h->head_dim, h->page_size,
+                                      h->num_kv_heads, num_pages, strides, h->layout, box_rows)
+               : make_kv_tensor_map(map, base, h->kv_dtype, h->head_dim, h->page_size,
+                                    h->num_kv_heads, num_pages, strides, h->layout, box_rows);
   if (rc) return rc;
-  pkd_handle::TmapEntry e{base, num_pages, {strides[0], strides[1], strides[2]}, h->kv_dtype,
+  pkd_handle::TmapEntry e{base, kv_stride, num_pages, {strides[0], strides[1], strides[2]}, h->kv_dtype,
                           h->head_dim, h->page_size, h->num_kv_heads, h->layout, box_rows, *map};
   if (h->tmaps.size() < pkd_handle::kTmapCacheSize) {
     h->tmaps.push_back(e);
@@ -777,10 +812,18 @@ int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_b
   }
   const int tile = h->kernel->tile_tokens;
   const int box_rows = h->page_size < tile ? h->page_size : tile;
-  int rc = cached_kv_tensor_map(h, &prm.tmap_k, k_base, num_pages, kv_strides, box_rows);
+  // A 4-bit pool with V behind K at a distance that a tensor map can hold takes one map, whose
+  // boxes bring a page's K and V together; else (a (k, v) pair the other way round) one map each.
+  const int64_t kv_stride = static_cast<const char*>(v_base) - static_cast<const char*>(k_base);
+  const bool one_map = sf && kv_stride > 0 && kv_stride % 16 == 0 && kv_stride < (int64_t(1) << 40);
+  prm_all.kv_maps = one_map ? 1 : 2;
+  int rc = cached_kv_tensor_map(h, &prm.tmap_k, k_base, num_pages, kv_strides, box_rows,
+                                one_map ? kv_stride : 0);
   if (rc) return rc;
-  rc = cached_kv_tensor_map(h, &prm.tmap_v, v_base, num_pages, kv_strides, box_rows);
-  if (rc) return rc;
+  if (!one_map) {
+    rc = cached_kv_tensor_map(h, &prm.tmap_v, v_base, num_pages, kv_strides, box_rows);
+    if (rc) return rc;
+  }
 
   char* iws = static_cast<char*>(h->int_ws);
   char* fws = static_cast<char*>(h->float_ws);

@@ -107,14 +107,18 @@ struct DecodeParams {
   float v_scale;
 };
 
-// The parameters of a kernel over a 4-bit cache: K and V maps over the code pools, and the e4m3
-// scale of (page, slot, head, block) at base + page*sf_stride[0] + slot*sf_stride[1] +
-// head*sf_stride[2] + block.
+// The parameters of a kernel over a 4-bit cache: 5-D maps over the code pools (d, head and slot in
+// the layout's order, K/V, page) and the e4m3 scale of (page, slot, head, block) at base +
+// page*sf_stride[0] + slot*sf_stride[1] + head*sf_stride[2] + block.
 struct DecodeE2m1Params : DecodeParams {
+  int kv_maps;  // 1: tmap_k's K/V axis holds both (a box: K rows, then V rows); 2: one map each
   const uint8_t* k_sf;
   const uint8_t* v_sf;
   int64_t sf_stride[3];
 };
+
+// CTAs per SM the decode kernels over 16- and 8-bit caches are sized for.
+constexpr int kDecodeCtasPerSm = 2;
 
 // A compiled decode kernel and how to launch it.
 struct DecodeKernel {
@@ -129,6 +133,7 @@ struct DecodeKernel {
   int tile_tokens;  // tokens per pipeline stage
   int rope;         // 1: rotates q and K (ROPE_LLAMA) before the QK product
   int nstages;      // pipeline stages
+  int max_ctas = kDecodeCtasPerSm;  // CTAs per SM it is sized for
 };
 
 // Registries filled by the kernel translation units.
@@ -258,8 +263,9 @@ int decode_geometry(const PlanRequest& r, DecodeSchedule* s, const char** err);
 // Cuts every row's attended tokens into tasks per (kv head, slice), one per CTA, longest first.
 int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, const char** err);
 
-// CTAs per SM the decode kernels are sized for.
-constexpr int kDecodeCtasPerSm = 2;
+// CTAs per SM the decode kernel of a request is sized for (DecodeKernel::max_ctas): two, but for
+// some kernels over a 4-bit cache.
+int decode_max_ctas(const PlanRequest& r);
 
 // Decode workspaces.  int: [status block (CUDA-graph mode: the task count at
 // kItemCountOffset) | one merge counter per merge entry | tasks | merge entries |

@@ -429,16 +429,24 @@ int decode_geometry(const PlanRequest& r, DecodeSchedule* s, const char** err) {
   // it streams faster than the CUDA-core kernel for groups of 1, 2, 4 and 8 alike
   s->kind = r.use_tensor_cores == 0 ? kCudaCore : kTensorCore;
   if (s->kind == kTensorCore) {
-    s->heads_per_cta = 8;
+    s->heads_per_cta = r.kv_dtype == kE2M1 && G <= 4 ? 4 : 8;
   } else {
     int gp = 1;
     while (gp < G && gp < 8) gp <<= 1;
     s->heads_per_cta = gp;
   }
   s->gslices = (G + s->heads_per_cta - 1) / s->heads_per_cta;
-  s->tile_tokens = 16384 / (r.head_dim * (r.kv_dtype == kE4M3 || r.kv_dtype == kE2M1 ? 1 : 2));
-  if (s->tile_tokens > 128) s->tile_tokens = 128;  // at most 8 consumer warps of 16 tokens
+  s->tile_tokens = 16384 / (r.head_dim * (r.kv_dtype == kE4M3 ? 1 : 2));
+  if (r.kv_dtype == kE2M1) s->tile_tokens = 128;
   return 0;
+}
+
+int decode_max_ctas(const PlanRequest& r) {
+  // the kernels over a 4-bit cache have 4 consumer warps and fit more often, the more so with the
+  // accumulators of 4 heads alone
+  if (r.kv_dtype != kE2M1 || r.num_kv_heads <= 0) return kDecodeCtasPerSm;
+  if (r.head_dim == 256) return 2;
+  return r.head_dim == 64 || r.num_qo_heads / r.num_kv_heads <= 4 ? 4 : 3;
 }
 
 namespace {
