@@ -1,14 +1,14 @@
 // cache_append.cu -- token rows into a paged cache, with the norm of each query and key head and
 // the position rotation in the same pass (pkd_append).
 //
-// A row of one head is spread over a group of head_dim / 8 lanes, eight values (16 bytes) each: the
-// sum of squares is a shuffle tree over the group, the rotation partner of the half-split form is
-// the value of another lane (one shuffle), that of the interleaved form is in the lane itself, and
-// a block of the 4-bit cache is two lanes.  A warp takes one token's neighbouring heads, all q, all
-// k or all v, up to R for each of its groups, and loads them before it uses the first; weights,
-// cosines and sines are read once for them, and all that depends on the token is the same in every
-// lane, so that every shuffle is the whole warp's (one over a part of it costs four instructions
-// more).  Pairs of values go through the packed 32-bit FMA.
+// A row of one head is spread over a group of head_dim / 16 lanes, two pieces of eight values (16
+// bytes) each: where pairs (i, i + rotary_dim / 2) turn, a lane holds both pieces of its pairs, else
+// 16 values on end, so that no rotation needs another lane's values.  The sum of squares is a
+// shuffle tree over the group; a block of the 4-bit cache is two pieces, wherever they are.  A warp
+// takes one token's neighbouring heads, all q, all k or all v, up to R for each of its groups, and
+// loads them before it uses the first; weights, cosines and sines are read once for them, and all
+// that depends on the token is the same in every lane, so that every shuffle is the whole warp's.
+// Pairs of values go through the packed 32-bit FMA.
 //
 // Codes.  A cache of 8 or 4 bits stores the code nearest to the exact quotient, so that neither
 // the order of a sum nor the lanes' roundings can show in it.  A value that comes straight from
@@ -47,337 +47,534 @@ constexpr float kValueErr = 9.5367431640625e-07f;  // 2^-20
 // ... and of a quotient against the value it is computed from (three roundings, doubled).
 constexpr float kQuotErr = 4.76837158203125e-07f;  // 2^-21
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kCtas = 4;  // per SM
 
-__device__ __forceinline__ void load_weight8(const void* w, int f32, int gl, bool bf16, float (&out)[8]) {
+// The dims of a lane's two pieces, and where a piece's other half of its 16-value block is.
+struct Place {
+  int d[2];        // first dim of each piece
+  bool turned;     // the lane's values are rotated
+  bool split;      // ... as pairs (d[0] + i, d[1] + i)
+  int lane[2];     // lane (of the warp) and piece that hold dims d[i] ^ 8 ..
+  int piece[2];
+};
+template <int D>
+__device__ __forceinline__ Place place_of(int lane, int rotary, int interleaved) {
+  constexpr int LANES = D / 16;
+  const int gl = lane & (LANES - 1), half = rotary / 2;
+  Place p;
+  p.turned = 16 * gl < rotary;
+  p.split = p.turned && !interleaved;
+  p.d[0] = p.split ? 8 * gl : 16 * gl;
+  p.d[1] = p.split ? half + 8 * gl : 16 * gl + 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int o = p.d[i] ^ 8;
+    const bool pair = !interleaved && o < rotary;
+    p.lane[i] = (lane - gl) + (pair ? (o < half ? o : o - half) / 8 : o / 16);
+    p.piece[i] = pair ? o >= half : (o >> 3) & 1;
+  }
+  return p;
+}
+
+// Eight weights as floats.
+template <typename T>
+__device__ __forceinline__ void load_weight8(const void* w, int f32, int d, float (&out)[8]) {
   if (f32) {
-    const float4* f = static_cast<const float4*>(w) + 2 * gl;
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + d);
     const float4 a = __ldg(f), b = __ldg(f + 1);
     out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
     out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
   } else {
-    const uint4 v = __ldg(static_cast<const uint4*>(w) + gl);
-    if (bf16) unpack8<__nv_bfloat16>(v, out);
-    else unpack8<__half>(v, out);
+    unpack8<T>(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + d)), out);
   }
 }
 
 struct Codes {
-  uint32_t lo, hi;   // e4m3: eight bytes; e2m1: eight nibbles in lo
-  uint32_t scale;    // e2m1: the block's scale byte
+  uint2 c[2];         // of each piece: e4m3: eight bytes; e2m1: eight nibbles in x
+  uint2 alt[2];       // quick_codes: where it differs from c the code is in doubt
+  uint32_t scale[2];  // e2m1: the scale byte of the piece's block
 };
+
+// 1 / sqrt(mean(x^2) + eps) of a row in 64 bits; x: this lane's 16 values.  The squares of 16-bit
+// values are exact in 32 bits and are summed with their rounding errors kept (Knuth's two-sum), so
+// that the 64-bit pipe, 16 cycles an instruction, has only the root to do: one Newton step from
+// the 32-bit root, good to 2^-42.  Whole warps.
+template <typename T, int D>
+__device__ __forceinline__ double exact_rnorm(const uint4 (&raw)[2], double eps) {
+  constexpr int LANES = D / 16;
+  float s = 0.f, low = 0.f;
+  auto add = [&](float x) {
+    const float t = s + x, b = t - s;
+    low += (s - (t - b)) + (x - b);
+    s = t;
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float x[8];
+    unpack8<T>(raw[i], x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) add(x[e] * x[e]);
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    const float os = __shfl_xor_sync(~0u, s, o), ol = __shfl_xor_sync(~0u, low, o);
+    add(os);
+    low += ol;
+  }
+  const double m = ((double)s + low) * (1.0 / D) + eps;
+  const double r = rsqrtf((float)m);
+  return r * (1.5 - 0.5 * m * r * r);
+}
+
+// One value (dim d) of a computed key row in 64 bits, over its divisor, rounded to odd.
+template <typename T>
+__device__ __noinline__ float exact_quotient(const T* src, const void* weight, int weight_f32, const float* cs,
+                                             int rotary, int interleaved, double rn, int d, float m, float unit) {
+  auto value = [&](int at) {
+    double x = (double)(float)src[at];
+    if (weight)
+      x = x * rn * (double)(weight_f32 ? static_cast<const float*>(weight)[at] : (float)static_cast<const T*>(weight)[at]);
+    return x;
+  };
+  double x = value(d);
+  if (d < rotary) {
+    const int half = rotary / 2, pair = interleaved ? d >> 1 : d < half ? d : d - half;
+    const bool first = interleaved ? !(d & 1) : d < half;
+    const double o = value(interleaved ? d ^ 1 : first ? d + half : d - half);
+    const double c = cs[pair], s = cs[half + pair];
+    x = first ? x * c - o * s : x * c + o * s;
+  }
+  return to_odd(x / ((double)m * unit));
+}
 
 // The codes of a computed key row, in 64 bits throughout.  Called by whole warps.
 template <typename T, int KV, int D>
 __device__ __noinline__ Codes exact_codes(const T* src, const void* weight, int weight_f32,
-                                          const float* cs, int rotary,
-                                          int interleaved, double eps, float unit) {
-  constexpr int LANES = D / 8;
-  const int lane = threadIdx.x & 31, gl = lane & (LANES - 1);
-  float xf[8];
-  unpack8<T>(*(reinterpret_cast<const uint4*>(src) + gl), xf);
-  double x[8];
+                                          const float* cs, int rotary, int interleaved, double eps,
+                                          float unit) {
+  constexpr int LANES = D / 16;
+  const Place pl = place_of<D>(threadIdx.x & 31, rotary, interleaved);
+  double x[2][8];
   double ss = 0.0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = xf[i];
-    ss += x[i] * x[i];
+  for (int i = 0; i < 2; ++i) {
+    float xf[8];
+    unpack8<T>(*reinterpret_cast<const uint4*>(src + pl.d[i]), xf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[i][e] = xf[e];
+      ss += x[i][e] * x[i][e];
+    }
   }
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
   if (weight != nullptr) {
-    float w[8];
-    load_weight8(weight, weight_f32, gl, std::is_same<T, __nv_bfloat16>::value, w);
     const double r = 1.0 / sqrt(ss / D + eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+    for (int i = 0; i < 2; ++i) {
+      float w[8];
+      load_weight8<T>(weight, weight_f32, pl.d[i], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * r * w[e];
+    }
   }
-  if (rotary) {
+  if (pl.turned) {
     const int half = rotary / 2;
-    const bool turned = 8 * gl < rotary;
-    if (interleaved) {
-      if (turned) {
+    if (pl.split) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const double c = cs[4 * gl + i], s = cs[half + 4 * gl + i];
-          const double u = x[2 * i], v = x[2 * i + 1];
-          x[2 * i] = u * c - v * s;
-          x[2 * i + 1] = v * c + u * s;
-        }
+      for (int e = 0; e < 8; ++e) {
+        const double c = cs[pl.d[0] + e], s = cs[half + pl.d[0] + e];
+        const double u = x[0][e], v = x[1][e];
+        x[0][e] = u * c - v * s;
+        x[1][e] = v * c + u * s;
       }
     } else {
-      const bool first = 8 * gl < half;
-      const int from = (lane - gl) + ((first ? gl + half / 8 : gl - half / 8) & (LANES - 1));
-      const int i0 = first ? 8 * gl : 8 * gl - half;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double other = __shfl_sync(~0u, x[i], from);
-        if (turned) {
-          const double c = cs[i0 + i], s = cs[half + i0 + i];
-          x[i] = first ? x[i] * c - other * s : x[i] * c + other * s;
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const double c = cs[pl.d[i] / 2 + e], s = cs[half + pl.d[i] / 2 + e];
+          const double u = x[i][2 * e], v = x[i][2 * e + 1];
+          x[i][2 * e] = u * c - v * s;
+          x[i][2 * e + 1] = v * c + u * s;
         }
-      }
     }
   }
-  Codes out{0, 0, 0};
-  double by = unit;
+  Codes out;
+  double by[2] = {unit, unit};
   if constexpr (KV == kFp4) {
-    double top = 0.0;
-    bool nan = false;
+    double top[2] = {0.0, 0.0};
+    bool nan[2] = {false, false};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      top = fmax(top, fabs(x[i]));
-      nan |= x[i] != x[i];
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        top[i] = fmax(top[i], fabs(x[i][e]));
+        nan[i] |= x[i][e] != x[i][e];
+      }
+    double both[2];
+    bool any[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const double t0 = __shfl_sync(~0u, top[0], pl.lane[i]), t1 = __shfl_sync(~0u, top[1], pl.lane[i]);
+      const int n0 = __shfl_sync(~0u, (int)nan[0], pl.lane[i]), n1 = __shfl_sync(~0u, (int)nan[1], pl.lane[i]);
+      both[i] = fmax(top[i], pl.piece[i] ? t1 : t0);
+      any[i] = nan[i] || (pl.piece[i] ? n1 : n0);
     }
-    top = fmax(top, __shfl_xor_sync(~0u, top, 1));
-    nan |= __shfl_xor_sync(~0u, (int)nan, 1) != 0;
-    const float t = to_odd(top / (6.0 * unit));
-    out.scale = nan ? 0x7fu : codes2<kFp8>(t, t) & 0xffu;
-    by = (double)e4m3_value(out.scale) * unit;
-    if (!(by > 0.0)) return out;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float t = to_odd(both[i] / (6.0 * unit));
+      out.scale[i] = any[i] ? 0x7fu : codes2<kFp8>(t, t) & 0xffu;
+      by[i] = (double)e4m3_value(out.scale[i]) * unit;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = to_odd(fabs(x[i]) / by);
-    const uint32_t sign = x[i] < 0.0 ? 1u : 0u;
-    if constexpr (KV == kFp8) {
-      const uint32_t c = (codes2<kFp8>(t, t) & 0xffu) | sign << 7;
-      if (i < 4) out.lo |= c << (8 * i);
-      else out.hi |= c << (8 * (i - 4));
-    } else {
-      out.lo |= ((codes2<kFp4>(t, t) & 0xfu) | sign << 3) << (4 * i);
-    }
+  for (int i = 0; i < 2; ++i) {
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = by[i] > 0.0 ? to_odd(x[i][e] / by[i]) : 0.f;  // a block of zeros: codes 0
+    out.c[i] = codes8<KV>(t);
   }
   return out;
 }
 
 // The codes of a row from its values y in 32 bits, each with the sum `err` of the terms it was
 // computed from (unused where `exact`); inv about 1 / unit.  Whole warps, whose lanes may differ in
-// `exact`; *doubt: some code needs exact_codes.
+// `exact`; *doubt: some code is in doubt (alt differs from c), *scale_doubt: a block's scale is.
 template <int KV>
-__device__ __forceinline__ Codes quick_codes(const float (&y)[8], const float (&err)[8],
-                                             bool exact, float unit, float inv, bool* doubt) {
-  Codes out{0, 0, 0};
-  float d = unit, dl = 0.f;  // the divisor and what its rounding left
+__device__ __forceinline__ Codes quick_codes(const Place& pl, const float (&y)[2][8],
+                                             const float (&err)[2][8], bool exact, bool all_exact,
+                                             float unit, float inv, bool* doubt, bool* scale_doubt) {
+  Codes out;
+  float d[2] = {unit, unit}, dl[2] = {0.f, 0.f}, inv2[2] = {inv, inv};  // divisors, what their rounding left
   if constexpr (KV == kFp4) {
-    float top = 0.f, off = 0.f;
-    bool nan = false;
+    // largest magnitude of each block, by its bits: a NaN's are above all others
+    uint32_t top[2] = {0, 0}, both[2];
+    float off[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      top = fmaxf(top, fabsf(y[i]));
-      nan |= y[i] != y[i];
-      if (!exact) off = fmaxf(off, err[i]);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top[i] = max(top[i], __float_as_uint(y[i][e]) & 0x7fffffffu);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t t0 = __shfl_sync(~0u, top[0], pl.lane[i]), t1 = __shfl_sync(~0u, top[1], pl.lane[i]);
+      both[i] = max(top[i], pl.piece[i] ? t1 : t0);
     }
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    off = fmaxf(off, __shfl_xor_sync(~0u, off, 1));  // (lanes differ in exact)
-    nan |= __shfl_xor_sync(~0u, (int)nan, 1) != 0;
-    const float sixth = inv * 0.16666667f;
-    if (exact) {
-      const float six = 6.f * unit, t = odd_quotient(top, six, fmaf(6.f, unit, -six), sixth);
-      out.scale = codes2<kFp8>(t, t) & 0xffu;
-    } else {
-      const float t = top * sixth, e = off * sixth * (kValueErr + kQuotErr);
-      const uint32_t c = codes2<kFp8>(t - e, t + e);
-      out.scale = c & 0xffu;
-      *doubt = out.scale != c >> 8;
+    if (!all_exact) {  // (the same in the whole warp)
+      float mine[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine[i] = fmaxf(mine[i], exact ? 0.f : err[i][e]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float t0 = __shfl_sync(~0u, mine[0], pl.lane[i]), t1 = __shfl_sync(~0u, mine[1], pl.lane[i]);
+        off[i] = fmaxf(mine[i], pl.piece[i] ? t1 : t0);
+      }
     }
-    if (nan) out.scale = 0x7fu;
-    const float m = e4m3_value(out.scale);
-    if (!(m > 0.f)) return out;  // a block of zeros (or a NaN's): all codes 0
-    d = m * unit;
-    dl = fmaf(m, unit, -d);
-    inv = rcp(d);
+    const float six = 6.f * unit, six_l = fmaf(6.f, unit, -six), sixth = inv * 0.16666667f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = __uint_as_float(both[i]);
+      if (exact) {
+        const float t = odd_quotient(a, six, six_l, sixth);
+        out.scale[i] = codes2<kFp8>(t, t) & 0xffu;
+      } else {
+        const float t = a * sixth, e = off[i] * sixth * (kValueErr + kQuotErr);
+        const uint32_t c = codes2<kFp8>(t - e, t + e);
+        out.scale[i] = c & 0xffu;
+        *scale_doubt |= out.scale[i] != c >> 8;
+      }
+      if (both[i] > 0x7f800000u) out.scale[i] = 0x7fu;
+      const float m = e4m3_value(out.scale[i]);
+      // (a block of zeros, or a NaN's, gets codes 0 by a zero in place of 1 / 0)
+      d[i] = m * unit;
+      dl[i] = fmaf(m, unit, -d[i]);
+      inv2[i] = m > 0.f ? rcp(d[i]) : 0.f;
+    }
   }
-  if (exact) {
-    float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = odd_quotient(y[i], d, dl, inv);
-    const uint2 c = codes8<KV>(t);
-    out.lo = c.x;
-    out.hi = c.y;
-  } else {
-    float lo[8], hi[8];
+  for (int i = 0; i < 2; ++i) {
+    if (exact) {
+      float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // (+ 0: a negative zero, from a zero head and a negative weight, is no doubt)
-      const float t = fmaf(y[i], inv, 0.f), e = err[i] * inv * (kValueErr + kQuotErr);
-      lo[i] = t - e;
-      hi[i] = t + e;
+      for (int e = 0; e < 8; ++e) t[e] = odd_quotient(y[i][e], d[i], dl[i], inv2[i]);
+      out.c[i] = out.alt[i] = codes8<KV>(t);
+    } else {
+      float lo[8], hi[8];
+      const float k = inv2[i] * (kValueErr + kQuotErr);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // (+ 0: a negative zero, from a zero head and a negative weight, is no doubt)
+        const float t = fmaf(y[i][e], inv2[i], 0.f), off = err[i][e] * k;
+        lo[e] = t - off;
+        hi[e] = t + off;
+      }
+      out.c[i] = codes8<KV>(lo);
+      out.alt[i] = codes8<KV>(hi);
     }
-    const uint2 a = codes8<KV>(lo), b = codes8<KV>(hi);
-    out.lo = a.x;
-    out.hi = a.y;
-    *doubt |= a.x != b.x || a.y != b.y;
+    if (KV == kFp4 && inv2[i] == 0.f) out.c[i] = out.alt[i] = make_uint2(0, 0);
+    *doubt |= out.c[i].x != out.alt[i].x || out.c[i].y != out.alt[i].y;
   }
   return out;
 }
 
-template <typename T, int KV, int D, int R>
-__global__ void __launch_bounds__(kThreads, KV == kSame16 ? 3 : 2) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int LANES = D / 8;
-  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const pkd_append_args& a = p.a;
-  constexpr int GROUPS = 32 / LANES;
-  const int lane = threadIdx.x & 31, gl = lane & (LANES - 1);
-  const uint32_t item = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  if (item >= p.items) return;  // whole warps from here on, until their last row is stored
-  const uint32_t tok = item / p.chunks;
-  int c = (int)(item - tok * p.chunks);
-  const int64_t t = p.token0 + tok;
+// What a warp works on, and what it has loaded of it.
+template <typename T, int D, int R>
+struct Item {
+  int64_t t;       // token
+  int kind;        // 0, 1, 2: q, k, v
+  int first;       // first head; group g takes first + g, first + g + GROUPS, ...
+  int b, pos, rpos;
+  uint4 raw[R][2];
 
-  // this warp's heads [h0, heads) of q, k or v: its group g takes h0 + g, h0 + g + GROUPS, ...
-  const int kind = c < p.qc ? 0 : c < p.qc + p.kc ? 1 : 2;
-  c -= kind == 0 ? 0 : kind == 1 ? p.qc : p.qc + p.kc;
-  const int heads = kind == 0 ? a.num_qo_heads : a.pool.num_kv_heads;
-  const int h0 = c * R * GROUPS + lane / LANES;
-  const int64_t st0 = kind == 0 ? a.q_strides[0] : kind == 1 ? a.k_strides[0] : a.v_strides[0];
-  const int64_t st1 = kind == 0 ? a.q_strides[1] : kind == 1 ? a.k_strides[1] : a.v_strides[1];
-  const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + t * st0;
-  const int b = __ldg(a.batch_indices + t);
-  const int pos = __ldg(a.positions + t);
-  const int rotary = a.rotary_dim;
-  const int rpos = rotary && a.rope_positions ? __ldg(a.rope_positions + t) : pos;
-  uint4 raw[R];
-#pragma unroll
-  for (int j = 0; j < R; ++j) {  // (a padding row's values are read and dropped; no head: zeros)
-    const int h = h0 + j * GROUPS;
-    raw[j] = h < heads ? *(reinterpret_cast<const uint4*>(src + h * st1) + gl) : make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ int heads(const pkd_append_args& a) const {
+    return kind == 0 ? a.num_qo_heads : a.pool.num_kv_heads;
   }
-  if (b < 0) return;
-  if (rotary && (rpos < 0 || rpos >= a.cos_sin_rows)) {
+  __device__ __forceinline__ Place place(const pkd_append_args& a, int lane) const {
+    return place_of<D>(lane, kind == 2 ? 0 : a.rotary_dim, a.interleaved);
+  }
+  __device__ __forceinline__ int64_t step(const pkd_append_args& a) const {
+    return kind == 0 ? a.q_strides[1] : kind == 1 ? a.k_strides[1] : a.v_strides[1];
+  }
+  __device__ __forceinline__ const T* row0(const pkd_append_args& a) const {
+    const int64_t st = kind == 0 ? a.q_strides[0] : kind == 1 ? a.k_strides[0] : a.v_strides[0];
+    return static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + t * st;
+  }
+  __device__ __forceinline__ void load(const AppendParams& p, uint32_t item, int lane) {
+    constexpr int GROUPS = 32 / (D / 16);
+    const pkd_append_args& a = p.a;
+    const uint32_t tok = item / p.chunks;
+    const int c = (int)(item - tok * p.chunks);
+    t = p.token0 + tok;
+    kind = c < p.qc ? 0 : c < p.qc + p.kc ? 1 : 2;
+    first = (c - (kind == 0 ? 0 : kind == 1 ? p.qc : p.qc + p.kc)) * R * GROUPS;
+    b = __ldg(a.batch_indices + t);
+    pos = __ldg(a.positions + t);
+    rpos = a.rotary_dim && a.rope_positions ? __ldg(a.rope_positions + t) : pos;
+    const Place pl = place(a, lane);
+    const int n = heads(a);
+    const T* src = row0(a);
+    const int64_t st = step(a);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {  // (a padding row's values are read and dropped; no head: zeros)
+      const int h = first + lane / (D / 16) + j * GROUPS;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        raw[j][i] = h < n ? *reinterpret_cast<const uint4*>(src + h * st + pl.d[i]) : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+
+template <typename T, int KV, int D, int R>
+__device__ __forceinline__ void append_item(const AppendParams& p, const Item<T, D, R>& it, int lane) {
+  constexpr int LANES = D / 16, GROUPS = 32 / LANES;
+  const pkd_append_args& a = p.a;
+  const int kind = it.kind, first = it.first, heads = it.heads(a), rotary = a.rotary_dim, rpos = it.rpos;
+  const int64_t t = it.t;
+  const int h0 = first + lane / LANES;
+  const Place pl = it.place(a, lane);
+  const uint4 (&raw)[R][2] = it.raw;
+  const void* w = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+  float wv[2][8];
+  if (w) {
+    load_weight8<T>(w, a.weight_f32, pl.d[0], wv[0]);
+    load_weight8<T>(w, a.weight_f32, pl.d[1], wv[1]);
+  }
+  // cosines and sines: of the lane's eight pairs (piece 0 with piece 1), or of the four of each piece
+  const bool turnable = !rotary || (rpos >= 0 && rpos < a.cos_sin_rows);
+  const float* cs_row = rotary && turnable ? a.cos_sin + (int64_t)rpos * rotary : nullptr;
+  float cs[8], sn[8];
+  if (pl.turned && turnable) {
+    const int half = rotary / 2;
+    const int at0 = pl.split ? pl.d[0] : pl.d[0] / 2, at1 = pl.split ? pl.d[0] + 4 : pl.d[1] / 2;
+    const float4 u0 = __ldg(reinterpret_cast<const float4*>(cs_row + at0));
+    const float4 u1 = __ldg(reinterpret_cast<const float4*>(cs_row + at1));
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs_row + half + at0));
+    const float4 s1 = __ldg(reinterpret_cast<const float4*>(cs_row + half + at1));
+    cs[0] = u0.x; cs[1] = u0.y; cs[2] = u0.z; cs[3] = u0.w;
+    cs[4] = u1.x; cs[5] = u1.y; cs[6] = u1.z; cs[7] = u1.w;
+    sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
+    sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+  }
+  // (what hangs on the batch index comes after the loads that do not)
+  if (it.b < 0) return;
+  if (!turnable) {
     if (lane == 0 && a.status) atomicOr(a.status, PKD_STATUS_BAD_TOKEN);
     return;
   }
   Slot slot{0, 0, 0};
   if (kind != 0) {
-    slot = find_slot(a.pool, p.page_log, b, pos);
+    slot = find_slot(a.pool, p.page_log, it.b, it.pos);
     if (slot.status) {
       if (lane == 0 && a.status) atomicOr(a.status, slot.status);
       return;
     }
   }
-  const bool turned = kind != 2 && 8 * gl < rotary;
-  const void* w = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
   const float unit = kind == 2 ? a.pool.v_scale : a.pool.k_scale, inv = kind == 2 ? p.v_inv : p.k_inv;
-  const int half = rotary / 2;
-  const bool first = 8 * gl < half;
-  const float* cs_row = rotary ? a.cos_sin + (int64_t)rpos * rotary : nullptr;
-  // cosines, and sines with the sign that this lane's values take their partners with
-  float cs[8], sn[8], wv[8];
-  if (turned) {
-    if (a.interleaved) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(cs_row + 4 * gl));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(cs_row + half + 4 * gl));
-      cs[0] = cs[1] = u.x; cs[2] = cs[3] = u.y; cs[4] = cs[5] = u.z; cs[6] = cs[7] = u.w;
-      sn[1] = s.x; sn[3] = s.y; sn[5] = s.z; sn[7] = s.w;
-      sn[0] = -s.x; sn[2] = -s.y; sn[4] = -s.z; sn[6] = -s.w;
-    } else {
-      const int i0 = first ? 8 * gl : 8 * gl - half;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(cs_row + i0) + i);
-        const float4 s = __ldg(reinterpret_cast<const float4*>(cs_row + half + i0) + i);
-        cs[4 * i] = u.x; cs[4 * i + 1] = u.y; cs[4 * i + 2] = u.z; cs[4 * i + 3] = u.w;
-        sn[4 * i] = s.x; sn[4 * i + 1] = s.y; sn[4 * i + 2] = s.z; sn[4 * i + 3] = s.w;
-      }
-      if (first)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  }
-  if (w) load_weight8(w, a.weight_f32, gl, kBf16, wv);
-  const int from = (lane - gl) + ((first ? gl + half / 8 : gl - half / 8) & (LANES - 1));
 
 #pragma unroll
   for (int j = 0; j < R; ++j) {
+    if (first + j * GROUPS >= heads) break;  // the warp's last heads are done
     const int h = h0 + j * GROUPS;
-    if (h0 - lane / LANES + j * GROUPS >= heads) break;  // the warp's last heads are done
     const bool live = h < heads;
-    float y[8], err[8];  // err: |terms| that a value is the sum of
-    unpack8<T>(raw[j], y);
+    float y[2][8], err[2][8];  // err: |terms| that a value is the sum of
+    unpack8<T>(raw[j][0], y[0]);
+    unpack8<T>(raw[j][1], y[1]);
     // ---- norm
     if (w) {
-      float2 ss = make_float2(0.f, 0.f);
+      float2 ss[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) ss = __ffma2_rn(make_float2(y[i], y[i + 1]), make_float2(y[i], y[i + 1]), ss);
-      float sum = ss.x + ss.y;
+      for (int e = 0; e < 8; e += 2)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 v = make_float2(y[i][e], y[i][e + 1]);
+          ss[i] = __ffma2_rn(v, v, ss[i]);
+        }
+      float sum = (ss[0].x + ss[0].y) + (ss[1].x + ss[1].y);
 #pragma unroll
       for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
       const float rn = rsqrtf(fmaf(sum, 1.f / D, p.eps));
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 v = __fmul2_rn(__fmul2_rn(make_float2(y[i], y[i + 1]), make_float2(rn, rn)), make_float2(wv[i], wv[i + 1]));
-        y[i] = v.x;
-        y[i + 1] = v.y;
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 v = __fmul2_rn(__fmul2_rn(make_float2(y[i][e], y[i][e + 1]), make_float2(rn, rn)),
+                                      make_float2(wv[i][e], wv[i][e + 1]));
+          y[i][e] = v.x;
+          y[i][e + 1] = v.y;
+        }
     }
     // ---- rotation
     if (KV != kSame16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) err[i] = fabsf(y[i]);
-    }
-    if (rotary && kind != 2) {
-      float other[8];
-      if (a.interleaved) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) other[i] = y[i ^ 1];
+        for (int e = 0; e < 8; ++e) err[i][e] = fabsf(y[i][e]);
+    }
+    if (pl.turned) {
+      if (pl.split) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 u = make_float2(y[0][e], y[0][e + 1]), v = make_float2(y[1][e], y[1][e + 1]);
+          const float2 cc = make_float2(cs[e], cs[e + 1]), s = make_float2(sn[e], sn[e + 1]);
+          const float2 vs = __fmul2_rn(v, make_float2(-s.x, -s.y)), us = __fmul2_rn(u, s);
+          const float2 nu = __ffma2_rn(u, cc, vs), nv = __ffma2_rn(v, cc, us);
+          if (KV != kSame16) {
+            err[0][e] = fabsf(u.x * cc.x) + fabsf(vs.x);
+            err[0][e + 1] = fabsf(u.y * cc.y) + fabsf(vs.y);
+            err[1][e] = fabsf(v.x * cc.x) + fabsf(us.x);
+            err[1][e + 1] = fabsf(v.y * cc.y) + fabsf(us.y);
+          }
+          y[0][e] = nu.x;
+          y[0][e + 1] = nu.y;
+          y[1][e] = nv.x;
+          y[1][e + 1] = nv.y;
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(~0u, y[i], from);
-      }
-      if (turned) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 os = __fmul2_rn(make_float2(other[i], other[i + 1]), make_float2(sn[i], sn[i + 1]));
-          const float2 cc = make_float2(cs[i], cs[i + 1]);
-          const float2 v = __ffma2_rn(make_float2(y[i], y[i + 1]), cc, os);
-          if (KV != kSame16) {
-            err[i] = fabsf(y[i] * cc.x) + fabsf(os.x);
-            err[i + 1] = fabsf(y[i + 1] * cc.y) + fabsf(os.y);
+          for (int e = 0; e < 4; ++e) {
+            const float u = y[i][2 * e], v = y[i][2 * e + 1], cc = cs[4 * i + e], s = sn[4 * i + e];
+            const float vs = v * -s, us = u * s;
+            if (KV != kSame16) {
+              err[i][2 * e] = fabsf(u * cc) + fabsf(vs);
+              err[i][2 * e + 1] = fabsf(v * cc) + fabsf(us);
+            }
+            y[i][2 * e] = fmaf(u, cc, vs);
+            y[i][2 * e + 1] = fmaf(v, cc, us);
           }
-          y[i] = v.x;
-          y[i + 1] = v.y;
-        }
       }
     }
     // ---- out
     if (kind == 0) {
       T* dst = static_cast<T*>(a.q_out) + t * a.q_out_strides[0] + h * a.q_out_strides[1];
-      if (live) *(reinterpret_cast<uint4*>(dst) + gl) = pack8<T>(y);
+      if (live) {
+        *reinterpret_cast<uint4*>(dst + pl.d[0]) = pack8<T>(y[0]);
+        *reinterpret_cast<uint4*>(dst + pl.d[1]) = pack8<T>(y[1]);
+      }
       continue;
     }
-    char* dst = row_addr<KV>(kind == 2 ? a.pool.v : a.pool.k, a.pool.strides, slot, h, gl);
+    char* dst = row_addr<KV>(kind == 2 ? a.pool.v : a.pool.k, a.pool.strides, slot, h, 0);
     if constexpr (KV == kSame16) {
-      if (live) *reinterpret_cast<uint4*>(dst) = kind == 2 ? raw[j] : pack8<T>(y);
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<uint4*>(dst + 2 * pl.d[i]) = kind == 2 ? raw[j][i] : pack8<T>(y[i]);
+      }
     } else {
-      const bool exact = kind == 2 || (!w && !turned);
-      bool doubt = false;
-      Codes cd = quick_codes<KV>(y, err, exact, unit, inv, &doubt);
-      if (__any_sync(~0u, doubt && live)) {
+      const bool exact = kind == 2 || (!w && !pl.turned);
+      bool doubt = false, scale_doubt = false;
+      Codes cd = quick_codes<KV>(pl, y, err, exact, kind == 2, unit, inv, &doubt, &scale_doubt);
+      if (KV == kFp4 && __any_sync(~0u, scale_doubt && live)) {
         // (a group without a head goes along on the warp's first one)
-        const T* row = src + (live ? h : h0 - lane / LANES) * st1;
-        const Codes e = exact_codes<T, KV, D>(row, w, a.weight_f32, cs_row, rotary, a.interleaved, a.eps, unit);
+        const Codes e = exact_codes<T, KV, D>(it.row0(a) + (live ? h : first) * it.step(a), w, a.weight_f32, cs_row,
+                                              rotary, a.interleaved, a.eps, unit);
         if (!exact) cd = e;
+      } else if (__any_sync(~0u, doubt && live)) {
+        const double rn = w ? exact_rnorm<T, D>(raw[j], a.eps) : 1.0;
+        if (live) {
+          constexpr int kBits = KV == kFp8 ? 8 : 4;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float m = KV == kFp4 ? e4m3_value(cd.scale[i]) : 1.f;
+            uint64_t code = cd.c[i].x | (uint64_t)cd.c[i].y << 32;
+            uint64_t diff = code ^ (cd.alt[i].x | (uint64_t)cd.alt[i].y << 32);
+            while (diff) {  // (one value, as a rule)
+              const int e = (__ffsll(diff) - 1) / kBits;
+              const uint64_t field = ((uint64_t(1) << kBits) - 1) << (e * kBits);
+              const float x = exact_quotient<T>(it.row0(a) + h * it.step(a), w, a.weight_f32, cs_row, rotary,
+                                                a.interleaved, rn, pl.d[i] + e, m, unit);
+              code = (code & ~field) | ((uint64_t)codes2<KV>(x, x) << (e * kBits) & field);
+              diff &= ~field;
+            }
+            cd.c[i] = make_uint2((uint32_t)code, (uint32_t)(code >> 32));
+          }
+        }
       }
       if (live) {
-        if constexpr (KV == kFp8) *reinterpret_cast<uint2*>(dst) = make_uint2(cd.lo, cd.hi);
-        else *reinterpret_cast<uint32_t*>(dst) = cd.lo;
-        if (KV == kFp4 && (gl & 1) == 0)
-          *scale_addr(kind == 2 ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot, h, gl) =
-              (uint8_t)cd.scale;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (KV == kFp8) {
+            *reinterpret_cast<uint2*>(dst + pl.d[i]) = cd.c[i];
+          } else {
+            *reinterpret_cast<uint32_t*>(dst + pl.d[i] / 2) = cd.c[i].x;
+            if ((pl.d[i] & 8) == 0)
+              scale_addr(kind == 2 ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot, h, 0)[pl.d[i] / 16] =
+                  (uint8_t)cd.scale[i];
+          }
+        }
       }
     }
   }
 }
 
 template <typename T, int KV, int D, int R>
+__global__ void __launch_bounds__(kThreads, kCtas) append_kernel(const __grid_constant__ AppendParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // whole warps, the next item's rows under way while the current one is worked on
+  const int lane = threadIdx.x & 31;
+  const uint32_t stride = gridDim.x * (kThreads / 32);
+  uint32_t item = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (item >= p.items) return;
+  Item<T, D, R> it, next;
+  it.load(p, item, lane);
+  while (true) {
+    const bool more = item + stride < p.items && item + stride > item;
+    if (more) next.load(p, item + stride, lane);
+    append_item<T, KV, D, R>(p, it, lane);
+    if (!more) break;
+    item += stride;
+    it = next;
+  }
+}
+
+template <typename T, int KV, int D, int R>
 cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
-  constexpr int PER = R * 32 / (D / 8);  // heads of a warp
+  constexpr int PER = R * 32 / (D / 16);  // heads of a warp
   AppendParams p;
   p.a = a;
   p.eps = (float)a.eps;
@@ -392,7 +589,10 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
     const int64_t n = a.num_tokens - t0 < slab ? a.num_tokens - t0 : slab;
     p.token0 = t0;
     p.items = (uint32_t)(n * p.chunks);
-    const unsigned grid = (p.items + kThreads / 32 - 1) / (kThreads / 32);
+    // as many CTAs as fit at once, and no more than there is work for
+    const unsigned need = (p.items + kThreads / 32 - 1) / (kThreads / 32);
+    const unsigned room = 152u * kCtas;
+    const unsigned grid = need < room ? need : room;
     cudaError_t e = launch_pdl(append_kernel<T, KV, D, R>, p, grid, kThreads, s);
     if (e != cudaSuccess) return e;
   }
@@ -404,7 +604,7 @@ cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
   // Heads a group takes: one while the call leaves SMs idle (a decode step is latency), several
   // once there is work for every SM several times over.
   const int64_t rows = a.num_tokens * (a.num_qo_heads + 2 * (int64_t)a.pool.num_kv_heads);
-  if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, KV == kSame16 ? 4 : 2>(a, s);
+  if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, KV == kSame16 ? 2 : 1>(a, s);
   return launch_r<T, KV, D, 1>(a, s);
 }
 

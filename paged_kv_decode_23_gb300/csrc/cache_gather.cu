@@ -20,9 +20,10 @@ struct GatherParams {
   uint32_t chunks;  // chunks of a token: hc of each of K and V that is asked for
   int hc;
   int page_log;
+  int wide;         // the outputs' rows are 32-byte aligned: one store a lane
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 
 // Eight values of raw (of an e2m1 block: its codes' values without the scale).
 template <typename T, int KV>
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     if (j >= n) break;
     // (an e2m1 value times its scale has at most 6 bits: only the last product is rounded)
     const float s = KV == kFp4 ? e4m3_value(sf[j]) : 1.f;
+    uint4 v16[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x[8];
@@ -114,7 +116,17 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
         x[e] = v.x;
         x[e + 1] = v.y;
       }
-      reinterpret_cast<uint4*>(dst + j * o1)[i] = pack8<T>(x);
+      v16[i] = pack8<T>(x);
+    }
+    if (p.wide) {
+      // whole sectors: two stores of 16 bytes would each write half of every sector
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + j * o1),
+                   "r"(v16[0].x), "r"(v16[0].y), "r"(v16[0].z), "r"(v16[0].w), "r"(v16[1].x),
+                   "r"(v16[1].y), "r"(v16[1].z), "r"(v16[1].w)
+                   : "memory");
+    } else {
+      reinterpret_cast<uint4*>(dst + j * o1)[0] = v16[0];
+      reinterpret_cast<uint4*>(dst + j * o1)[1] = v16[1];
     }
   }
 }
@@ -124,6 +136,10 @@ cudaError_t launch_r(const pkd_gather_args& a, cudaStream_t s) {
   constexpr int LANES = D / 16;
   GatherParams p;
   p.a = a;
+  uint64_t bits = 0;  // of every address a row can start at, in bytes
+  if (a.k_out) bits |= (uint64_t)a.k_out | (uint64_t)(2 * a.k_out_strides[0]) | (uint64_t)(2 * a.k_out_strides[1]);
+  if (a.v_out) bits |= (uint64_t)a.v_out | (uint64_t)(2 * a.v_out_strides[0]) | (uint64_t)(2 * a.v_out_strides[1]);
+  p.wide = (bits & 31) == 0;
   p.hc = (a.pool.num_kv_heads + R - 1) / R;
   p.chunks = (uint32_t)(p.hc * ((a.k_out != nullptr) + (a.v_out != nullptr)));
   p.page_log = __builtin_ctz((unsigned)a.pool.page_size);
