@@ -10,13 +10,15 @@ from __future__ import annotations
 
 import ctypes
 import struct
+from array import array
 from typing import Optional
 
 import numpy as np
 import torch
 
 from . import _lib as L
-from .decode import _DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, _host_i32, pool_views
+from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, _host_i32, new_output, pool_views,
+                     raw_stream)
 
 _POOL = "4Pq3q3q2Pq5i2fi"  # pkd_paged_pool
 _APPEND = struct.Struct("@" + _POOL + "4P8q3P2PPqPqd6i")  # pkd_append_args
@@ -24,96 +26,87 @@ _GATHER = struct.Struct("@" + _POOL + "2P4q2PPq2i")  # pkd_gather_args
 _IO_DTYPES = (torch.float16, torch.bfloat16)
 
 
-def _index(t, name: str, device, n: Optional[int] = None) -> int:
-    """Address of a contiguous int32 tensor on `device` (of n entries)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+_INT32 = torch.int32
+
+
+def _index(t, name: str, dev: int, n: Optional[int] = None) -> int:
+    """Address of a contiguous int32 tensor on CUDA device `dev` (of n entries)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the rows are on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the rows are on cuda:{dev}")
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} has {t.shape[0]} entries, expected {n}")
     return t.data_ptr()
 
 
-def _status(status, device) -> int:
+def _status(status, dev: int) -> int:
     if status is None:
         return 0
-    if status.numel() != 1 or status.element_size() != 4 or status.device != device:
-        raise ValueError(f"status must be one 32-bit integer on {device}")
+    if status.numel() != 1 or status.element_size() != 4 or status.get_device() != dev:
+        raise ValueError(f"status must be one 32-bit integer on cuda:{dev}")
     return status.data_ptr()
 
 
-def _rows(t, name: str, dtype, device, shape):
+def _rows(t, name: str, dtype, dev: int, shape):
     """(address, token stride, head stride) of rows [tokens, heads, head_dim]."""
-    if t.dim() != 3 or tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}")
-    st = t.stride()
-    if st[2] != 1:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on cuda:{dev}")
+    st0, st1, st2 = t.stride()
+    if st2 != 1:
         raise ValueError(f"{name} must have its last axis contiguous")
     # the stride of an axis of one entry is never used; any value will do
-    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+    return t.data_ptr(), st0 if shape[0] > 1 else 0, st1 if shape[1] > 1 else 0
 
 
-def _pool_fields(cache, scales, indptr, indices, kv_layout, k_scale, v_scale, device, io_dtype):
-    """pkd_paged_pool's fields, and (num_kv_heads, head_dim)."""
-    if kv_layout not in ("NHD", "HND"):
+def _pool_fields(cache, scales, indptr, indices, kv_layout, k_scale, v_scale, dev, io_dtype):
+    """pkd_paged_pool's fields, num_kv_heads and head_dim."""
+    if kv_layout != "NHD" and kv_layout != "HND":
         raise ValueError("kv_layout must be 'NHD' or 'HND'")
     first = cache[0] if isinstance(cache, (tuple, list)) else cache
-    if first.device != device:
-        raise ValueError(f"paged_kv_cache is on {first.device}, the rows are on {device}")
-    k, v, strides, ps, hkv = pool_views(cache, kv_layout)
-    pages, d = first.shape[0], first.shape[-1]
-    ks = vs = 0
-    sf_strides = (0, 0, 0)
+    if first.get_device() != dev:
+        raise ValueError(f"paged_kv_cache is on {first.device}, the rows are on cuda:{dev}")
+    k, v, (s0, s1, s2), ps, hkv = pool_views(cache, kv_layout)
+    shape, kv_dtype = first.shape, first.dtype
+    pages, d = shape[0], shape[-1]
+    ks = vs = f0 = f1 = f2 = 0
     if scales is not None:
-        if first.dtype not in CODE_DTYPES:
+        if kv_dtype not in CODE_DTYPES:
             raise ValueError("kv_block_scales belongs to a 4-bit cache (uint8 or float4_e2m1fn_x2 codes)")
         d *= 2
         sf = scales[0] if isinstance(scales, (tuple, list)) else scales
-        ks, vs, sf_strides, sps, shkv = pool_views(scales, kv_layout, "kv_block_scales")
-        if (sf.dtype not in SCALE_DTYPES or sf.device != device
+        ks, vs, (f0, f1, f2), sps, shkv = pool_views(scales, kv_layout, "kv_block_scales")
+        if (sf.dtype not in SCALE_DTYPES or sf.get_device() != dev
                 or (sf.shape[0], sps, shkv, 16 * sf.shape[-1]) != (pages, ps, hkv, d)):
             raise ValueError("kv_block_scales must be float8_e4m3fn (or uint8) of the cache's shape "
                              "with a last axis of head_dim / 16, on its device")
         code = L.DTYPE_E2M1
-    elif first.dtype == io_dtype or first.dtype == torch.float8_e4m3fn:
-        code = _DTYPE_CODE[first.dtype]
+    elif kv_dtype is io_dtype or kv_dtype is torch.float8_e4m3fn:
+        code = _DTYPE_CODE[kv_dtype]
     else:
-        raise ValueError(f"a cache of {first.dtype} does not go with rows of {io_dtype} (a 4-bit "
+        raise ValueError(f"a cache of {kv_dtype} does not go with rows of {io_dtype} (a 4-bit "
                          "cache needs kv_block_scales)")
-    n = indptr.shape[0]
-    return (k, v, ks, vs, pages, *strides, *sf_strides, _index(indptr, "kv_indptr", device),
-            _index(indices, "kv_indices", device), indices.shape[0], max(0, n - 1), code, hkv, d, ps,
-            1.0 if k_scale is None else float(k_scale), 1.0 if v_scale is None else float(v_scale),
-            0), hkv, d
+    ip, ix = _index(indptr, "kv_indptr", dev), _index(indices, "kv_indices", dev)
+    return (k, v, ks, vs, pages, s0, s1, s2, f0, f1, f2, ip, ix, indices.shape[0],
+            max(0, indptr.shape[0] - 1), code, hkv, d, ps, 1.0 if k_scale is None else float(k_scale),
+            1.0 if v_scale is None else float(v_scale), 0), hkv, d
 
 
-class _On:
-    """The stream a call launches on, with its device current meanwhile."""
-
-    def __init__(self, device, stream):
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors are on {device}")
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-
-def _new(shape, dtype, device, stream):
-    """An output, allocated on the stream that will write it."""
+def _launch(call, dev: int, stream, *args) -> None:
+    """call(*args, stream) with the tensors' device current and an error raised."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        s = raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
+    else:
+        s = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = call(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, s)
+    if rc:
+        L.check(rc)
 
 
 def append_paged_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -154,61 +147,66 @@ def append_paged_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opt
         raise ValueError("append needs q, or k and v, or all three")
     if not isinstance(first, torch.Tensor) or first.dim() != 3 or first.dtype not in _IO_DTYPES:
         raise ValueError("q, k and v must be fp16 or bf16 tensors [tokens, heads, head_dim]")
-    if not first.is_cuda:
+    dev, dtype = first.get_device(), first.dtype
+    if dev < 0:
         raise ValueError("q, k and v must be CUDA tensors")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (q, k, v, q_weight, k_weight)):
+    if torch.is_grad_enabled() and (first.requires_grad or (k is not None and (k.requires_grad or v.requires_grad))
+                                    or (q_weight is not None and q_weight.requires_grad)
+                                    or (k_weight is not None and k_weight.requires_grad)):
         raise NotImplementedError("append has no backward pass (detach its inputs)")
-    device, dtype = first.device, first.dtype
     n, hq, d = first.shape
-    if q is None:
-        hq = 0
     if k is not None:
         pool, hkv, pd = _pool_fields(paged_kv_cache, kv_block_scales, kv_indptr, kv_indices, kv_layout,
-                                     k_scale, v_scale, device, dtype)
+                                     k_scale, v_scale, dev, dtype)
         if pd != d:
             raise ValueError(f"the cache's head_dim is {pd}, the rows' is {d}")
-        kr, vr = (_rows(t, name, dtype, device, (n, hkv, d)) for t, name in ((k, "k"), (v, "v")))
+        kp, k0, k1 = _rows(k, "k", dtype, dev, (n, hkv, d))
+        vp, v0, v1 = _rows(v, "v", dtype, dev, (n, hkv, d))
     else:
-        pool, kr, vr = (0,) * 14 + (0, 0, 0, d, 0, 1.0, 1.0, 0), (0, 0, 0), (0, 0, 0)
-    qr = outr = (0, 0, 0)
+        pool = (0,) * 14 + (0, 0, 0, d, 0, 1.0, 1.0, 0)
+        kp = k0 = k1 = vp = v0 = v1 = 0
     if q is not None:
-        qr = _rows(q, "q", dtype, device, (n, hq, d))
+        qp, q0, q1 = _rows(q, "q", dtype, dev, (n, hq, d))
         if out is None:
-            out = _new((n, hq, d), dtype, device, stream)
-        outr = _rows(out, "out", dtype, device, (n, hq, d))
+            out = new_output((n, hq, d), q, dtype, stream)
+        op, o0, o1 = _rows(out, "out", dtype, dev, (n, hq, d))
     elif out is not None:
         raise ValueError("out without q")
-    weight_f32 = 0
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is None:
-            continue
-        if tuple(w.shape) != (d,) or w.dtype not in (dtype, torch.float32) or w.device != device \
-                or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [{d}] tensor of {dtype} or float32 on {device}")
-        weight_f32 = int(w.dtype == torch.float32)
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must have one dtype")
+    else:
+        hq = qp = q0 = q1 = op = o0 = o1 = 0
+    weight_f32 = qw = kw = 0
+    if q_weight is not None:
+        qw, weight_f32 = _weight(q_weight, "q_weight", dtype, dev, d)
+    if k_weight is not None:
+        kw, f32 = _weight(k_weight, "k_weight", dtype, dev, d)
+        if q_weight is not None and f32 != weight_f32:
+            raise ValueError("q_weight and k_weight must have one dtype")
+        weight_f32 = f32
     rotary = rows = cs = rp = 0
     if cos_sin_cache is not None:
         c = cos_sin_cache
-        if c.dim() != 2 or c.dtype != torch.float32 or not c.is_contiguous() or c.device != device:
-            raise ValueError(f"cos_sin_cache must be a contiguous float32 [positions, rotary_dim] tensor on {device}")
+        if c.dim() != 2 or c.dtype is not torch.float32 or not c.is_contiguous() or c.get_device() != dev:
+            raise ValueError(f"cos_sin_cache must be a contiguous float32 [positions, rotary_dim] tensor on cuda:{dev}")
         rows, rotary = c.shape
         cs = c.data_ptr()
         if rope_positions is not None:
-            rp = _index(rope_positions, "rope_positions", device, n)
+            rp = _index(rope_positions, "rope_positions", dev, n)
     elif rope_positions is not None:
         raise ValueError("rope_positions without cos_sin_cache")
     args = _APPEND.pack(
-        *pool, qr[0], kr[0], vr[0], outr[0], *qr[1:], *kr[1:], *vr[1:], *outr[1:],
-        _index(batch_indices, "batch_indices", device, n), _index(positions, "positions", device, n),
-        rp, 0 if q_weight is None else q_weight.data_ptr(),
-        0 if k_weight is None else k_weight.data_ptr(), cs, rows, _status(status, device), n,
-        float(eps), hq, _DTYPE_CODE[dtype], weight_f32, rotary, int(bool(interleaved)), 0)
-    with _On(device, stream) as s:
-        L.check(L.lib().pkd_append(args, s))
+        *pool, qp, kp, vp, op, q0, q1, k0, k1, v0, v1, o0, o1,
+        _index(batch_indices, "batch_indices", dev, n), _index(positions, "positions", dev, n),
+        rp, qw, kw, cs, rows, _status(status, dev), n,
+        eps, hq, _DTYPE_CODE[dtype], weight_f32, rotary, 1 if interleaved else 0, 0)
+    _launch(L.lib().pkd_append, dev, stream, args)
     return out
+
+
+def _weight(w, name: str, dtype, dev: int, d: int):
+    """(address, whether it is float32) of a norm's weights."""
+    if w.shape != (d,) or w.dtype not in (dtype, torch.float32) or w.get_device() != dev or w.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous [{d}] tensor of {dtype} or float32 on cuda:{dev}")
+    return w.data_ptr(), int(w.dtype is torch.float32)
 
 
 def gather_paged_kv(batch_indices: torch.Tensor, positions: torch.Tensor, paged_kv_cache,
@@ -225,9 +223,9 @@ def gather_paged_kv(batch_indices: torch.Tensor, positions: torch.Tensor, paged_
     in ``out = (k, v)``, and undefined in fresh tensors.  The cache arguments are those of
     ``append_paged_kv``.  For prefill over a cached prefix, and for moving a cache elsewhere."""
     first = paged_kv_cache[0] if isinstance(paged_kv_cache, (tuple, list)) else paged_kv_cache
-    if not first.is_cuda:
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("the cache must be a CUDA tensor")
-    device = first.device
     if out is not None:
         k, v = out
         if out_dtype is not None and out_dtype != k.dtype:
@@ -238,18 +236,29 @@ def gather_paged_kv(batch_indices: torch.Tensor, positions: torch.Tensor, paged_
     if out_dtype not in _IO_DTYPES:
         raise ValueError("out_dtype must be fp16 or bf16")
     pool, hkv, d = _pool_fields(paged_kv_cache, kv_block_scales, kv_indptr, kv_indices, kv_layout,
-                                k_scale, v_scale, device, out_dtype)
+                                k_scale, v_scale, dev, out_dtype)
     n = batch_indices.shape[0]
     if out is None:
-        k, v = (_new((n, hkv, d), out_dtype, device, stream) for _ in range(2))
-    kr, vr = (_rows(t, name, out_dtype, device, (n, hkv, d)) for t, name in ((k, "k out"), (v, "v out")))
-    args = _GATHER.pack(*pool, kr[0], vr[0], *kr[1:], *vr[1:],
-                        _index(batch_indices, "batch_indices", device),
-                        _index(positions, "positions", device, n), _status(status, device), n,
+        k, v = new_output((n, hkv, d), first, out_dtype, stream), new_output((n, hkv, d), first, out_dtype, stream)
+    kp, k0, k1 = _rows(k, "k out", out_dtype, dev, (n, hkv, d))
+    vp, v0, v1 = _rows(v, "v out", out_dtype, dev, (n, hkv, d))
+    args = _GATHER.pack(*pool, kp, vp, k0, k1, v0, v1, _index(batch_indices, "batch_indices", dev),
+                        _index(positions, "positions", dev, n), _status(status, dev), n,
                         _DTYPE_CODE[out_dtype], 0)
-    with _On(device, stream) as s:
-        L.check(L.lib().pkd_gather(args, s))
+    _launch(L.lib().pkd_gather, dev, stream, args)
     return k, v
+
+
+def _host_ids(x, name: str):
+    """(address, count, what to keep alive) of host page ids."""
+    if isinstance(x, torch.Tensor) and x.dtype is _INT32 and x.device.type == "cpu" and x.is_contiguous():
+        if x.dim() != 1:
+            raise ValueError(f"{name} must be a list of page ids")
+        return x.data_ptr(), x.shape[0], x
+    a = _host_i32(x)
+    if a.ndim != 1:
+        raise ValueError(f"{name} must be a list of page ids")
+    return a.ctypes.data, a.shape[0], a
 
 
 def copy_pages(pools, src_pages, dst_pages, stream=None) -> None:
@@ -257,26 +266,34 @@ def copy_pages(pools, src_pages, dst_pages, stream=None) -> None:
     one launch for all layers' pools and scales.  Every pool has its pages on axis 0, the same
     number of them, each page one contiguous block.  The ids are host integers (a list, a numpy
     array or a CPU tensor); a destination may appear once and may be no source."""
-    pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
-    src, dst = _host_i32(src_pages), _host_i32(dst_pages)
-    if src.ndim != 1 or src.shape != dst.shape:
+    if isinstance(pools, torch.Tensor):
+        pools = (pools,)
+    sp, n, keep_src = _host_ids(src_pages, "src_pages")
+    dp, n_dst, keep_dst = _host_ids(dst_pages, "dst_pages")
+    if n != n_dst:
         raise ValueError("src_pages and dst_pages must be lists of one length")
-    if not pools:
+    if not len(pools):
         return
-    device, pages = pools[0].device, pools[0].shape[0]
-    table = []
+    if any(t.dim() < 1 for t in pools):
+        raise ValueError("every pool must have its pages on axis 0")
+    dev, pages = pools[0].get_device(), pools[0].shape[0]
+    bases, strides, sizes = array("q"), array("q"), array("q")
     for i, t in enumerate(pools):
-        if not t.is_cuda or t.device != device or t.dim() < 1 or t.shape[0] != pages:
-            raise ValueError(f"pools[{i}] must hold {pages} pages on axis 0, on {device}")
-        if not t.is_contiguous() and pages > 0 and not t[0].is_contiguous():
-            raise ValueError(f"pools[{i}]: a page must be one contiguous block")
+        if t.get_device() != dev or dev < 0 or t.shape[0] != pages:
+            raise ValueError(f"pools[{i}] must hold {pages} pages on axis 0, on one CUDA device")
         size = t.element_size()
-        page = t.numel() // max(1, pages) * size
-        table.append((t.data_ptr(), t.stride(0) * size if pages > 1 else page, page))
-    at = np.array(table, dtype=np.int64).T.copy()
-    with _On(device, stream) as s:
-        L.check(L.lib().pkd_copy_pages(at[0].ctypes.data, at[1].ctypes.data, at[2].ctypes.data,
-                                       len(table), pages, src.ctypes.data, dst.ctypes.data, len(src), s))
+        stride = t.stride(0) * size
+        if t.is_contiguous():
+            page = stride if pages > 1 else t.numel() * size
+        else:
+            if pages > 0 and not t[0].is_contiguous():
+                raise ValueError(f"pools[{i}]: a page must be one contiguous block")
+            page = t.numel() // max(1, pages) * size
+        bases.append(t.data_ptr())
+        strides.append(stride if pages > 1 else page)
+        sizes.append(page)
+    _launch(L.lib().pkd_copy_pages, dev, stream, bases.buffer_info()[0], strides.buffer_info()[0],
+            sizes.buffer_info()[0], len(sizes), pages, sp, dp, n)
 
 
 def make_cos_sin_cache(max_position: int, rotary_dim: int, rope_theta: float = 1e4,

@@ -78,9 +78,26 @@ def _i32p(a: np.ndarray) -> int:
     return a.ctypes.data
 
 
+_I64x3 = ctypes.c_int64 * 3
+
+# The current stream's handle on a device.  torch's own accessor of the handle takes a tenth of the
+# time of building a Stream object for it; where torch has none, the object does.
+raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return raw_stream(torch.cuda.current_device())
+
+
+def new_output(shape, like, dtype, stream):
+    """An output on `like`'s device, allocated on the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 _POS_CODE = {"NONE": 0, "ROPE_LLAMA": 1, "ALIBI": 2}
@@ -232,7 +249,7 @@ class BatchDecodePagedKV:
             1.0 if rope_scale is None else float(rope_scale),
             1e4 if rope_theta is None else float(rope_theta), _stream_ptr(stream)))
         self._indices = indices
-        self._plan_args = dict(batch=batch, q_len=int(q_len_per_req),
+        self._plan_args = dict(batch=batch, q_len=int(q_len_per_req), rows=batch * int(q_len_per_req),
                                num_qo_heads=num_qo_heads, num_kv_heads=num_kv_heads,
                                head_dim=head_dim, page_size=page_size, q_dtype=q_dt,
                                kv_dtype=kv_dt, o_dtype=o_dt)
@@ -240,8 +257,6 @@ class BatchDecodePagedKV:
     # ------------------------------------------------------------------ run
     def _kv_pointers(self, paged_kv_cache):
         a = self._plan_args
-        if a["kv_dtype"] == E2M1:
-            a = dict(a, head_dim=a["head_dim"] // 2)  # two values a byte
         if isinstance(paged_kv_cache, (tuple, list)):
             k, v = paged_kv_cache
             if k.dim() != 4 or v.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
@@ -292,8 +307,14 @@ class BatchDecodePagedKV:
         exp_q = (a["batch"] * a["q_len"], a["num_qo_heads"], a["head_dim"])
         if tuple(q.shape) != exp_q or q.dtype != a["q_dtype"] or not q.is_contiguous():
             raise ValueError(f"q must be a contiguous {a['q_dtype']} tensor of shape {exp_q}")
+        if (kv_block_scales is not None) != (a["kv_dtype"] == E2M1):
+            raise ValueError("kv_block_scales belongs to a plan with kv_data_type 'e2m1', and such "
+                             "a plan needs it")
+        if kv_block_scales is not None:
+            return self._run_scaled(q, paged_kv_cache, kv_block_scales, q_scale, k_scale, v_scale, out,
+                                    lse, return_lse, stream, timing_events, enable_pdl)
         kv, k_ptr, v_ptr, num_pages, strides = self._kv_pointers(paged_kv_cache)
-        if kv.dtype not in (CODE_DTYPES if a["kv_dtype"] == E2M1 else (a["kv_dtype"],)):
+        if kv.dtype != a["kv_dtype"]:
             raise ValueError(f"KV dtype {kv.dtype} does not match the plan ({a['kv_dtype']})")
         if out is None:
             out = torch.empty(exp_q, dtype=a["o_dtype"], device=q.device)
@@ -307,27 +328,6 @@ class BatchDecodePagedKV:
         if enable_pdl is not None:
             L.check(L.lib().pkd_set_pdl(self._h, int(bool(enable_pdl))))
         ev0, ev1 = timing_events if timing_events is not None else (None, None)
-        if (kv_block_scales is not None) != (a["kv_dtype"] == E2M1):
-            raise ValueError("kv_block_scales belongs to a plan with kv_data_type 'e2m1', and such "
-                             "a plan needs it")
-        if kv_block_scales is not None:
-            sf = kv_block_scales[0] if isinstance(kv_block_scales, (tuple, list)) else kv_block_scales
-            ks, vs, sf_strides, ps, hkv = pool_views(kv_block_scales, self.kv_layout, "kv_block_scales")
-            if (sf.dtype not in SCALE_DTYPES or sf.shape[-1] != a["head_dim"] // 16
-                    or (sf.shape[0], ps, hkv) != (num_pages, a["page_size"], a["num_kv_heads"])):
-                raise ValueError("kv_block_scales must be float8_e4m3fn (or uint8) of the cache's "
-                                 "shape with a last axis of head_dim / 16")
-            if not (q.device == kv.device == sf.device == self._float_ws.device):
-                raise ValueError("q, the cache, its scales and the workspace must be on one device")
-            L.check(L.lib().pkd_run_scaled(
-                self._h, q.data_ptr(), k_ptr, v_ptr, num_pages, st, ks, vs,
-                (ctypes.c_int64 * 3)(*sf_strides), 1.0 if q_scale is None else float(q_scale),
-                1.0 if k_scale is None else float(k_scale),
-                1.0 if v_scale is None else float(v_scale), out.data_ptr(),
-                lse.data_ptr() if lse is not None else None, _stream_ptr(stream),
-                ev0.cuda_event if ev0 is not None else None,
-                ev1.cuda_event if ev1 is not None else None))
-            return (out, lse) if return_lse else out
         L.check(L.lib().pkd_run_timed(
             self._h, q.data_ptr(), k_ptr, v_ptr, num_pages, st,
             1.0 if q_scale is None else float(q_scale), 1.0 if k_scale is None else float(k_scale),
@@ -335,6 +335,53 @@ class BatchDecodePagedKV:
             lse.data_ptr() if lse is not None else None, _stream_ptr(stream),
             ev0.cuda_event if ev0 is not None else None,
             ev1.cuda_event if ev1 is not None else None))
+        return (out, lse) if return_lse else out
+
+    def _run_scaled(self, q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse, stream,
+                    timing_events, enable_pdl):
+        """run() on a plan with a 4-bit cache; q's shape and dtype are checked."""
+        a = self._plan_args
+        rows, hq, d, ps, hkv = a["rows"], a["num_qo_heads"], a["head_dim"], a["page_size"], a["num_kv_heads"]
+        dev = q.get_device()
+        if torch.cuda.current_device() != dev >= 0:
+            with torch.cuda.device(dev):
+                return self._run_scaled(q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse,
+                                        stream, timing_events, enable_pdl)
+        kv = cache[0] if isinstance(cache, (tuple, list)) else cache
+        sf = scales[0] if isinstance(scales, (tuple, list)) else scales
+        k_ptr, v_ptr, strides, kv_ps, kv_hkv = pool_views(cache, self.kv_layout)
+        ks, vs, sf_strides, sf_ps, sf_hkv = pool_views(scales, self.kv_layout, "kv_block_scales")
+        pages = kv.shape[0]
+        if kv.dtype not in CODE_DTYPES or (kv_ps, kv_hkv, 2 * kv.shape[-1]) != (ps, hkv, d):
+            raise ValueError(f"paged_kv_cache of {kv.dtype} {tuple(kv.shape)} does not match the plan: "
+                             f"4-bit codes, {d // 2} bytes a row")
+        if sf.dtype not in SCALE_DTYPES or (sf.shape[0], sf_ps, sf_hkv, 16 * sf.shape[-1]) != (pages, ps, hkv, d):
+            raise ValueError("kv_block_scales must be float8_e4m3fn (or uint8) of the cache's shape "
+                             "with a last axis of head_dim / 16")
+        if not (dev == kv.get_device() == sf.get_device() == self._float_ws.get_device()):
+            raise ValueError("q, the cache, its scales and the workspace must be on one device")
+        if out is None:
+            out = new_output((rows, hq, d), q, a["o_dtype"], stream)
+        elif (out.shape != (rows, hq, d) or out.dtype != a["o_dtype"] or not out.is_contiguous()
+              or out.get_device() != dev):
+            raise ValueError("out has the wrong shape, dtype, layout or device")
+        if lse is None:
+            if return_lse:
+                lse = new_output((rows, hq), q, torch.float32, stream)
+        elif (lse.shape != (rows, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()
+              or lse.get_device() != dev):
+            raise ValueError("lse must be a contiguous float32 [batch * q_len_per_req, num_qo_heads] "
+                             "tensor on q's device")
+        if enable_pdl is not None:
+            L.check(L.lib().pkd_set_pdl(self._h, int(bool(enable_pdl))))
+        ev0, ev1 = timing_events if timing_events is not None else (None, None)
+        L.check(L.lib().pkd_run_scaled(
+            self._h, q.data_ptr(), k_ptr, v_ptr, pages, _I64x3(*strides), ks, vs, _I64x3(*sf_strides),
+            1.0 if q_scale is None else float(q_scale), 1.0 if k_scale is None else float(k_scale),
+            1.0 if v_scale is None else float(v_scale), out.data_ptr(),
+            None if lse is None else lse.data_ptr(),
+            raw_stream(dev) if stream is None else stream.cuda_stream,
+            None if ev0 is None else ev0.cuda_event, None if ev1 is None else ev1.cuda_event))
         return (out, lse) if return_lse else out
 
     def run_return_lse(self, q: torch.Tensor, paged_kv_cache, *args, **kw):
