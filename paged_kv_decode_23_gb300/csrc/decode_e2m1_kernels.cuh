@@ -127,8 +127,8 @@ __device__ __forceinline__ uint32_t e2m1_off(int r, int c) {
   return (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
 
-// A stage holds its pages one after the other, each as `br` K rows and then br V rows (br = rows of
-// a box: a page, or a tile inside a page).  Row of token j's K; its V is br rows further.
+// A stage holds its boxes one after the other, each as `br` K rows and then br V rows (a box is a
+// page, or a piece of a page of SLICE tokens, so that slices lie at a fixed distance).  Row of token j's K; its V is br rows further.
 __device__ __forceinline__ int e2m1_row(int j, int br) { return j + (j & -br); }
 
 // Token (within 16) of row j of S^T.  Rows of 64 and 32 bytes: in order.  Rows of 128 bytes: the
@@ -175,7 +175,7 @@ __device__ __forceinline__ void produce_e2m1(const DecodeE2m1Params& p, const Bl
   using namespace dev;
   constexpr int TS = G::TS, NSTAGES = G::NSTAGES;
   const int ps = p.page_size, ps_log = __ffs(ps) - 1;
-  const int br = ps < TS ? ps : TS;  // rows of a box: a page, or a tile inside a page
+  const int br = ps < G::SLICE ? ps : G::SLICE;  // rows of a box: a page, or a piece of one
   const int boxes = TS / br;
   const uint32_t tx_per_box = 2u * br * G::ROW;
   const uint64_t pol = policy_evict_first();
@@ -194,7 +194,7 @@ __device__ __forceinline__ void produce_e2m1(const DecodeE2m1Params& p, const Bl
     const int bt0 = t0 + lane * br;
     const bool need = lane < boxes && bt0 < b.it.tok_end && bt0 + br > b.it.tok_begin;
     win.move(tile0 >> ps_log, lane);
-    const int pid = win.id((tile0 >> ps_log) + lane);
+    const int pid = win.id((tile0 + lane * br) >> ps_log);  // (lanes past the boxes: any page)
     const bool whole = t0 >= b.it.tok_begin && t0 + TS <= b.it.tok_end;
     const uint8_t* src[TS / 32];
     bool valid[TS / 32];
@@ -308,6 +308,26 @@ __device__ __forceinline__ void load_q_e2m1(const DecodeParams& p, const BlockCo
   }
 }
 
+// c = a * b, without an accumulator to clear.
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// cap * tanh(x) in base-2 units.  Up to |x| = 1 Lambert's continued fraction for tanh, cut after
+// five terms (off by less than 6e-8 of its value there); beyond, 1 - 2 / (e^(2x) + 1), which loses
+// bits for small x alone.
+__device__ __forceinline__ float soft_cap(float x, float cap_log2, bool any_large) {
+  const float y = x * x;
+  const float n = fmaf(y, y + 105.f, 945.f), d = fmaf(y, fmaf(15.f, y, 420.f), 945.f);
+  float t = x * __fdividef(n, d);
+  if (any_large) t = fabsf(x) > 1.f ? tanh_via_exp2(x) : t;
+  return cap_log2 * t;
+}
+
 // x * (the low or the high half of s, on both halves).
 __device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t s, bool high) {
   const __half2 v = *reinterpret_cast<const __half2*>(&x), f = *reinterpret_cast<const __half2*>(&s);
@@ -329,7 +349,7 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
   const float scale_qk[2] = {p.scale_qk * qmul[0], p.scale_qk * qmul[1]};
   const float cap_log2 = p.cap_log2;
   const int g_row = lane >> 2, tig = lane & 3;
-  const int br = p.page_size < TS ? p.page_size : TS;
+  const int br = p.page_size < G::SLICE ? p.page_size : G::SLICE;
   // tokens (within a 16-token slice) of this lane's two S^T rows
   const int tok_a = e2m1_tok<D>(g_row), tok_b = tok_a + 8;
   // ALiBi slopes of this lane's two C columns (dead columns read the last live head's)
@@ -359,8 +379,7 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
   const uint32_t sf_sel = g_row >= 4 ? 0x7531u : 0x6420u;
   // HEADS 4: columns 0-3 of B take P in the even slots, columns 4-7 in the odd ones
   const uint32_t p_sel0 = g_row < 4 ? 0x4410u : 0x1044u, p_sel1 = g_row < 4 ? 0x4432u : 0x3244u;
-  // stage offset of a warp's next slice (a box of the whole tile keeps K and V rows together)
-  const uint32_t slice = (uint32_t)((br == TS ? 1 : 2) * G::SLICE * G::ROW);
+  constexpr uint32_t kSlice = 2 * G::SLICE * G::ROW;  // stage offset of a warp's next slice
 
   int s = 0;
   uint32_t phase = 0;
@@ -378,24 +397,23 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
 #pragma unroll
     for (int h = 1; h < SL; ++h) work |= hi > h * G::SLICE && lo < h * G::SLICE + 16;
     if (work) {
-      // ---- S^T = K * Q^T : rows = 16 tokens, cols = qo heads; per slice two accumulators
-      float c[SL][4], c2[SL][4];
+      // ---- S^T = K * Q^T : rows = 16 tokens, cols = qo heads
+      float c[SL][4];
 #pragma unroll
       for (int h = 0; h < SL; ++h) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[h][e] = c2[h][e] = 0.f;
         auto k_word = [&](int kk, uint32_t wa, uint32_t wb, uint32_t sa, uint32_t sb, bool high_a, bool high_b) {
           uint32_t x[4], y[4];
           e2m1x8_to_half2x4(wa, x);
           e2m1x8_to_half2x4(wb, y);
           const uint32_t a0[4] = {scaled(x[0], sa, high_a), scaled(y[0], sb, high_b),
                                   scaled(x[1], sa, high_a), scaled(y[1], sb, high_b)};
-          mma_16816<__half>(c[h], a0, qb[kk][0], qb[kk][1]);
+          if (kk == 0) mma_first(c[h], a0, qb[kk][0], qb[kk][1]);
+          else mma_16816<__half>(c[h], a0, qb[kk][0], qb[kk][1]);
           const uint32_t a1[4] = {scaled(x[2], sa, high_a), scaled(y[2], sb, high_b),
                                   scaled(x[3], sa, high_a), scaled(y[3], sb, high_b)};
-          mma_16816<__half>(c2[h], a1, qb[kk + 1][0], qb[kk + 1][1]);
+          mma_16816<__half>(c[h], a1, qb[kk + 1][0], qb[kk + 1][1]);
         };
-        const uint32_t sth = st + h * slice, sfh = st + ksf + h * G::SLICE * G::SB;
+        const uint32_t sth = st + h * kSlice, sfh = st + ksf + h * G::SLICE * G::SB;
         if constexpr (D == 64) {
           const uint2 wa = lds_v2(sth + koff_a[0]), wb = lds_v2(sth + koff_b[0]);
           const uint32_t sf = e4m3x2_to_half2((uint16_t)(lds_u8(sfh) | lds_u8(sfh + 8 * G::SB) << 8));
@@ -418,17 +436,21 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
       // rows g_row (e & 2 clear) and g_row + 8 of slice e / 4, column e & 1
       float sc[4 * SL];
 #pragma unroll
-      for (int e = 0; e < 4 * SL; ++e) sc[e] = c[e >> 2][e & 3] + c2[e >> 2][e & 3];
+      for (int e = 0; e < 4 * SL; ++e) sc[e] = c[e >> 2][e & 3] * scale_qk[e & 1];
       if (p.alibi) {
 #pragma unroll
         for (int e = 0; e < 4 * SL; ++e) {
           const int t = ((e & 2) ? tok_b : tok_a) + (e >> 2) * G::SLICE;
-          sc[e] = score_log2(sc[e], scale_qk[e & 1],
-                             ((e & 1) ? slope1 : slope0) * (float)(t_w + t - b.it.q_pos), cap_log2);
+          sc[e] += ((e & 1) ? slope1 : slope0) * (float)(t_w + t - b.it.q_pos);
         }
-      } else {
+      }
+      if (cap_log2 > 0.f) {
+        float largest = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4 * SL; ++e) sc[e] = score_log2(sc[e], scale_qk[e & 1], 0.f, cap_log2);
+        for (int e = 0; e < 4 * SL; ++e) largest = fmaxf(largest, fabsf(sc[e]));
+        const bool any_large = __any_sync(~0u, largest > 1.f);
+#pragma unroll
+        for (int e = 0; e < 4 * SL; ++e) sc[e] = soft_cap(sc[e], cap_log2, any_large);
       }
       if (lo > 0 || hi < (SL - 1) * G::SLICE + 16) {
 #pragma unroll
@@ -513,7 +535,7 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) {  // two chunks at a time
           uint32_t r[4];
-          ldsm_x4_trans(st + h * slice + voff[x], r);
+          ldsm_x4_trans(st + h * kSlice + voff[x], r);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int ch = 2 * x + y;
@@ -651,6 +673,7 @@ DecodeKernel make_decode_e2m1(int q_dtype) {
   k.rope = 0;
   k.nstages = G::NSTAGES;
   k.max_ctas = CTAS;
+  k.box_rows = G::SLICE;
   return k;
 }
 

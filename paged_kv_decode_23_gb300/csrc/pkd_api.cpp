@@ -810,8 +810,8 @@ int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_b
     prm_all.v_sf = static_cast<const uint8_t*>(sf->v);
     for (int i = 0; i < 3; ++i) prm_all.sf_stride[i] = sf->strides[i];
   }
-  const int tile = h->kernel->tile_tokens;
-  const int box_rows = h->page_size < tile ? h->page_size : tile;
+  const int most = h->kernel->box_rows ? h->kernel->box_rows : h->kernel->tile_tokens;
+  const int box_rows = h->page_size < most ? h->page_size : most;
   // A 4-bit pool with V behind K at a distance that a tensor map can hold takes one map, whose
   // boxes bring a page's K and V together; else (a (k, v) pair the other way round) one map each.
   const int64_t kv_stride = static_cast<const char*>(v_base) - static_cast<const char*>(k_base);

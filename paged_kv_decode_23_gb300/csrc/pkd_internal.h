@@ -134,6 +134,7 @@ struct DecodeKernel {
   int rope;         // 1: rotates q and K (ROPE_LLAMA) before the QK product
   int nstages;      // pipeline stages
   int max_ctas = kDecodeCtasPerSm;  // CTAs per SM it is sized for
+  int box_rows = 0;                 // rows of a tensor-map box at most; 0: tile_tokens
 };
 
 // Registries filled by the kernel translation units.
