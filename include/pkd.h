@@ -178,19 +178,33 @@ int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* 
 
 /*
  * Run a plan whose kv_dtype is PKD_DTYPE_E2M1 (pkd_run refuses it, and this call refuses every
- * other plan).  Arguments as in pkd_run_timed, and the scale pools:
- *   k_base / v_base, kv_strides: the code pools; strides in bytes, multiples of 16 as above.
- *   k_scales / v_scales (device), scale_strides[3]: scale byte (page, slot, head, block) of K / V
- *     lives at base + page*scale_strides[0] + slot*scale_strides[1] + head*scale_strides[2] +
- *     block.  Strides in bytes, in any order; bases and strides are multiples of head_dim / 16
- *     (4, 8 or 16 bytes: a token's scales are one copy).
+ * other plan).  The fields are pkd_run_timed's arguments, and the scale pools:
+ *   k / v, strides: the code pools; strides in bytes, multiples of 16 as above.
+ *   k_scales / v_scales (device), scale_strides: scale byte (page, slot, head, block) of K / V lives
+ *     at base + page*scale_strides[0] + slot*scale_strides[1] + head*scale_strides[2] + block.
+ *     Strides in bytes, in any order; bases and strides are multiples of head_dim / 16 (4, 8 or
+ *     16 bytes: a token's scales are one copy).
  * A slot outside a request's attended tokens may hold anything, NaN scales among it.
  */
-int pkd_run_scaled(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
-                   int64_t num_pages, const int64_t kv_strides[3], const void* k_scales,
-                   const void* v_scales, const int64_t scale_strides[3], float q_scale,
-                   float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
-                   void* ev_end);
+typedef struct pkd_scaled_run {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* k_scales;
+  const void* v_scales;
+  int64_t num_pages;
+  int64_t strides[3];
+  int64_t scale_strides[3];
+  void* o;
+  float* lse;     /* or NULL */
+  void* ev_start; /* cudaEvent_t or NULL, as in pkd_run_timed */
+  void* ev_end;
+  float q_scale;
+  float k_scale;
+  float v_scale;
+  int32_t reserved;
+} pkd_scaled_run;
+int pkd_run_scaled(pkd_handle* h, const pkd_scaled_run* run, void* stream);
 
 /*
  * Programmatic dependent launch (the page's run(enable_pdl=...)), on by default.  When on, the

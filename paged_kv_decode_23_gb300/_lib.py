@@ -42,9 +42,8 @@ SIGNATURES = {
                          _vp, _vp, _vp]),
     "pkd_run_timed": (_c_int, [_vp, _vp, _vp, _vp, ctypes.c_int64, _i64p, _c_float, _c_float,
                                _c_float, _vp, _vp, _vp, _vp, _vp]),
-    "pkd_run_scaled": (_c_int, [_vp, _vp, _vp, _vp, ctypes.c_int64, _i64p, _vp, _vp, _i64p, _c_float,
-                                _c_float, _c_float, _vp, _vp, _vp, _vp, _vp]),
-    # the argument structs travel as packed bytes (cache.py)
+    # the argument structs of these three travel as packed bytes (decode.py, cache.py)
+    "pkd_run_scaled": (_c_int, [_vp, ctypes.c_char_p, _vp]),
     "pkd_append": (_c_int, [ctypes.c_char_p, _vp]),
     "pkd_gather": (_c_int, [ctypes.c_char_p, _vp]),
     "pkd_copy_pages": (_c_int, [_vp, _vp, _vp, _c_int, ctypes.c_int64, _vp, _vp, ctypes.c_int64, _vp]),

@@ -898,14 +898,11 @@ int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* 
                     o, lse, stream, ev_start, ev_end);
 }
 
-int pkd_run_scaled(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
-                   int64_t num_pages, const int64_t kv_strides[3], const void* k_scales,
-                   const void* v_scales, const int64_t scale_strides[3], float q_scale,
-                   float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
-                   void* ev_end) {
-  const ScalePools sf{k_scales, v_scales, scale_strides};
-  return run_decode(h, q, k_base, v_base, num_pages, kv_strides, &sf, q_scale, k_scale, v_scale, o,
-                    lse, stream, ev_start, ev_end);
+int pkd_run_scaled(pkd_handle* h, const pkd_scaled_run* r, void* stream) {
+  if (!r) return fail(PKD_ERR_INVALID_ARG, "run is null");
+  const ScalePools sf{r->k_scales, r->v_scales, r->scale_strides};
+  return run_decode(h, r->q, r->k, r->v, r->num_pages, r->strides, &sf, r->q_scale, r->k_scale,
+                    r->v_scale, r->o, r->lse, stream, r->ev_start, r->ev_end);
 }
 
 int pkd_run(pkd_handle* h, const void* q, const void* k_base, const void* v_base,

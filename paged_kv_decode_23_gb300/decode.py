@@ -10,6 +10,7 @@ device memory and the current stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Tuple, Union
 
 import numpy as np
@@ -78,7 +79,7 @@ def _i32p(a: np.ndarray) -> int:
     return a.ctypes.data
 
 
-_I64x3 = ctypes.c_int64 * 3
+_SCALED_RUN = struct.Struct("@5Pq3q3q4P3fi")  # pkd_scaled_run
 
 # The current stream's handle on a device.  torch's own accessor of the handle takes a tenth of the
 # time of building a Stream object for it; where torch has none, the object does.
@@ -361,7 +362,7 @@ class BatchDecodePagedKV:
         if not (dev == kv.get_device() == sf.get_device() == self._float_ws.get_device()):
             raise ValueError("q, the cache, its scales and the workspace must be on one device")
         if out is None:
-            out = new_output((rows, hq, d), q, a["o_dtype"], stream)
+            out = torch.empty_like(q) if stream is None else new_output((rows, hq, d), q, q.dtype, stream)
         elif (out.shape != (rows, hq, d) or out.dtype != a["o_dtype"] or not out.is_contiguous()
               or out.get_device() != dev):
             raise ValueError("out has the wrong shape, dtype, layout or device")
@@ -375,13 +376,14 @@ class BatchDecodePagedKV:
         if enable_pdl is not None:
             L.check(L.lib().pkd_set_pdl(self._h, int(bool(enable_pdl))))
         ev0, ev1 = timing_events if timing_events is not None else (None, None)
-        L.check(L.lib().pkd_run_scaled(
-            self._h, q.data_ptr(), k_ptr, v_ptr, pages, _I64x3(*strides), ks, vs, _I64x3(*sf_strides),
-            1.0 if q_scale is None else float(q_scale), 1.0 if k_scale is None else float(k_scale),
-            1.0 if v_scale is None else float(v_scale), out.data_ptr(),
-            None if lse is None else lse.data_ptr(),
-            raw_stream(dev) if stream is None else stream.cuda_stream,
-            None if ev0 is None else ev0.cuda_event, None if ev1 is None else ev1.cuda_event))
+        args = _SCALED_RUN.pack(
+            q.data_ptr(), k_ptr, v_ptr, ks, vs, pages, *strides, *sf_strides, out.data_ptr(),
+            0 if lse is None else lse.data_ptr(), 0 if ev0 is None else ev0.cuda_event,
+            0 if ev1 is None else ev1.cuda_event, 1.0 if q_scale is None else q_scale,
+            1.0 if k_scale is None else k_scale, 1.0 if v_scale is None else v_scale, 0)
+        rc = L.lib().pkd_run_scaled(self._h, args, raw_stream(dev) if stream is None else stream.cuda_stream)
+        if rc:
+            L.check(rc)
         return (out, lse) if return_lse else out
 
     def run_return_lse(self, q: torch.Tensor, paged_kv_cache, *args, **kw):

@@ -263,3 +263,24 @@ def test_cos_sin_cache():
     for bad in (0, 8, -16):
         with pytest.raises(ValueError):
             make_cos_sin_cache(10, bad, device="cpu")
+
+
+def test_packed_structs_have_the_header_s_sizes(tmp_path):
+    """The binding packs the argument structs by hand: their sizes and a field's place in each must
+    be the C compiler's."""
+    import os
+    import struct
+    import subprocess
+    from paged_kv_decode_23_gb300 import cache as C, decode as D
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include "pkd.h"\nint main(void) { printf("%zu %zu %zu %zu %zu %zu %zu\\n", '
+                   "sizeof(pkd_paged_pool), sizeof(pkd_append_args), sizeof(pkd_gather_args), sizeof(pkd_scaled_run), "
+                   "offsetof(pkd_append_args, eps), offsetof(pkd_gather_args, out_dtype), offsetof(pkd_scaled_run, q_scale));"
+                   " return 0; }\n")
+    exe = tmp_path / "sizes"
+    subprocess.run(["gcc", "-I", include, str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    sizes = [struct.Struct("@" + C._POOL).size, C._APPEND.size, C._GATHER.size, D._SCALED_RUN.size]
+    assert got[:4] == sizes
+    assert got[4:] == [C._APPEND.size - 8 - 24, C._GATHER.size - 8, D._SCALED_RUN.size - 16]
