@@ -423,8 +423,8 @@ typedef struct pkd_paged_pool {
   int32_t dtype; /* PKD_DTYPE_* of the cache */
   int32_t num_kv_heads;
   int32_t head_dim;  /* 64, 128 or 256 */
-  int32_t page_size; /* a power of two in [1, 2^20] */
-  float k_scale;     /* value = stored value * k_scale (v_scale): positive, finite, 1 if unused */
+  int32_t page_size; /* a power of two in [8, 256] */
+  float k_scale;     /* value = stored value * k_scale (v_scale): in [2^-64, 2^64], 1 if unused */
   float v_scale;
   int32_t reserved;
 } pkd_paged_pool;
@@ -449,8 +449,9 @@ typedef struct pkd_paged_pool {
  *     [0, cos_sin_rows) leaves the whole row out, with PKD_STATUS_BAD_TOKEN.
  *   - Two rows of one call must not have the same slot (nor one sequence share a page that it
  *     appends to with another: see pkd_pages_fork).
+ * eps: 0 or a normal 32-bit number.
  * q may be NULL (num_qo_heads 0), and k with v NULL (only q is normed and rotated).  q_out may be
- * q itself.  All of q, k, v, q_out: in_dtype F16 or BF16, head_dim contiguous, 16-byte aligned,
+ * q itself; its rows must not overlap.  All of q, k, v, q_out: in_dtype F16 or BF16, head_dim contiguous, 16-byte aligned,
  * strides {token, head} in elements, multiples of 8.  Weights: head_dim values of in_dtype, or
  * float32 with weight_f32; 16-byte aligned.  rotary_dim: 0 or a multiple of 16 up to head_dim;
  * cos_sin float32 [cos_sin_rows, rotary_dim], contiguous, 16-byte aligned.
@@ -491,7 +492,7 @@ int pkd_append(const pkd_append_args* args, void* stream);
  * BF16; for a 16-bit cache its own type).  Rows of padding (negative batch index) and rows with no
  * slot are left as they were, the latter with a status bit as in pkd_append.
  * k_out / v_out: head_dim contiguous, 16-byte aligned, strides {token, head} in elements,
- * multiples of 8; either may be NULL.  A row may be listed any number of times.
+ * multiples of 8, without overlap; either may be NULL.  A row may be listed any number of times.
  */
 typedef struct pkd_gather_args {
   pkd_paged_pool pool;

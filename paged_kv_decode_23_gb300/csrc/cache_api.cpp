@@ -2,7 +2,7 @@
 // and the bookkeeping of a pool's pages (pkd_pages_*).
 #include <cuda_runtime.h>
 
-#include <cmath>
+#include <cfloat>
 #include <cstring>
 #include <exception>
 #include <new>
@@ -92,6 +92,18 @@ int check_rows(const void* p, const int64_t (&st)[2], const char* name) {
   return PKD_OK;
 }
 
+// Rows that are written: no two may share bytes.
+int check_out(const void* p, const int64_t (&st)[2], int64_t tokens, int64_t heads, int head_dim,
+              const char* name) {
+  if (int rc = check_rows(p, st, name)) return rc;
+  const int64_t D = head_dim;
+  const bool by_token = (heads <= 1 || st[1] >= D) && (tokens <= 1 || st[0] >= (heads - 1) * st[1] + D);
+  const bool by_head = (tokens <= 1 || st[0] >= D) && (heads <= 1 || st[1] / (tokens > 1 ? tokens - 1 : 1) >= st[0] &&
+                                                        st[1] - (tokens - 1) * st[0] >= D);
+  if (!by_token && !by_head) return bad(std::string(name) + ": its rows overlap");
+  return PKD_OK;
+}
+
 }  // namespace
 
 extern "C" int pkd_append(const pkd_append_args* args, void* stream) {
@@ -109,7 +121,7 @@ extern "C" int pkd_append(const pkd_append_args* args, void* stream) {
     if (!kv && !a.q) return bad("neither q nor k and v are given");
     if (a.q) {
       if (int rc = check_rows(a.q, a.q_strides, "q")) return rc;
-      if (int rc = check_rows(a.q_out, a.q_out_strides, "q_out")) return rc;
+      if (int rc = check_out(a.q_out, a.q_out_strides, a.num_tokens, a.num_qo_heads, a.pool.head_dim, "q_out")) return rc;
     }
     if (kv) {
       if (int rc = check_rows(a.k, a.k_strides, "k")) return rc;
@@ -118,7 +130,8 @@ extern "C" int pkd_append(const pkd_append_args* args, void* stream) {
     if (!a.batch_indices || !a.positions) return bad("null batch_indices / positions");
     if ((a.q_weight && !on16(a.q_weight)) || (a.k_weight && !on16(a.k_weight)))
       return bad("the norm weights must be 16-byte aligned");
-    if (!(a.eps >= 0.0 && std::isfinite(a.eps))) return bad("eps must be >= 0 and finite");
+    if (!(a.eps == 0.0 || (a.eps >= FLT_MIN && a.eps <= FLT_MAX)))
+      return bad("eps must be 0 or a normal 32-bit number");
     if (a.rotary_dim < 0 || a.rotary_dim > a.pool.head_dim || a.rotary_dim % 16 != 0)
       return bad("rotary_dim must be 0 or a multiple of 16 up to head_dim");
     if (a.rotary_dim > 0 && (!a.cos_sin || !on16(a.cos_sin) || a.cos_sin_rows < 0))
@@ -136,9 +149,11 @@ extern "C" int pkd_gather(const pkd_gather_args* args, void* stream) {
     if (a.num_tokens == 0) return done(cudaSuccess, "");
     if (!a.k_out && !a.v_out) return bad("k_out and v_out are both null");
     if (a.k_out)
-      if (int rc = check_rows(a.k_out, a.k_out_strides, "k_out")) return rc;
+      if (int rc = check_out(a.k_out, a.k_out_strides, a.num_tokens, a.pool.num_kv_heads, a.pool.head_dim, "k_out"))
+        return rc;
     if (a.v_out)
-      if (int rc = check_rows(a.v_out, a.v_out_strides, "v_out")) return rc;
+      if (int rc = check_out(a.v_out, a.v_out_strides, a.num_tokens, a.pool.num_kv_heads, a.pool.head_dim, "v_out"))
+        return rc;
     if (!a.batch_indices || !a.positions) return bad("null batch_indices / positions");
     return done(launch_gather(a, static_cast<cudaStream_t>(stream)), "gather kernel launch");
   });

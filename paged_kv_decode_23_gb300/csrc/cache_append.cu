@@ -5,9 +5,10 @@
 // bytes) each: where pairs (i, i + rotary_dim / 2) turn, a lane holds both pieces of its pairs, else
 // 16 values on end, so that no rotation needs another lane's values.  The sum of squares is a
 // shuffle tree over the group; a block of the 4-bit cache is two pieces, wherever they are.  A warp
-// takes one token's neighbouring heads, all q, all k or all v, up to R for each of its groups, and
-// loads them before it uses the first; weights, cosines and sines are read once for them, and all
-// that depends on the token is the same in every lane, so that every shuffle is the whole warp's.
+// takes one token's neighbouring heads, all q, all k or all v, up to R for each of its groups;
+// weights, cosines and sines are read once for them, and all that depends on the token is the same
+// in every lane, so that every shuffle is the whole warp's.  Warps stay for several items where a
+// call has more than fit, the next item's rows under way while the current ones are worked on.
 // Pairs of values go through the packed 32-bit FMA.
 //
 // Codes.  A cache of 8 or 4 bits stores the code nearest to the exact quotient, so that neither
@@ -15,11 +16,15 @@
 // the input (v; k without norm, outside the rotated dims) is exact: its quotient is rounded to odd
 // and that to the code.  Ties are common there, one value in eight with a scale of few bits.  A
 // computed value's quotient t has an error bound e: where the codes of t - e and t + e agree (all
-// but about one value in 1e5) that is the code, else its warp goes through its rows once more in
-// 64 bits.
+// but about one value in 1e5) that is the code, else that value is computed once more in 64 bits;
+// where it is a block's scale that is in doubt, the warp's rows are.
 //
-// Bound: bytes.  Every input byte is read once and every output byte written once; see the
-// figures at the launcher.
+// Bound: every input byte is read once and every output byte written once.  A 16-bit cache comes
+// near that: 8,190 tokens of 64 + 2 * 8 heads of 128, fp16, norm and rotation, 340 MB: 65 us, 5.2 TB/s.
+// An 8- or 4-bit cache is bound by instructions (two conversions a computed value, the products
+// rounded to odd of the others): 4,095 tokens of 16 + 2 * 2 heads of 256, bf16 into e4m3, 81 MB:
+// 31 us, 2.6 TB/s, 0.63 warp instructions issued per cycle and scheduler, 50 % of the ALU pipe.  A decode
+// step's call is latency: 3.5 us (4.8 us a replayed graph of one call).
 #include <type_traits>
 
 #include "cache_rows.cuh"
@@ -99,10 +104,25 @@ struct Codes {
 // 1 / sqrt(mean(x^2) + eps) of a row in 64 bits; x: this lane's 16 values.  The squares of 16-bit
 // values are exact in 32 bits and are summed with their rounding errors kept (Knuth's two-sum), so
 // that the 64-bit pipe, 16 cycles an instruction, has only the root to do: one Newton step from
-// the 32-bit root, good to 2^-42.  Whole warps.
+// the 32-bit root, good to 2^-42.  (bf16 rows of magnitudes whose squares would leave the 32-bit
+// range are scaled by a power of 2 first.)  Whole warps.
 template <typename T, int D>
 __device__ __forceinline__ double exact_rnorm(const uint4 (&raw)[2], double eps) {
   constexpr int LANES = D / 16;
+  float z = 1.f;
+  if (std::is_same<T, __nv_bfloat16>::value) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float x[8];
+      unpack8<T>(raw[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+    }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    z = top > 0x1p55f ? 0x1p-70f : top < 0x1p-45f ? 0x1p80f : 1.f;
+  }
   float s = 0.f, low = 0.f;
   auto add = [&](float x) {
     const float t = s + x, b = t - s;
@@ -114,7 +134,7 @@ __device__ __forceinline__ double exact_rnorm(const uint4 (&raw)[2], double eps)
     float x[8];
     unpack8<T>(raw[i], x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) add(x[e] * x[e]);
+    for (int e = 0; e < 8; ++e) add((x[e] * z) * (x[e] * z));
   }
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) {
@@ -122,7 +142,8 @@ __device__ __forceinline__ double exact_rnorm(const uint4 (&raw)[2], double eps)
     add(os);
     low += ol;
   }
-  const double m = ((double)s + low) * (1.0 / D) + eps;
+  const double m = ((double)s + low) * (1.0 / D) / ((double)z * z) + eps;
+  if (!(m > 0x1p-100 && m < 0x1p120)) return 1.0 / sqrt(m);
   const double r = rsqrtf((float)m);
   return r * (1.5 - 0.5 * m * r * r);
 }
@@ -435,7 +456,23 @@ __device__ __forceinline__ void append_item(const AppendParams& p, const Item<T,
       float sum = (ss[0].x + ss[0].y) + (ss[1].x + ss[1].y);
 #pragma unroll
       for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      const float rn = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+      float m = fmaf(sum, 1.f / D, p.eps);
+      // bf16 has 32-bit floats' range: rows whose squares would leave it are scaled by a power of 2
+      if (std::is_same<T, __nv_bfloat16>::value && __any_sync(~0u, !(m > 0x1p-100f && m < 0x1p120f))) {
+        const float z = m > 0x1p-100f && m < 0x1p120f ? 1.f : m < 1.f ? 0x1p80f : 0x1p-70f;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y[i][e] *= z;
+            sum = fmaf(y[i][e], y[i][e], sum);
+          }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        m = fmaf(sum, 1.f / D, p.eps * z * z);
+      }
+      const float rn = rsqrtf(m);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -601,8 +638,10 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
 
 template <typename T, int KV, int D>
 cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
-  // Heads a group takes: one while the call leaves SMs idle (a decode step is latency), several
-  // once there is work for every SM several times over.
+  // Heads a group takes of a 16-bit cache's call: one while the call leaves SMs idle, two once there
+  // is work for every SM several times over, which keeps more bytes under way.  Replayed graphs with
+  // one and with two: one token of 32 + 2 * 8 heads of 128 4.8 and 5.5 us, 340 MB of prompts 85.8 and
+  // 67.3 us.  Rows that become codes take the registers that a second head would: always one.
   const int64_t rows = a.num_tokens * (a.num_qo_heads + 2 * (int64_t)a.pool.num_kv_heads);
   if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, KV == kSame16 ? 2 : 1>(a, s);
   return launch_r<T, KV, D, 1>(a, s);

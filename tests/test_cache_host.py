@@ -160,6 +160,8 @@ APPEND_REFUSALS = [
     dict(n=-1), dict(hq=0), dict(q=0), dict(kr=0), dict(vr=0), dict(out=0), dict(q=264), dict(qst=(512, 4)),
     dict(bi=0), dict(pos=0), dict(qw=8), dict(eps=-1.0), dict(eps=float("nan")), dict(rotary=8, cs=64),
     dict(rotary=144, cs=64), dict(rotary=64), dict(rotary=64, cs=72), dict(kst=(-256, 128)), dict(batch=-1),
+    dict(eps=1e-50), dict(eps=1e300), dict(n=2, ost=(0, 128)), dict(n=3, ost=(504, 128)), dict(ost=(512, 120)),
+    dict(n=3, ost=(128, 376)), dict(n=2, ost=(64, 512)),
 ]
 
 
@@ -180,6 +182,8 @@ def test_append_and_gather_of_nothing_need_no_device():
     for bad in ((*pool, 0, 0, 256, 128, 256, 128, 64, 64, 0, 1, 1, 0),      # no output
                 (*pool, 264, 0, 256, 128, 256, 128, 64, 64, 0, 1, 1, 0),    # misaligned
                 (*pool, 256, 0, 256, 128, 256, 128, 0, 64, 0, 1, 1, 0),     # no batch_indices
+                (*pool, 256, 0, 248, 128, 256, 128, 64, 64, 0, 2, 1, 0),    # k's rows overlap
+                (*pool, 256, 256, 256, 128, 0, 128, 64, 64, 0, 2, 1, 0),    # v's rows overlap
                 (*pool, 256, 0, 256, 128, 256, 128, 64, 64, 0, 1, 0, 0)):   # bf16 cache, fp16 rows
         assert L.lib().pkd_gather(C._GATHER.pack(*bad), None) in (-1, -5)
 

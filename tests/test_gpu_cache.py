@@ -183,12 +183,31 @@ def test_append_special_values(kv):
         want = np.zeros_like(nan)
         if wide:  # the norm spreads a NaN over its head
             want[row, head] = True
-            want[7, 1] = nan[7, 1]  # (3e38)^2 overflows: its head is 0 or NaN
         elif kv == "e2m1":
             want[row, head, d0 // 16 * 16:d0 // 16 * 16 + 16] = True
         else:
             want[row, head, d0] = True
         assert np.array_equal(nan, want)
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3", "e2m1"])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_append_norm_of_any_magnitude(kv, eps):
+    """bf16 rows whose squares leave the 32-bit range, at either end, and rows of mixed magnitudes."""
+    power = [-126, -110, -100, -70, -62, -50, -40, -20, 0, 30, 50, 58, 62, 63, 64, 80, 100, 125]
+    n, hkv, d = len(power) + 2, 3, 64
+    pg = Pages([n], 16, hkv, d, kv, "NHD", seed=4)
+    q, k, v = _qkv(n, 5, hkv, d, BF16, seed=9, fused=False)
+    for x in (q, k):
+        x.clamp_(-4, 4)  # (times 2^125 that is the type's range)
+        for i, p in enumerate(power):
+            x[i] = (x[i].double() * 2.0 ** p).to(BF16)
+        x[n - 2, :, 3] = 2.0 ** 120
+        x[n - 1] = (x[n - 1].double() * 2.0 ** -120).to(BF16)
+        x[n - 1, :, 40] = 2.0 ** -70
+    w = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(8))).cuda()
+    check_append(pg, q, k, v, np.zeros(n, int), np.arange(n), w, w, cos_sin=_table(n, 32), eps=eps,
+                 k_scale=None if kv == "same" else 0.4)
 
 
 def test_append_strides_alignment_and_in_place():
