@@ -7,13 +7,15 @@
 // (S^T = K Q^T and O^T += V^T P^T, mma.m16n8k16, fp32 accumulators) take exact operands and the
 // only rounding before the epilogue is P's to fp16 (11 bits).
 //
-// Structure as in decode_kernels.cuh (producer warp, mbarrier ring, consumer warps of 16 tokens
-// each, split partials merged by the last chunk's CTA), with these differences:
+// Structure as in decode_kernels.cuh (producer warp, mbarrier ring, consumer warps, split partials
+// merged by the last chunk's CTA), with these differences:
+//   * four consumer warps take two slices of 16 tokens of a tile each and make one softmax step of
+//     them; more and smaller CTAs per SM (up to four) hide each other's waits;
 //   * the codes come by TMA, one box per page that holds both its K and its V rows (a 5-D map with
 //     K and V as an axis): the TMA unit takes some 65 cycles a request whatever its size, and a
-//     page's K rows alone are 1 KiB at page size 16.  A second producer warp copies the scales
+//     page's K rows alone are 1 KiB at page size 16.  The producer's lanes copy the scales
 //     (D/16 bytes a token: too short for a tensor-map box in every layout) by cp.async on the
-//     same full barrier.  Both keep the ids of 32 pages in registers, loaded 32 pages ahead.
+//     same full barrier, and keep the ids of 32 pages in registers, loaded 32 pages ahead.
 //     Tokens that are not attended, or whose page id is bad, get zero scales: whatever bits their
 //     codes hold, their V rows are zeros (an e2m1 code is always finite), so no row needs masking
 //     before P V;
@@ -25,8 +27,14 @@
 //     registers, the product is taken twice with P next to zeros: slots {2t, 2t+1} of an A row hold
 //     dims d and d+1 of token t; B = (p, 0) gives O[d] and B = (0, p) gives O[d+1].  That costs
 //     eight more MMAs per 16 tokens (head_dim 128) and saves 32 permutes.
-// Bound: the integer pipe (a cvt per pair of values, 64 per 16 tokens and warp) next to HBM, see
-// the figures at the registry.
+//   * tasks of up to 4 qo heads: the eight columns of P^T are those heads twice, next to (p, 0) and to
+//     (0, p), so that one MMA makes both products.
+// Bound: instructions next to HBM.  A cvt per pair of values (head_dim 128: 64 per 16 tokens and
+// warp) and the scales' products go through pipes of 2 warp instructions a cycle.  32 qo and 8 kv
+// heads of 128, 4 contexts of 131,072 (604 MB, HND, fp16): 110 us, 5.5 TB/s, ALU pipe 55 %,
+// tensor pipe 28 %; with the copies alone 94 us, with the arithmetic alone 99.  64 contexts of
+// 512 to 4,096 (171 MB, NHD, bf16): 46 us, 3.7 TB/s, of which 7 us go into NHD's scale copies (8 bytes a token, each
+// in a sector of its own; HND: 39.7 us).
 #pragma once
 
 #include <cfloat>

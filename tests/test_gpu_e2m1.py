@@ -181,6 +181,67 @@ def test_strided_pools():
     assert torch.equal(dec.run(q, wide[:, :, 2:18, 1:, 16:80], kv_block_scales=sf), want)
 
 
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+@pytest.mark.parametrize("page", [8, 32, 128])
+@pytest.mark.parametrize("first", ["k", "v"])
+def test_k_and_v_in_buffers_of_their_own(layout, page, first):
+    """A (k, v) pair of separate tensors, K's buffer below V's and above it."""
+    pg = Pages([1000, 1, 333, 64], page, 2, 128, "e2m1", layout, seed=6)
+    q = _q(4, 8, 128, BF16)
+    dec = _dec(pg, 8, BF16)
+    want = dec.run(q, pg.pool, kv_block_scales=pg.scales)
+
+    def apart(x):
+        b = torch.empty((2, x.shape[0]) + x.shape[2:], dtype=torch.uint8, device="cuda")
+        at = (0, 1) if first == "k" else (1, 0)
+        for i, j in enumerate(at):
+            b[j] = x.view(torch.uint8)[:, i]
+        return b[at[0]], b[at[1]]
+    got = dec.run(q, apart(pg.pool), kv_block_scales=apart(pg.scales))
+    torch.cuda.synchronize()
+    assert dec.check_status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("cap", [1.0, 50.0])
+def test_soft_cap_of_small_logits(cap):
+    """Logits far below the cap pass it unchanged but for their cube: lse is good to its own
+    rounding (2^-21 near 7) and the 32-bit sums' (16 roundings), below 2e-6; five times that."""
+    pg = Pages([1000, 40], 16, 2, 128, "e2m1", "HND", seed=2)
+    q = (_q(2, 8, 128, F16).float() * 1e-3).to(F16)
+    dec = _dec(pg, 8, F16, logits_soft_cap=cap)
+    o, lse = dec.run(q, pg.pool, kv_block_scales=pg.scales, return_lse=True)
+    assert_decode(pg, q, o, lse, 8, cap=cap)
+    _, ref = _ref(pg, q, 8, cap=cap)
+    assert np.abs(lse.double().cpu().numpy() - ref).max() <= 1e-5
+
+
+def test_two_plans_on_two_streams():
+    """Two handles with workspaces of their own, their appends, runs and gathers in flight at once."""
+    from paged_kv_decode_23_gb300 import append_paged_kv, gather_paged_kv
+    sides = []
+    for i, (hq, d) in enumerate(((8, 128), (24, 64))):
+        pg = Pages([2000 + i, 700, 1], 16, 2, d, "e2m1", "NHD", seed=20 + i)
+        g = torch.Generator().manual_seed(i)
+        rows = [torch.randn(3, h, d, generator=g).to(BF16).cuda() for h in (hq, 2, 2)]
+        b = torch.arange(3, dtype=torch.int32, device="cuda")
+        pos = torch.from_numpy(pg.lens.astype(np.int32) - 1).cuda()
+        sides.append((pg, _dec(pg, hq, BF16), rows, b, pos, torch.cuda.Stream()))
+
+    def step(side, stream):
+        pg, dec, rows, b, pos, _ = side
+        table = dict(kv_indptr=pg.indptr, kv_indices=pg.indices, kv_layout="NHD", kv_block_scales=pg.scales)
+        q = append_paged_kv(*rows, b, pos, pg.pool, stream=stream, **table)
+        o = dec.run(q, pg.pool, kv_block_scales=pg.scales, stream=stream)
+        return (o,) + gather_paged_kv(b, pos, pg.pool, stream=stream, **table)
+    want = [step(s, None) for s in sides]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [step(s, s[5]) for s in sides]
+    torch.cuda.synchronize()
+    for s, g, w in zip(sides, got, want):
+        assert s[1].check_status() == 0 and all(torch.equal(x, y) for x, y in zip(g, w))
+
+
 def test_refusals():
     from paged_kv_decode_23_gb300 import PkdError
     pg = Pages([40], 16, 2, 128, "e2m1", "NHD", seed=3)
