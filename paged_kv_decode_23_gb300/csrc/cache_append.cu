@@ -101,6 +101,19 @@ struct Codes {
   uint32_t scale[2];  // e2m1: the scale byte of the piece's block
 };
 
+// Mean square of z times a row, a power of 2; a, b: this lane's 16 values.  Whole warps.
+template <typename T, int D>
+__device__ __noinline__ float scaled_mean(uint4 a, uint4 b, float z) {
+  float x[16], sum = 0.f;
+  unpack8<T>(a, *reinterpret_cast<float(*)[8]>(x));
+  unpack8<T>(b, *reinterpret_cast<float(*)[8]>(x + 8));
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sum = fmaf(x[e] * z, x[e] * z, sum);
+#pragma unroll
+  for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return sum * (1.f / D);
+}
+
 // 1 / sqrt(mean(x^2) + eps) of a row in 64 bits; x: this lane's 16 values.  The squares of 16-bit
 // values are exact in 32 bits and are summed with their rounding errors kept (Knuth's two-sum), so
 // that the 64-bit pipe, 16 cycles an instruction, has only the root to do: one Newton step from
@@ -460,17 +473,11 @@ __device__ __forceinline__ void append_item(const AppendParams& p, const Item<T,
       // bf16 has 32-bit floats' range: rows whose squares would leave it are scaled by a power of 2
       if (std::is_same<T, __nv_bfloat16>::value && __any_sync(~0u, !(m > 0x1p-100f && m < 0x1p120f))) {
         const float z = m > 0x1p-100f && m < 0x1p120f ? 1.f : m < 1.f ? 0x1p80f : 0x1p-70f;
-        sum = 0.f;
+        m = scaled_mean<T, D>(raw[j][0], raw[j][1], z) + p.eps * z * z;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[i][e] *= z;
-            sum = fmaf(y[i][e], y[i][e], sum);
-          }
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        m = fmaf(sum, 1.f / D, p.eps * z * z);
+          for (int e = 0; e < 8; ++e) y[i][e] *= z;
       }
       const float rn = rsqrtf(m);
 #pragma unroll
