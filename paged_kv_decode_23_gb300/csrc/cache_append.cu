@@ -8,7 +8,9 @@
 // takes one token's neighbouring heads, all q, all k or all v, up to R for each of its groups;
 // weights, cosines and sines are read once for them, and all that depends on the token is the same
 // in every lane, so that every shuffle is the whole warp's.  Warps stay for several items where a
-// call has more than fit, the next item's rows under way while the current ones are worked on.
+// call has more than fit, the next item's rows under way while the current ones are worked on; into
+// a 16-bit cache a warp's items are all of one chunk of heads, whose weights it keeps (65.2 -> 62.9 us
+// for the prompts below; codes take the registers that this needs, and cost unlike q).
 // Pairs of values go through the packed 32-bit FMA.
 //
 // Codes.  A cache of 8 or 4 bits stores the code nearest to the exact quotient, so that neither
@@ -20,10 +22,10 @@
 // where it is a block's scale that is in doubt, the warp's rows are.
 //
 // Bound: every input byte is read once and every output byte written once.  A 16-bit cache comes
-// near that: 8,190 tokens of 64 + 2 * 8 heads of 128, fp16, norm and rotation, 340 MB: 65 us, 5.2 TB/s.
+// near that: 8,190 tokens of 64 + 2 * 8 heads of 128, fp16, norm and rotation, 340 MB: 63 us, 5.4 TB/s.
 // An 8- or 4-bit cache is bound by instructions (two conversions a computed value, the products
 // rounded to odd of the others): 4,095 tokens of 16 + 2 * 2 heads of 256, bf16 into e4m3, 81 MB:
-// 31 us, 2.6 TB/s, 0.63 warp instructions issued per cycle and scheduler, 50 % of the ALU pipe.  A decode
+// 32.5 us, 2.5 TB/s, 0.63 warp instructions issued per cycle and scheduler, 50 % of the ALU pipe.  A decode
 // step's call is latency: 3.5 us (4.8 us a replayed graph of one call).
 #include <type_traits>
 
@@ -38,6 +40,8 @@ struct AppendParams {
   pkd_append_args a;
   int64_t token0;     // first token of this launch
   uint32_t items;     // (token, chunk of heads) pairs of this launch, a warp each
+  uint32_t warps;     // warps of this launch; warp i takes items i, i + warps, ...
+  uint32_t parallel;  // 16-bit caches: tokens that lie between a warp's items
   uint32_t chunks;    // chunks of a token: qc of q, kc of k, kc of v
   int qc, kc;
   int page_log;
@@ -376,14 +380,24 @@ struct Item {
     const int64_t st = kind == 0 ? a.q_strides[0] : kind == 1 ? a.k_strides[0] : a.v_strides[0];
     return static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + t * st;
   }
-  __device__ __forceinline__ void load(const AppendParams& p, uint32_t item, int lane) {
+  __device__ __forceinline__ const void* weight(const pkd_append_args& a) const {
+    return kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+  }
+  __device__ __forceinline__ void weights(const pkd_append_args& a, int lane, float (&wv)[2][8]) const {
+    if (!weight(a)) return;
+    const Place pl = place(a, lane);
+    load_weight8<T>(weight(a), a.weight_f32, pl.d[0], wv[0]);
+    load_weight8<T>(weight(a), a.weight_f32, pl.d[1], wv[1]);
+  }
+  __device__ __forceinline__ void aim(const AppendParams& p, int c) {
     constexpr int GROUPS = 32 / (D / 16);
-    const pkd_append_args& a = p.a;
-    const uint32_t tok = item / p.chunks;
-    const int c = (int)(item - tok * p.chunks);
-    t = p.token0 + tok;
     kind = c < p.qc ? 0 : c < p.qc + p.kc ? 1 : 2;
     first = (c - (kind == 0 ? 0 : kind == 1 ? p.qc : p.qc + p.kc)) * R * GROUPS;
+  }
+  __device__ __forceinline__ void load(const AppendParams& p, uint32_t token, int lane) {
+    constexpr int GROUPS = 32 / (D / 16);
+    const pkd_append_args& a = p.a;
+    t = p.token0 + token;
     b = __ldg(a.batch_indices + t);
     pos = __ldg(a.positions + t);
     rpos = a.rotary_dim && a.rope_positions ? __ldg(a.rope_positions + t) : pos;
@@ -402,7 +416,8 @@ struct Item {
 };
 
 template <typename T, int KV, int D, int R>
-__device__ __forceinline__ void append_item(const AppendParams& p, const Item<T, D, R>& it, int lane) {
+__device__ __forceinline__ void append_item(const AppendParams& p, const Item<T, D, R>& it,
+                                            float (&wv)[2][8], int lane) {
   constexpr int LANES = D / 16, GROUPS = 32 / LANES;
   const pkd_append_args& a = p.a;
   const int kind = it.kind, first = it.first, heads = it.heads(a), rotary = a.rotary_dim, rpos = it.rpos;
@@ -410,12 +425,8 @@ __device__ __forceinline__ void append_item(const AppendParams& p, const Item<T,
   const int h0 = first + lane / LANES;
   const Place pl = it.place(a, lane);
   const uint4 (&raw)[R][2] = it.raw;
-  const void* w = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
-  float wv[2][8];
-  if (w) {
-    load_weight8<T>(w, a.weight_f32, pl.d[0], wv[0]);
-    load_weight8<T>(w, a.weight_f32, pl.d[1], wv[1]);
-  }
+  const void* w = it.weight(a);
+  if (KV != kSame16) it.weights(a, lane, wv);
   // cosines and sines: of the lane's eight pairs (piece 0 with piece 1), or of the four of each piece
   const bool turnable = !rotary || (rpos >= 0 && rpos < a.cos_sin_rows);
   const float* cs_row = rotary && turnable ? a.cos_sin + (int64_t)rpos * rotary : nullptr;
@@ -600,18 +611,32 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kernel(const __grid_co
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // whole warps, the next item's rows under way while the current one is worked on
+  constexpr bool KEEP = KV == kSame16;
   const int lane = threadIdx.x & 31;
-  const uint32_t stride = gridDim.x * (kThreads / 32);
   uint32_t item = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  if (item >= p.items) return;
+  if (item >= p.warps) return;
   Item<T, D, R> it, next;
-  it.load(p, item, lane);
+  uint32_t token = item / p.chunks;
+  it.aim(p, (int)(item - token * p.chunks));
+  it.load(p, token, lane);
+  float wv[2][8];
+  if (KEEP) it.weights(p.a, lane, wv);
   while (true) {
-    const bool more = item + stride < p.items && item + stride > item;
-    if (more) next.load(p, item + stride, lane);
-    append_item<T, KV, D, R>(p, it, lane);
+    const bool more = item + p.warps < p.items && item + p.warps > item;
+    item += p.warps;
+    next.kind = it.kind;
+    next.first = it.first;
+    if (more) {
+      if (KEEP) {
+        token += p.parallel;
+      } else {
+        token = item / p.chunks;
+        next.aim(p, (int)(item - token * p.chunks));
+      }
+      next.load(p, token, lane);
+    }
+    append_item<T, KV, D, R>(p, it, wv, lane);
     if (!more) break;
-    item += stride;
     it = next;
   }
 }
@@ -633,10 +658,12 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
     const int64_t n = a.num_tokens - t0 < slab ? a.num_tokens - t0 : slab;
     p.token0 = t0;
     p.items = (uint32_t)(n * p.chunks);
-    // as many CTAs as fit at once, and no more than there is work for
-    const unsigned need = (p.items + kThreads / 32 - 1) / (kThreads / 32);
-    const unsigned room = 152u * kCtas;
-    const unsigned grid = need < room ? need : room;
+    // as many warps as fit at once, and no more than there are items
+    uint32_t room = 152u * kCtas * (kThreads / 32);
+    if (KV == kSame16) room = (room < p.chunks ? 1 : room / p.chunks) * p.chunks;
+    p.warps = p.items < room ? p.items : room;
+    p.parallel = p.warps / p.chunks;
+    const unsigned grid = (p.warps + kThreads / 32 - 1) / (kThreads / 32);
     cudaError_t e = launch_pdl(append_kernel<T, KV, D, R>, p, grid, kThreads, s);
     if (e != cudaSuccess) return e;
   }
@@ -645,12 +672,12 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
 
 template <typename T, int KV, int D>
 cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
-  // Heads a group takes of a 16-bit cache's call: one while the call leaves SMs idle, two once there
-  // is work for every SM several times over, which keeps more bytes under way.  Replayed graphs with
-  // one and with two: one token of 32 + 2 * 8 heads of 128 4.8 and 5.5 us, 340 MB of prompts 85.8 and
-  // 67.3 us.  Rows that become codes take the registers that a second head would: always one.
+  // Heads a group takes: one while the call leaves SMs idle, two once there is work for every SM
+  // several times over, which keeps more bytes under way.  Replayed graphs with one and with two: one
+  // token of 32 + 2 * 8 heads of 128 4.8 and 5.5 us, 340 MB of prompts 83 and 66 us, the chunk into
+  // e4m3 36.3 and 36.0 us, the same into 4 bits (with its gather) 60.4 and 56.0 us.
   const int64_t rows = a.num_tokens * (a.num_qo_heads + 2 * (int64_t)a.pool.num_kv_heads);
-  if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, KV == kSame16 ? 2 : 1>(a, s);
+  if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, 2>(a, s);
   return launch_r<T, KV, D, 1>(a, s);
 }
 
