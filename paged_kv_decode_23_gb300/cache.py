@@ -274,24 +274,25 @@ def copy_pages(pools, src_pages, dst_pages, stream=None) -> None:
         raise ValueError("src_pages and dst_pages must be lists of one length")
     if not len(pools):
         return
-    if any(t.dim() < 1 for t in pools):
-        raise ValueError("every pool must have its pages on axis 0")
-    dev, pages = pools[0].get_device(), pools[0].shape[0]
-    bases, strides, sizes = array("q"), array("q"), array("q")
-    for i, t in enumerate(pools):
-        if t.get_device() != dev or dev < 0 or t.shape[0] != pages:
-            raise ValueError(f"pools[{i}] must hold {pages} pages on axis 0, on one CUDA device")
-        size = t.element_size()
-        stride = t.stride(0) * size
-        if t.is_contiguous():
-            page = stride if pages > 1 else t.numel() * size
-        else:
-            if pages > 0 and not t[0].is_contiguous():
-                raise ValueError(f"pools[{i}]: a page must be one contiguous block")
-            page = t.numel() // max(1, pages) * size
-        bases.append(t.data_ptr())
-        strides.append(stride if pages > 1 else page)
-        sizes.append(page)
+    try:
+        dev, pages = pools[0].get_device(), pools[0].shape[0]
+        bases, strides, sizes = [], [], []
+        for t in pools:
+            if t.get_device() != dev or dev < 0 or t.shape[0] != pages:
+                raise ValueError(f"every pool must hold {pages} pages on axis 0, on one CUDA device")
+            if t.is_contiguous():
+                page = stride = t.nbytes // (pages or 1)
+            else:
+                if pages > 0 and not t[0].is_contiguous():
+                    raise ValueError("a page of a pool must be one contiguous block")
+                page = t.nbytes // (pages or 1)
+                stride = t.stride(0) * t.element_size() if pages > 1 else page
+            bases.append(t.data_ptr())
+            strides.append(stride)
+            sizes.append(page)
+    except IndexError:
+        raise ValueError("every pool must have its pages on axis 0") from None
+    bases, strides, sizes = array("q", bases), array("q", strides), array("q", sizes)
     _launch(L.lib().pkd_copy_pages, dev, stream, bases.buffer_info()[0], strides.buffer_info()[0],
             sizes.buffer_info()[0], len(sizes), pages, sp, dp, n)
 
