@@ -136,7 +136,8 @@ __device__ __forceinline__ uint32_t e2m1_off(int r, int c) {
 }
 
 // A stage holds its boxes one after the other, each as `br` K rows and then br V rows (a box is a
-// page, or a piece of a page of SLICE tokens, so that slices lie at a fixed distance).  Row of token j's K; its V is br rows further.
+// page, or a piece of a page of SLICE tokens, so that slices lie at a fixed distance).  Row of token
+// j's K; its V is br rows further.
 __device__ __forceinline__ int e2m1_row(int j, int br) { return j + (j & -br); }
 
 // Token (within 16) of row j of S^T.  Rows of 64 and 32 bytes: in order.  Rows of 128 bytes: the
