@@ -106,6 +106,8 @@ class PkdError(RuntimeError):
 def lib():
     """The loaded library; raises if it is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -17,8 +17,8 @@ import numpy as np
 import torch
 
 from . import _lib as L
-from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, _host_i32, new_output, pool_views,
-                     raw_stream)
+from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, _host_i32, current_device, new_output,
+                     pool_views, raw_stream)
 
 _POOL = "4Pq3q3q2Pq5i2fi"  # pkd_paged_pool
 _APPEND = struct.Struct("@" + _POOL + "4P8q3P2PPqPqd6i")  # pkd_append_args
@@ -100,7 +100,7 @@ def _launch(call, dev: int, stream, *args) -> None:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
     else:
         s = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if current_device() == dev:
         rc = call(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -204,9 +204,10 @@ def append_paged_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opt
 
 def _weight(w, name: str, dtype, dev: int, d: int):
     """(address, whether it is float32) of a norm's weights."""
-    if w.shape != (d,) or w.dtype not in (dtype, torch.float32) or w.get_device() != dev or w.stride(0) != 1:
+    f32 = w.dtype is not dtype
+    if f32 and w.dtype is not torch.float32 or w.shape != (d,) or w.get_device() != dev or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{d}] tensor of {dtype} or float32 on cuda:{dev}")
-    return w.data_ptr(), int(w.dtype is torch.float32)
+    return w.data_ptr(), 1 if f32 else 0
 
 
 def gather_paged_kv(batch_indices: torch.Tensor, positions: torch.Tensor, paged_kv_cache,

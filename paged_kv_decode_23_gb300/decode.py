@@ -85,6 +85,8 @@ _SCALED_RUN = struct.Struct("@5Pq3q3q4P3fi")  # pkd_scaled_run
 # time of building a Stream object for it; where torch has none, the object does.
 raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# Likewise the current device's index (CUDA is initialised wherever a tensor lies on a device).
+current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
@@ -344,7 +346,7 @@ class BatchDecodePagedKV:
         a = self._plan_args
         rows, hq, d, ps, hkv = a["rows"], a["num_qo_heads"], a["head_dim"], a["page_size"], a["num_kv_heads"]
         dev = q.get_device()
-        if torch.cuda.current_device() != dev >= 0:
+        if dev >= 0 and current_device() != dev:
             with torch.cuda.device(dev):
                 return self._run_scaled(q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse,
                                         stream, timing_events, enable_pdl)
