@@ -487,3 +487,44 @@ def test_copy_pages_in_a_graph_and_on_a_stream():
     copy_pages(pool, [0], [5], stream=side)
     torch.cuda.synchronize()
     assert torch.equal(pool[5], pool[0])
+
+
+def test_appends_and_copies_queued_on_two_streams_and_in_two_graphs():
+    """Two captured steps over pools of their own, replayed on two streams at once: nothing is shared."""
+    from paged_kv_decode_23_gb300 import append_paged_kv, copy_pages, gather_paged_kv
+    sides = []
+    for i, kv in enumerate(("e4m3", "e2m1")):
+        pg = Pages([500, 300], 16, 2, 128, kv, "HND", seed=30 + i)
+        q, k, v = _qkv(800, 4, 2, 128, BF16, seed=40 + i)
+        b, pos = _idx([0] * 500 + [1] * 300), _idx(list(range(500)) + list(range(300)))
+        pools = [pg.pool] + ([pg.scales] if pg.scales is not None else [])
+        src, dst = pg.host_indices[:2].copy(), np.setdiff1d(np.arange(pg.num_pages), pg.host_indices)[:2]
+        sides.append((pg, q, k, v, b, pos, pools, src, dst, torch.cuda.Stream()))
+
+    def step(side):
+        pg, q, k, v, b, pos, pools, src, dst, _ = side
+        kw = dict(kv_indptr=pg.indptr, kv_indices=pg.indices, kv_layout=pg.layout, kv_block_scales=pg.scales)
+        out = append_paged_kv(q, k, v, b, pos, pg.pool, **kw)
+        copy_pages(pools, src, dst)
+        return (out,) + gather_paged_kv(b, pos, pg.pool, **kw)
+    want = [[t.clone() for t in step(s)] for s in sides]
+    torch.cuda.synchronize()
+    graphs = []
+    for s in sides:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step(s)
+        graphs.append((g, got))
+    for s in sides:
+        s[6][0].view(torch.uint8).zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, (g, _) in zip(sides, graphs):
+            with torch.cuda.stream(s[9]):
+                g.replay()
+    torch.cuda.synchronize()
+    for s, (_, got), w in zip(sides, graphs, want):
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
+        for t in s[6]:
+            raw = t.view(torch.uint8)
+            assert torch.equal(raw[torch.from_numpy(s[8]).long()], raw[torch.from_numpy(s[7]).long()])

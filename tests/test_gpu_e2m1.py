@@ -99,6 +99,16 @@ def test_decode_several_queries_a_sequence(q_len):
     assert_decode(pg, q, o, lse, 16, q_len=q_len)
 
 
+def test_batches_of_nothing():
+    """No sequence at all, and sequences without tokens: o = 0, lse = -inf."""
+    pg = Pages([], 16, 2, 128, "e2m1", "NHD")
+    o, lse = _dec(pg, 8, BF16).run(_q(0, 8, 128, BF16), pg.pool, kv_block_scales=pg.scales, return_lse=True)
+    assert o.shape == (0, 8, 128) and lse.shape == (0, 8)
+    pg = Pages([0, 0, 0], 16, 2, 128, "e2m1", "NHD")
+    o, lse = _dec(pg, 8, BF16).run(_q(3, 8, 128, BF16), pg.pool, kv_block_scales=pg.scales, return_lse=True)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
 def test_unattended_slots_hold_anything():
     """NaN scales and any codes behind the last token, before the window and in foreign pages."""
     lens, window = [50, 9, 200, 16], 70
