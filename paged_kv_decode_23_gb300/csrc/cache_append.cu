@@ -19,7 +19,8 @@
 // and that to the code.  Ties are common there, one value in eight with a scale of few bits.  A
 // computed value's quotient t has an error bound e: where the codes of t - e and t + e agree (all
 // but about one value in 1e5) that is the code, else that value is computed once more in 64 bits;
-// where it is a block's scale that is in doubt, the warp's rows are.
+// so are the largest values of a block whose scale is in doubt.  (The 64-bit pipe is far too slow for
+// whole rows.)
 //
 // Bound: every input byte is read once and every output byte written once.  A 16-bit cache comes
 // near that: 8,190 tokens of 64 + 2 * 8 heads of 128, fp16, norm and rotation, 340 MB: 63 us, 5.4 TB/s.
@@ -186,104 +187,15 @@ __device__ __noinline__ float exact_quotient(const T* src, const void* weight, i
   return to_odd(x / ((double)m * unit));
 }
 
-// The codes of a computed key row, in 64 bits throughout.  Called by whole warps.
-template <typename T, int KV, int D>
-__device__ __noinline__ Codes exact_codes(const T* src, const void* weight, int weight_f32,
-                                          const float* cs, int rotary, int interleaved, double eps,
-                                          float unit) {
-  constexpr int LANES = D / 16;
-  const Place pl = place_of<D>(threadIdx.x & 31, rotary, interleaved);
-  double x[2][8];
-  double ss = 0.0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float xf[8];
-    unpack8<T>(*reinterpret_cast<const uint4*>(src + pl.d[i]), xf);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[i][e] = xf[e];
-      ss += x[i][e] * x[i][e];
-    }
-  }
-#pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-  if (weight != nullptr) {
-    const double r = 1.0 / sqrt(ss / D + eps);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float w[8];
-      load_weight8<T>(weight, weight_f32, pl.d[i], w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * r * w[e];
-    }
-  }
-  if (pl.turned) {
-    const int half = rotary / 2;
-    if (pl.split) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double c = cs[pl.d[0] + e], s = cs[half + pl.d[0] + e];
-        const double u = x[0][e], v = x[1][e];
-        x[0][e] = u * c - v * s;
-        x[1][e] = v * c + u * s;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const double c = cs[pl.d[i] / 2 + e], s = cs[half + pl.d[i] / 2 + e];
-          const double u = x[i][2 * e], v = x[i][2 * e + 1];
-          x[i][2 * e] = u * c - v * s;
-          x[i][2 * e + 1] = v * c + u * s;
-        }
-    }
-  }
-  Codes out;
-  double by[2] = {unit, unit};
-  if constexpr (KV == kFp4) {
-    double top[2] = {0.0, 0.0};
-    bool nan[2] = {false, false};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        top[i] = fmax(top[i], fabs(x[i][e]));
-        nan[i] |= x[i][e] != x[i][e];
-      }
-    double both[2];
-    bool any[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const double t0 = __shfl_sync(~0u, top[0], pl.lane[i]), t1 = __shfl_sync(~0u, top[1], pl.lane[i]);
-      const int n0 = __shfl_sync(~0u, (int)nan[0], pl.lane[i]), n1 = __shfl_sync(~0u, (int)nan[1], pl.lane[i]);
-      both[i] = fmax(top[i], pl.piece[i] ? t1 : t0);
-      any[i] = nan[i] || (pl.piece[i] ? n1 : n0);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float t = to_odd(both[i] / (6.0 * unit));
-      out.scale[i] = any[i] ? 0x7fu : codes2<kFp8>(t, t) & 0xffu;
-      by[i] = (double)e4m3_value(out.scale[i]) * unit;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float t[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = by[i] > 0.0 ? to_odd(x[i][e] / by[i]) : 0.f;  // a block of zeros: codes 0
-    out.c[i] = codes8<KV>(t);
-  }
-  return out;
-}
-
 // The codes of a row from its values y in 32 bits, each with the sum `err` of the terms it was
-// computed from (unused where `exact`); inv about 1 / unit.  Whole warps, whose lanes may differ in
-// `exact`; *doubt: some code is in doubt (alt differs from c), *scale_doubt: a block's scale is.
-template <int KV>
+// computed from (unused where `exact`); inv about 1 / unit.  exact_at(rn, i, e, m): value e of piece
+// i over m * unit, to odd, given rn = exact_norm().  Whole warps, whose lanes may differ in `exact`;
+// *doubt: some code is in doubt (alt differs from c).
+template <int KV, class Norm, class At>
 __device__ __forceinline__ Codes quick_codes(const Place& pl, const float (&y)[2][8],
                                              const float (&err)[2][8], bool exact, bool all_exact,
-                                             float unit, float inv, bool* doubt, bool* scale_doubt) {
+                                             float unit, float inv, bool live, Norm exact_norm,
+                                             At exact_at, bool* doubt) {
   Codes out;
   float d[2] = {unit, unit}, dl[2] = {0.f, 0.f}, inv2[2] = {inv, inv};  // divisors, what their rounding left
   if constexpr (KV == kFp4) {
@@ -311,6 +223,7 @@ __device__ __forceinline__ Codes quick_codes(const Place& pl, const float (&y)[2
         off[i] = fmaxf(mine[i], pl.piece[i] ? t1 : t0);
       }
     }
+    bool unsure[2] = {false, false};
     const float six = 6.f * unit, six_l = fmaf(6.f, unit, -six), sixth = inv * 0.16666667f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -322,8 +235,31 @@ __device__ __forceinline__ Codes quick_codes(const Place& pl, const float (&y)[2
         const float t = a * sixth, e = off[i] * sixth * (kValueErr + kQuotErr);
         const uint32_t c = codes2<kFp8>(t - e, t + e);
         out.scale[i] = c & 0xffu;
-        *scale_doubt |= out.scale[i] != c >> 8;
+        unsure[i] = out.scale[i] != c >> 8;
       }
+    }
+    if (!all_exact && __any_sync(~0u, (unsure[0] || unsure[1]) && live)) {
+      // the scale again, from the exact values of those that can be the block's largest
+      const double rn = exact_norm();
+      float best[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t which = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          which |= (uint32_t) !(fabsf(y[i][e]) + 2.f * off[i] * kValueErr < __uint_as_float(both[i])) << e;
+        if (!unsure[i] || !live) which = 0;
+        for (; which; which &= which - 1) best[i] = fmaxf(best[i], fabsf(exact_at(rn, i, __ffs(which) - 1, 6.f)));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float t0 = __shfl_sync(~0u, best[0], pl.lane[i]), t1 = __shfl_sync(~0u, best[1], pl.lane[i]);
+        const float t = fmaxf(best[i], pl.piece[i] ? t1 : t0);
+        if (unsure[i]) out.scale[i] = codes2<kFp8>(t, t) & 0xffu;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
       if (both[i] > 0x7f800000u) out.scale[i] = 0x7fu;
       const float m = e4m3_value(out.scale[i]);
       // (a block of zeros, or a NaN's, gets codes 0 by a zero in place of 1 / 0)
@@ -561,15 +497,15 @@ __device__ __forceinline__ void append_item(const AppendParams& p, const Item<T,
       }
     } else {
       const bool exact = kind == 2 || (!w && !pl.turned);
-      bool doubt = false, scale_doubt = false;
-      Codes cd = quick_codes<KV>(pl, y, err, exact, kind == 2, unit, inv, &doubt, &scale_doubt);
-      if (KV == kFp4 && __any_sync(~0u, scale_doubt && live)) {
-        // (a group without a head goes along on the warp's first one)
-        const Codes e = exact_codes<T, KV, D>(it.row0(a) + (live ? h : first) * it.step(a), w, a.weight_f32, cs_row,
-                                              rotary, a.interleaved, a.eps, unit);
-        if (!exact) cd = e;
-      } else if (__any_sync(~0u, doubt && live)) {
-        const double rn = w ? exact_rnorm<T, D>(raw[j], a.eps) : 1.0;
+      bool doubt = false;
+      auto exact_norm = [&] { return w ? exact_rnorm<T, D>(raw[j], a.eps) : 1.0; };
+      auto exact_at = [&](double rn, int i, int e, float m) {
+        return exact_quotient<T>(it.row0(a) + h * it.step(a), w, a.weight_f32, cs_row, rotary, a.interleaved, rn,
+                                 pl.d[i] + e, m, unit);
+      };
+      Codes cd = quick_codes<KV>(pl, y, err, exact, kind == 2, unit, inv, live, exact_norm, exact_at, &doubt);
+      if (__any_sync(~0u, doubt && live)) {
+        const double rn = exact_norm();
         if (live) {
           constexpr int kBits = KV == kFp8 ? 8 : 4;
 #pragma unroll
@@ -580,8 +516,7 @@ __device__ __forceinline__ void append_item(const AppendParams& p, const Item<T,
             while (diff) {  // (one value, as a rule)
               const int e = (__ffsll(diff) - 1) / kBits;
               const uint64_t field = ((uint64_t(1) << kBits) - 1) << (e * kBits);
-              const float x = exact_quotient<T>(it.row0(a) + h * it.step(a), w, a.weight_f32, cs_row, rotary,
-                                                a.interleaved, rn, pl.d[i] + e, m, unit);
+              const float x = exact_at(rn, i, e, m);
               code = (code & ~field) | ((uint64_t)codes2<KV>(x, x) << (e * kBits) & field);
               diff &= ~field;
             }
