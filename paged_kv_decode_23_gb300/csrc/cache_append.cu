@@ -229,7 +229,7 @@ __device__ __forceinline__ Codes quick_codes(const Place& pl, const float (&y)[2
     for (int i = 0; i < 2; ++i) {
       const float a = __uint_as_float(both[i]);
       if (exact) {
-        const float t = odd_quotient(a, six, six_l, sixth);
+        const float t = odd_quotients(a, a, six, six_l, sixth).x;
         out.scale[i] = codes2<kFp8>(t, t) & 0xffu;
       } else {
         const float t = a * sixth, e = off[i] * sixth * (kValueErr + kQuotErr);
@@ -273,17 +273,25 @@ __device__ __forceinline__ Codes quick_codes(const Place& pl, const float (&y)[2
     if (exact) {
       float t[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = odd_quotient(y[i][e], d[i], dl[i], inv2[i]);
+      for (int e = 0; e < 8; e += 2) {
+        const float2 q = odd_quotients(y[i][e], y[i][e + 1], d[i], dl[i], inv2[i]);
+        t[e] = q.x;
+        t[e + 1] = q.y;
+      }
       out.c[i] = out.alt[i] = codes8<KV>(t);
     } else {
       float lo[8], hi[8];
       const float k = inv2[i] * (kValueErr + kQuotErr);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 8; e += 2) {
         // (+ 0: a negative zero, from a zero head and a negative weight, is no doubt)
-        const float t = fmaf(y[i][e], inv2[i], 0.f), off = err[i][e] * k;
-        lo[e] = t - off;
-        hi[e] = t + off;
+        const float2 t = __ffma2_rn(make_float2(y[i][e], y[i][e + 1]), make_float2(inv2[i], inv2[i]), make_float2(0.f, 0.f));
+        const float2 off = make_float2(err[i][e], err[i][e + 1]);
+        const float2 l = __ffma2_rn(off, make_float2(-k, -k), t), h = __ffma2_rn(off, make_float2(k, k), t);
+        lo[e] = l.x;
+        lo[e + 1] = l.y;
+        hi[e] = h.x;
+        hi[e + 1] = h.y;
       }
       out.c[i] = codes8<KV>(lo);
       out.alt[i] = codes8<KV>(hi);
@@ -610,7 +618,7 @@ cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
   // Heads a group takes: one while the call leaves SMs idle, two once there is work for every SM
   // several times over, which keeps more bytes under way.  Replayed graphs with one and with two: one
   // token of 32 + 2 * 8 heads of 128 4.8 and 5.5 us, 340 MB of prompts 83 and 66 us, the chunk into
-  // e4m3 36.3 and 36.0 us, the same into 4 bits (with its gather) 60.4 and 56.0 us.
+  // e4m3 36.3 and 36.0 us, twice its tokens into 4 bits (and read back) 90.3 and 88.9 us.
   const int64_t rows = a.num_tokens * (a.num_qo_heads + 2 * (int64_t)a.pool.num_kv_heads);
   if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, 2>(a, s);
   return launch_r<T, KV, D, 1>(a, s);

@@ -120,21 +120,28 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // a / (d + dl) rounded to odd, so that one more rounding to a type of few bits is that of the exact
-// quotient: a finite, d + dl the exact divisor as a float and the rest it leaves, inv about 1 / d.
+// quotient, for two values: d + dl the exact divisor as a float and the rest it leaves, inv about 1 / d.
 // One Newton step makes t faithful; the remainder then keeps its sign through its two FMAs.
-__device__ __forceinline__ float odd_quotient(float a, float d, float dl, float inv) {
-  const float x = fabsf(a);
-  float t = x * inv;
-  float r = fmaf(-t, dl, fmaf(-t, d, x));
-  t = fmaf(r, inv, t);
-  r = fmaf(-t, dl, fmaf(-t, d, x));
-  uint32_t bits = __float_as_uint(t);
-  if (r < 0.f) --bits;  // truncated ...
-  if (r != 0.f) bits |= 1u;  // ... with what was cut off kept in the last bit
-  // (beyond the range of any code nothing is left to decide; a NaN or an infinity stays one)
-  if (!(x * inv < 1e30f)) bits = __float_as_uint(x * inv);
-  if (x == 0.f) bits = 0u;
-  return __uint_as_float(bits | (__float_as_uint(a) & 0x80000000u));
+__device__ __forceinline__ float2 odd_quotients(float a, float b, float d, float dl, float inv) {
+  // (what passes 2^20 has no code left to decide on; min.NaN keeps a NaN, and an infinity out)
+  auto clamp = [&](float v) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(v)), "f"(d * 0x1p20f));
+    return r;
+  };
+  const float2 x = make_float2(clamp(a), clamp(b)), by = make_float2(inv, inv);
+  const float2 nd = make_float2(-d, -d), ndl = make_float2(-dl, -dl);
+  float2 t = __fmul2_rn(x, by);
+  float2 r = __ffma2_rn(t, ndl, __ffma2_rn(t, nd, x));
+  t = __ffma2_rn(r, by, t);
+  r = __ffma2_rn(t, ndl, __ffma2_rn(t, nd, x));
+  // truncated (one unit less where t is above the quotient), with what was cut off kept in the last bit
+  auto odd = [](float t, float r, float sign) {
+    uint32_t bits = __float_as_uint(t) + (uint32_t)(__float_as_int(r) >> 31);
+    if (r != 0.f) bits |= 1u;
+    return __uint_as_float(bits | (__float_as_uint(sign) & 0x80000000u));
+  };
+  return make_float2(odd(t.x, r.x, a), odd(t.y, r.y, b));
 }
 
 }  // namespace rows

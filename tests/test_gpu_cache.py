@@ -153,6 +153,22 @@ def test_append_codes_of_many_values_are_exact(kv):
     check_append(pg, q, v.clone(), v, np.zeros(n, int), np.arange(n), cos_sin=_table(n, 32), k_scale=1.0, v_scale=1.0)
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("scale", [1 / 17, 1 / 19, 1 / 7, 1 / 5, 1 / 3, 0.1, 1 / 27])
+def test_append_codes_next_to_borders(kv, scale):
+    """Values of few bits over scales whose rounding puts the quotient within 2^-24 of a border
+    between two codes, on either side: 1 / float32(1 / 17) against 17, and the like."""
+    n, hkv, d = 400, 4, 128
+    pg = Pages([n], 16, hkv, d, kv, "NHD", seed=5)
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (((torch.randint(-15, 16, (n, h, d), generator=g) * 2.0 ** torch.randint(-3, 4, (n, h, 1), generator=g))
+                .to(BF16).cuda()) for h in (2, hkv, hkv))
+    check_append(pg, q, k, v, np.zeros(n, int), np.arange(n), k_scale=scale, v_scale=scale)
+    # the same values of k through the computed path
+    check_append(pg, q, k, v, np.zeros(n, int), np.arange(n), cos_sin=_table(n, d), rope_positions=np.zeros(n, int),
+                 k_scale=scale, v_scale=scale)
+
+
 @pytest.mark.parametrize("kv", ["same", "e4m3", "e2m1"])
 def test_append_special_values(kv):
     """Zeros, the type's extremes, subnormals, infinities and NaNs stay in their own rows."""
