@@ -26,7 +26,7 @@
 // near that: 8,190 tokens of 64 + 2 * 8 heads of 128, fp16, norm and rotation, 340 MB: 63 us, 5.4 TB/s.
 // An 8- or 4-bit cache is bound by instructions (two conversions a computed value, the products
 // rounded to odd of the others): 4,095 tokens of 16 + 2 * 2 heads of 256, bf16 into e4m3, 81 MB:
-// 33 us, 2.5 TB/s, 0.54 warp instructions issued per cycle and scheduler, 46 % of the ALU pipe.  A decode
+// 33 us, 2.5 TB/s, 0.53 warp instructions issued per cycle and scheduler, 44 % of the ALU pipe.  A decode
 // step's call is latency: 3.5 us (4.8 us a replayed graph of one call).
 #include <type_traits>
 
