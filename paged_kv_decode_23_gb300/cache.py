@@ -134,8 +134,9 @@ def append_paged_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opt
     (i, i + rotary_dim / 2), or (2i, 2i + 1) if ``interleaved``, at ``rope_positions`` (default:
     ``positions``).
 
-    ``paged_kv_cache`` (5-D, or a (k, v) pair) holds the rows' type, float8_e4m3fn (k / k_scale,
-    v / v_scale), or 4-bit codes with ``kv_block_scales`` as ``BatchDecodePagedKV.run`` reads them.
+    ``paged_kv_cache`` (5-D, or a (k, v) pair) receives k / k_scale and v / v_scale in the rows' type
+    or float8_e4m3fn, rounded once, or as 4-bit codes with ``kv_block_scales`` as
+    ``BatchDecodePagedKV.run`` reads them.
     Returns q's rows (``out``, which may be ``q``; a fresh tensor's padding rows are undefined), or
     None without q.  ``q`` may be None, or ``k`` and ``v`` with the cache and page table.
 

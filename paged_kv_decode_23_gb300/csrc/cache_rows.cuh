@@ -112,6 +112,19 @@ __device__ __forceinline__ float to_odd(double x) {
              : f;
 }
 
+// a / d rounded to odd (as to_odd), for any a and normal d in [2^-64, 2^64].  The remainder of a
+// correctly rounded quotient is a float; small values are scaled so that it stays in range.
+__device__ __forceinline__ float odd_quotient(float a, float d) {
+  const float q = __fdiv_rn(a, d), z = fabsf(a) < 1.f ? 0x1p64f : 1.f;
+  const float r = fmaf(-(q * z), d, a * z);
+  uint32_t bits = __float_as_uint(q);
+  if (fabsf(q) < __int_as_float(0x7f800000) && r != 0.f) {  // truncated, the last bit set
+    bits -= (__float_as_uint(r) ^ __float_as_uint(a)) >> 31;
+    bits |= 1u;
+  }
+  return __uint_as_float(bits);
+}
+
 // 1 / x within one unit in the last place, for normal x.
 __device__ __forceinline__ float rcp(float x) {
   float r;

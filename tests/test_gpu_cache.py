@@ -544,3 +544,84 @@ def test_appends_and_copies_queued_on_two_streams_and_in_two_graphs():
         for t in s[6]:
             raw = t.view(torch.uint8)
             assert torch.equal(raw[torch.from_numpy(s[8]).long()], raw[torch.from_numpy(s[7]).long()])
+
+
+# ------------------------------------------------------------------------------ scales of a 16-bit cache
+def nearest16(x, dtype):
+    """fp64 x rounded once to dtype (ties to even), as fp64; exact where x is within 2^-48 of its true
+    value and that is no closer to a border."""
+    fi = torch.finfo(dtype)
+    bits = {BF16: 8, F16: 11}[dtype]
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(invalid="ignore", over="ignore"):
+        e = np.maximum(np.frexp(np.where(np.isfinite(x), x, 1.0))[1], np.frexp(fi.tiny)[1])
+        step = np.ldexp(1.0, e - bits)
+        r = np.rint(x / step) * step
+        return np.where(np.abs(r) > fi.max, np.copysign(np.inf, x), r)
+
+
+@pytest.mark.parametrize("dtype,layout,d", [(BF16, "NHD", 128), (F16, "HND", 64), (BF16, "HND", 256), (F16, "NHD", 128)])
+@pytest.mark.parametrize("scales", [(0.5, 4.0), (0.3, 2.7), (1 / 17, 1 / 3)])
+def test_append_divides_into_a_16_bit_cache(dtype, layout, d, scales):
+    """A 16-bit cache holds k / k_scale and v / v_scale: copied values rounded once from the exact
+    quotient, computed ones within their 32-bit error; gather and decode multiply them back."""
+    from paged_kv_decode_23_gb300 import BatchDecodePagedKV, append_paged_kv, gather_paged_kv
+    n, hq, hkv, page = 45, 4, 2, 16
+    ks, vs = (float(np.float32(s)) for s in scales)
+    q, k, v = _qkv(n, hq, hkv, d, dtype, seed=d)
+    b, pos = [0] * n, np.arange(n)
+    w = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(8))).cuda()
+    table = _table(n, d // 2)
+    pools = []
+    for kw, ref in ((dict(), (_f64(k), None)),
+                    (dict(cos_sin_cache=table), norm_rotate(_f64(k), None, 0, table.cpu().numpy(), pos)),
+                    (dict(k_weight=w, cos_sin_cache=table, interleaved=True),
+                     norm_rotate(_f64(k), _f64(w), 1e-6, table.cpu().numpy(), pos, True))):
+        pg = Pages([n], page, hkv, d, "same", layout, seed=2, dtype=dtype)
+        out = append_paged_kv(q, k, v, _idx(b), _idx(pos), pg.pool, pg.indptr, pg.indices, layout, k_scale=scales[0],
+                              v_scale=scales[1], **kw)
+        kc, vc = (pg.rows(pg.pool, i, b, pos) for i in range(2))
+        assert np.array_equal(_f64(vc), nearest16(_f64(v) / vs, dtype))
+        x, terms = ref
+        if terms is None:
+            assert np.array_equal(_f64(kc), nearest16(x / ks, dtype)) and torch.equal(out, q)
+        else:
+            assert_rounded(kc, x / ks, terms / ks, dtype, "k")
+            flat = slice(d // 2, None)  # dims that are not rotated
+            if "k_weight" not in kw:
+                assert np.array_equal(_f64(kc)[..., flat], nearest16(x[..., flat] / ks, dtype))
+        gk, gv = gather_paged_kv(_idx(b), _idx(pos), pg.pool, pg.indptr, pg.indices, layout, k_scale=scales[0], v_scale=scales[1])
+        # two roundings to the type, one of them of the quotient
+        for got, want, t in ((gk, x, 0 if terms is None else 2.0 ** -20 * terms), (gv, _f64(v), 0)):
+            assert (np.abs(_f64(got) - want) <= 2.01 * half_step(dtype) * np.abs(want) + t + 1e-6).all()
+        pools.append(pg)
+    if scales == (0.5, 4.0):  # powers of two: the same bits as without scales
+        outs = []
+        for ks, vs in ((None, None), scales):
+            pg = pools[0]
+            append_paged_kv(None, k, v, _idx(b), _idx(pos), pg.pool, pg.indptr, pg.indices, layout, k_scale=ks, v_scale=vs)
+            dec = BatchDecodePagedKV(torch.zeros(32 << 20, dtype=torch.uint8, device="cuda"), layout)
+            dec.plan(torch.from_numpy(pg.host_indptr), pg.indices, torch.from_numpy(pg.last), hq, hkv, d, page, q_data_type=dtype)
+            outs.append(dec.run(q[-1:].contiguous(), pg.pool, k_scale=ks, v_scale=vs, return_lse=True))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 1e-9, 1 / 17, 0.999, 3.0, 1e9, 2.0 ** 64])
+def test_append_into_16_bits_over_any_scale(dtype, scale):
+    """Quotients of every magnitude: into the subnormals, past the largest value, and those whose
+    32-bit rounding is a border of the 16-bit type; infinities, NaNs and signed zeros."""
+    from paged_kv_decode_23_gb300 import append_paged_kv
+    n, hkv, d = 300, 2, 64
+    g = torch.Generator().manual_seed(3)
+    raw = torch.randint(-32768, 32768, (2, n, hkv, d), generator=g, dtype=torch.int32).to(torch.int16).view(dtype).cuda()
+    k, v = raw[0], raw[1].clone()
+    # few bits over a scale that rounds a simple fraction: quotients next to borders
+    v[: n // 2] = (torch.randint(-4095, 4096, (n // 2, hkv, d), generator=g) * 2.0 ** -6).to(dtype).cuda()
+    pg = Pages([n], 16, hkv, d, "same", "NHD", seed=2, dtype=dtype)
+    append_paged_kv(None, k, v, _idx([0] * n), _idx(np.arange(n)), pg.pool, pg.indptr, pg.indices, k_scale=scale, v_scale=scale)
+    s = float(np.float32(scale))
+    for i, x in enumerate((k, v)):
+        got, want = _f64(pg.rows(pg.pool, i, [0] * n, np.arange(n))), nearest16(_f64(x) / s, dtype)
+        assert np.array_equal(got, want, equal_nan=True), f"{(got != want).sum()} differ"
+        assert np.array_equal(np.signbit(got[~np.isnan(want)]), np.signbit(want[~np.isnan(want)]))
