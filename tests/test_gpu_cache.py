@@ -625,3 +625,59 @@ def test_append_into_16_bits_over_any_scale(dtype, scale):
         got, want = _f64(pg.rows(pg.pool, i, [0] * n, np.arange(n))), nearest16(_f64(x) / s, dtype)
         assert np.array_equal(got, want, equal_nan=True), f"{(got != want).sum()} differ"
         assert np.array_equal(np.signbit(got[~np.isnan(want)]), np.signbit(want[~np.isnan(want)]))
+
+
+# ------------------------------------------------------------------------------ large calls
+def _large_tokens(lens, n, seed):
+    """n rows over the sequences, each token at most once, with one row in nine padding."""
+    rng = np.random.default_rng(seed)
+    every = np.concatenate([np.stack([np.full(m, i), np.arange(m)], axis=1) for i, m in enumerate(lens)])
+    rows = every[rng.permutation(len(every))[:n]]
+    b, pos = rows[:, 0].copy(), rows[:, 1].copy()
+    b[rng.random(n) < 1 / 9] = -1
+    return b, pos
+
+
+LARGE = {64: (21, 11, 3700, 16), 128: (13, 5, 3400, 32), 256: (7, 3, 3000, 8)}  # hq, hkv, rows, page
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kv", ["same", "e4m3", "e2m1"])
+@pytest.mark.parametrize("dtype,layout,inter", [(BF16, "NHD", False), (F16, "HND", True)])
+def test_append_of_large_calls(dtype, layout, inter, kv, d):
+    """Calls above the size from which groups of lanes take two heads each and warps several items:
+    head counts that leave a warp's last heads empty, padding rows all over."""
+    hq, hkv, n, page = LARGE[d]
+    assert n * (hq + 2 * hkv) * (d // 8) >= 4 * 152 * 2048
+    lens = [1500, 1, 2000, 900]
+    b, pos = _large_tokens(lens, n, seed=d)
+    pg = Pages(lens, page, hkv, d, kv, layout, seed=3, dtype=dtype)
+    q, k, v = _qkv(n, hq, hkv, d, dtype, seed=d)
+    qw, kw = ((1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(i))).cuda() for i in (1, 2))
+    rotary = {64: 64, 128: 96, 256: 64}[d]
+    scales = {} if kv == "same" else dict(k_scale=0.1, v_scale=1.25)
+    check_append(pg, q, k, v, b, pos, qw, kw, cos_sin=_table(2000, rotary), interleaved=inter, **scales)
+    if kv != "same":  # copied and computed values in one row
+        check_append(pg, q, k, v, b, pos, cos_sin=_table(2000, 16), interleaved=inter, **scales)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype,layout", [(BF16, "HND"), (F16, "NHD")])
+def test_append_of_large_calls_over_scales(dtype, layout, d):
+    from paged_kv_decode_23_gb300 import append_paged_kv
+    hq, hkv, n, page = LARGE[d]
+    lens = [1500, 1, 2000, 900]
+    b, pos = _large_tokens(lens, n, seed=d + 1)
+    live = b >= 0
+    pg = Pages(lens, page, hkv, d, "same", layout, seed=3, dtype=dtype)
+    q, k, v = _qkv(n, hq, hkv, d, dtype, seed=d)
+    w = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(1))).cuda()
+    table = _table(2000, 32)
+    out = append_paged_kv(q, k, v, _idx(b), _idx(pos), pg.pool, pg.indptr, pg.indices, layout, q_weight=w, k_weight=w,
+                          cos_sin_cache=table, k_scale=0.3, v_scale=2.7)
+    cs = table.cpu().numpy()
+    (wq, tq), (wk, tk) = (norm_rotate(_f64(x)[live], _f64(w), 1e-6, cs, pos[live]) for x in (q, k))
+    ks, vs = float(np.float32(0.3)), float(np.float32(2.7))
+    assert_rounded(out[torch.from_numpy(live).cuda()], wq, tq, dtype, "q")
+    assert_rounded(pg.rows(pg.pool, 0, b[live], pos[live]), wk / ks, tk / ks, dtype, "k")
+    assert np.array_equal(_f64(pg.rows(pg.pool, 1, b[live], pos[live])), nearest16(_f64(v)[live] / vs, dtype))
