@@ -4,8 +4,11 @@
 // qo heads) on a cache whose K and V hold e2m1 values, two a byte (the first in the low half),
 // with one e4m3 scale per 16 consecutive dims: x[d] = e2m1[d] * scale[d / 16].  Such a product
 // has at most 6 significant bits and lies in [2^-10, 2688], so it is an fp16 value: both MMAs
-// (S^T = K Q^T and O^T += V^T P^T, mma.m16n8k16, fp32 accumulators) take exact operands and the
-// only rounding before the epilogue is P's to fp16 (11 bits).
+// (S^T = K Q^T and O^T += V^T P^T, mma.m16n8k16, fp32 accumulators) take K and V exactly.  What is
+// rounded before the epilogue is P, to fp16: 11 bits, and an absolute 2^-32 of the row's largest weight
+// (P is held 2^kHeadroom above it, so that what lies far below a dominant key still counts in the
+// numerator as it does in the sum, which is taken in 32 bits); and of a bf16 q what lies more than 2^27
+// below its head's largest value (load_q_e2m1).
 //
 // Structure as in decode_kernels.cuh (producer warp, mbarrier ring, consumer warps, split partials
 // merged by the last chunk's CTA), with these differences:
@@ -42,6 +45,10 @@
 #include "decode_kernels.cuh"
 
 namespace pkd {
+
+// log2 of the weight of a row's largest key right after its maximum was taken; with kLazyMax on top of
+// it a weight stays below 2^15, inside fp16.
+constexpr float kHeadroom = 7.f;
 
 // D: head_dim.  HEADS: qo heads of a task, 4 or 8.  SL: 16-token slices a consumer warp takes of each
 // tile.  NW consumer warps and one producer warp; a tile is NW * SL * 16 tokens.
@@ -474,7 +481,7 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
         top[0] = fmaxf(top[0], fmaxf(sc[4 * h], sc[4 * h + 2]));
         top[1] = fmaxf(top[1], fmaxf(sc[4 * h + 1], sc[4 * h + 3]));
       }
-      if (__any_sync(~0u, top[0] > m2[0] + kLazyMax || top[1] > m2[1] + kLazyMax)) {
+      if (__any_sync(~0u, top[0] > m2[0] + (kHeadroom + kLazyMax) || top[1] > m2[1] + (kHeadroom + kLazyMax))) {
         float alpha[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -482,7 +489,7 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
           mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-          const float mnew = fmaxf(m2[j], mx);
+          const float mnew = fmaxf(m2[j], mx - kHeadroom);
           alpha[j] = fast_exp2(m2[j] - mnew);
           lsum[j] *= alpha[j];
           m2[j] = mnew;
@@ -503,8 +510,8 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
       }
 #pragma unroll
       for (int h = 0; h < SL; ++h) {
-        // ---- P^T as B operands next to zeros, in fp16 (p <= 2^kLazyMax; 11 bits, see the
-        // header): set 0 takes S^T rows 2t (and 2t + 8), set 1 rows 2t + 1 (and 2t + 9)
+        // ---- P^T as B operands next to zeros, in fp16 (p <= 2^15, see kHeadroom): set 0 takes S^T
+        // rows 2t (and 2t + 8), set 1 rows 2t + 1 (and 2t + 9)
         const uint32_t p0 = movmatrix_trans(pack2<__half>(sc[4 * h], sc[4 * h + 1]));
         const uint32_t p1 = movmatrix_trans(pack2<__half>(sc[4 * h + 2], sc[4 * h + 3]));
         uint32_t be[2][2], bo[2][2];

@@ -463,3 +463,30 @@ def test_rotated_keys_match_rope_in_the_decode_kernel():
     # rotated q and k are rounded to fp16 in both: scores of std 1 with terms of up to ~8 differ by
     # some 2^-11 * 8 * 2, weights by that, o (|o| < 1, weights of 200 tokens) by less than 2e-2
     assert (outs[0] - outs[1]).abs().max() <= 2e-2
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,layout", [(F16, 4, 1, 128, "HND"), (BF16, 8, 1, 128, "NHD"), (F16, 16, 2, 64, "NHD"),
+                                                   (BF16, 3, 3, 64, "HND"), (F16, 8, 2, 256, "NHD"), (BF16, 6, 1, 256, "HND")])
+@pytest.mark.parametrize("depth", [14, 20, 25.5, 29])
+def test_weights_far_below_a_dominant_key_count(dtype, hq, hkv, d, layout, depth):
+    """A long row of keys `depth` bits below a few dominant ones, which weigh nothing in V: all of o comes
+    from the small weights.  A weight is held to 11 bits, and to 2^-32 of the largest."""
+    n = 65536
+    pg = Pages([n], 64, hkv, d, "e2m1", layout, seed=1)
+    pg.scales.fill_(1.0)
+    pg.pool.zero_()
+    codes = pg.pool if layout == "NHD" else pg.pool.transpose(2, 3)  # [pages, 2, slot, head, d / 2]
+    codes[:, 1] = 0x57  # V: 6 and 3
+    top = [3, 19, 35, 51]  # one key in every 16 of the first page
+    codes[int(pg.host_indices[0]), 0, top, :, 0] = 0x07  # K: 6 in dim 0
+    codes[int(pg.host_indices[0]), 1, top] = 0
+    q = torch.zeros(1, hq, d)
+    q[..., 0] = depth * np.log(2.0) * np.sqrt(d) / 6.0
+    q[:, 1::2] *= 0.75
+    q = q.to(dtype).cuda()
+    o = _dec(pg, hq, dtype, disable_split_kv=True).run(q, pg.pool, kv_block_scales=pg.scales)
+    ref_o, _ = _ref(pg, q, hq)
+    o = o.double().cpu().numpy()
+    # the weights sum to 4 at least where the largest is 1
+    tol = (half_step(dtype) + 2.0 ** -11 + 1e-4) * np.abs(ref_o) + 2.0 ** -32 * n * 6.0 / 4 + float(torch.finfo(dtype).tiny) * half_step(dtype)
+    assert (np.abs(o - ref_o) <= tol).all(), f"off by up to {(np.abs(o - ref_o) / np.abs(ref_o)).max():.3f} of o"
