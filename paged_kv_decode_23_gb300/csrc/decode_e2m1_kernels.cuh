@@ -504,9 +504,14 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4 * SL; ++e) {
-        sc[e] = fast_exp2(sc[e] - m2[e & 1]);
-        lsum[e & 1] += sc[e];
+      for (int e = 0; e < 4 * SL; ++e) sc[e] = fast_exp2(sc[e] - m2[e & 1]);
+      // (a step's weights first: every addition to a large sum rounds small ones, and the same way)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float step = sc[j] + sc[j + 2];
+#pragma unroll
+        for (int h = 1; h < SL; ++h) step += sc[4 * h + j] + sc[4 * h + j + 2];
+        lsum[j] += step;
       }
 #pragma unroll
       for (int h = 0; h < SL; ++h) {

@@ -490,3 +490,22 @@ def test_weights_far_below_a_dominant_key_count(dtype, hq, hkv, d, layout, depth
     # the weights sum to 4 at least where the largest is 1
     tol = (half_step(dtype) + 2.0 ** -11 + 1e-4) * np.abs(ref_o) + 2.0 ** -32 * n * 6.0 / 4 + float(torch.finfo(dtype).tiny) * half_step(dtype)
     assert (np.abs(o - ref_o) <= tol).all(), f"off by up to {(np.abs(o - ref_o) / np.abs(ref_o)).max():.3f} of o"
+
+
+@pytest.mark.parametrize("hq,d", [(4, 128), (8, 128), (4, 64), (8, 256)])
+@pytest.mark.parametrize("depth", [19.3, 20.4, 21.8])
+def test_the_sum_of_small_weights_next_to_a_dominant_one(hq, d, depth):
+    """lse of a long row whose small weights all round the same way when they are added to a large sum.
+    Of n tokens a lane adds up n / 128 steps of four, each rounded to 2^-24 of the sum at most; scores,
+    exp2 and the joining of the lanes stay within 1e-5 here (one product a score)."""
+    n = 131072
+    pg = Pages([n], 64, 1, d, "e2m1", "HND", seed=1)
+    pg.scales.fill_(1.0)
+    pg.pool.zero_()
+    pg.pool[int(pg.host_indices[0]), 0, 0, [3, 19, 35, 51], 0] = 0x07  # K: 6 in dim 0 of one key in every 16
+    q = torch.zeros(1, hq, d)
+    q[..., 0] = depth * np.log(2.0) * np.sqrt(d) / 6.0 * (1 + torch.arange(hq) / 64)
+    q = q.to(F16).cuda()
+    _, lse = _dec(pg, hq, F16, disable_split_kv=True).run(q, pg.pool, kv_block_scales=pg.scales, return_lse=True)
+    _, ref = _ref(pg, q, hq)
+    assert np.abs(lse.double().cpu().numpy() - ref).max() <= n / 128 * 2.0 ** -24 + 1e-5
