@@ -8,7 +8,9 @@
 // rounded before the epilogue is P, to fp16: 11 bits, and an absolute 2^-32 of the row's largest weight
 // (P is held 2^kHeadroom above it, so that what lies far below a dominant key still counts in the
 // numerator as it does in the sum, which is taken in 32 bits); and of a bf16 q what lies more than 2^27
-// below its head's largest value (load_q_e2m1).
+// below its head's largest value (load_q_e2m1).  A second product with what P's rounding leaves took
+// 48.8 us for 46.5, 122 for 110 and 72 for 60 (the last with 8 heads of 256, cap and window); the error
+// of fp16 outputs against 64 bits was 2.1e-4 instead of 3.0e-4, of bf16 outputs 1.7e-3 in both.
 //
 // Structure as in decode_kernels.cuh (producer warp, mbarrier ring, consumer warps, split partials
 // merged by the last chunk's CTA), with these differences:
