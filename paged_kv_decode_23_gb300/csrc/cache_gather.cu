@@ -3,8 +3,9 @@
 // A row of one head is spread over head_dim / 16 lanes, sixteen values each (of a 4-bit cache one
 // block: eight code bytes and its scale): 32, 16 or 8 bytes in, 32 bytes out.  A group of lanes
 // takes up to R neighbouring heads of one token's K or V, all loaded before the first is used.
-// Nothing is computed but the widening and one multiply: bytes bound.  345 MB of prefixes out of a
+// Nothing is computed but the widening and one product, rounded once: bytes bound.  345 MB of prefixes out of a
 // 4-bit cache (HND, 8 heads of 128): 54.8 us, 6.3 TB/s; a call of some MB is latency, 3 us.
+#include <cstring>
 #include <type_traits>
 
 #include "cache_rows.cuh"
@@ -22,9 +23,28 @@ struct GatherParams {
   int hc;
   int page_log;
   int wide;         // the outputs' rows are 32-byte aligned: one store a lane
+  int rounding[2];  // of K's and V's products
 };
 
 constexpr int kThreads = 64;
+
+// How a product x * unit reaches T with one rounding; x has at most 11 bits.
+//   kExact  unit has at most 12 bits: the 32-bit product is exact.
+//   kSticky unit has more: no product is then a border of T (a border's odd part is below 2^12 and unit's
+//           odd part divides the product's), so that the product cut off to 32 bits with its last bit set
+//           rounds as the exact one does.
+//   kWide   a unit of few bits that can take a bf16 value's product below 2^-149: 64 bits.
+// The prefixes above out of 4 bits, e4m3 and bf16: 55.1, 62.5 and 80.7 us with kExact, 55.2, 63.7 and
+// 88.0 with kSticky.  Every product's rest from an FMA, one way for all units, took 72.7 and 118 (4 bits, bf16).
+enum Rounding { kExact = 0, kSticky = 1, kWide = 2 };
+
+Rounding rounding_of(float unit, bool bf16_values) {
+  uint32_t bits;
+  std::memcpy(&bits, &unit, sizeof bits);  // (a normal number)
+  const int zeros = __builtin_ctz((bits & 0x7fffffu) | 0x800000u);
+  if (24 - zeros > 12) return kSticky;
+  return bf16_values && (int)(bits >> 23) - 127 - (23 - zeros) < -16 ? kWide : kExact;
+}
 
 // Eight values of raw (of an e2m1 block: its codes' values without the scale).
 template <typename T, int KV>
@@ -45,6 +65,12 @@ __device__ __forceinline__ void widen8(const uint4& raw, float (&x)[8]) {
         : "r"(raw.x));
     unpack8<__half>(h, x);
   }
+}
+
+// x with its last bit set; an infinity (of a 16-bit cache) is itself.
+template <int KV>
+__device__ __forceinline__ float sticky(float x) {
+  return KV == kSame16 && !(fabsf(x) < __int_as_float(0x7f800000)) ? x : __uint_as_float(__float_as_uint(x) | 1u);
 }
 
 template <typename T, int KV, int D, int R>
@@ -93,18 +119,24 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
 #pragma unroll
     for (int j = 0; j < R; ++j) sf[j] = j < n ? at[j * a.pool.scale_strides[2]] : 0u;
   }
+  constexpr bool bf16_values = KV == kSame16 && std::is_same<T, __nv_bfloat16>::value;
   const float unit = is_v ? a.pool.v_scale : a.pool.k_scale;
+  const int rounding = p.rounding[is_v];
   const int64_t o0 = is_v ? a.v_out_strides[0] : a.k_out_strides[0];
   const int64_t o1 = is_v ? a.v_out_strides[1] : a.k_out_strides[1];
   T* dst = static_cast<T*>(is_v ? a.v_out : a.k_out) + t * o0 + h0 * o1 + 16 * gl;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     if (j >= n) break;
-    // (an e2m1 value times its scale has at most 6 bits: only the last product is rounded)
+    // (an e2m1 value times its scale has at most 6 bits and is exact)
     const float s = KV == kFp4 ? e4m3_value(sf[j]) : 1.f;
     uint4 v16[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (KV == kSame16 && unit == 1.f) {
+        v16[i] = raw[j][KV == kSame16 ? i : 0];
+        continue;
+      }
       float x[8];
       if constexpr (KV == kSame16) widen8<T, KV>(raw[j][i], x);
       else if constexpr (KV == kFp8) widen8<T, KV>(i ? make_uint4(raw[j][0].z, raw[j][0].w, 0, 0) : raw[j][0], x);
@@ -113,7 +145,14 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
       for (int e = 0; e < 8; e += 2) {
         float2 v = make_float2(x[e], x[e + 1]);
         if constexpr (KV == kFp4) v = __fmul2_rn(v, make_float2(s, s));
-        v = __fmul2_rn(v, make_float2(unit, unit));
+        if (rounding == kExact) {
+          v = __fmul2_rn(v, make_float2(unit, unit));
+        } else if (bf16_values && rounding == kWide) {
+          v = make_float2(to_odd((double)v.x * unit), to_odd((double)v.y * unit));
+        } else {
+          const float2 w = __fmul2_rz(v, make_float2(unit, unit));
+          v = make_float2(sticky<KV>(w.x), sticky<KV>(w.y));
+        }
         x[e] = v.x;
         x[e + 1] = v.y;
       }
@@ -141,6 +180,9 @@ cudaError_t launch_r(const pkd_gather_args& a, cudaStream_t s) {
   if (a.k_out) bits |= (uint64_t)a.k_out | (uint64_t)(2 * a.k_out_strides[0]) | (uint64_t)(2 * a.k_out_strides[1]);
   if (a.v_out) bits |= (uint64_t)a.v_out | (uint64_t)(2 * a.v_out_strides[0]) | (uint64_t)(2 * a.v_out_strides[1]);
   p.wide = (bits & 31) == 0;  // (those 345 MB take 62.7 us with two 16-byte stores a lane, 54.8 with one)
+  constexpr bool bf16_values = KV == kSame16 && std::is_same<T, __nv_bfloat16>::value;
+  p.rounding[0] = rounding_of(a.pool.k_scale, bf16_values);
+  p.rounding[1] = rounding_of(a.pool.v_scale, bf16_values);
   p.hc = (a.pool.num_kv_heads + R - 1) / R;
   p.chunks = (uint32_t)(p.hc * ((a.k_out != nullptr) + (a.v_out != nullptr)));
   p.page_log = __builtin_ctz((unsigned)a.pool.page_size);

@@ -681,3 +681,57 @@ def test_append_of_large_calls_over_scales(dtype, layout, d):
     assert_rounded(out[torch.from_numpy(live).cuda()], wq, tq, dtype, "q")
     assert_rounded(pg.rows(pg.pool, 0, b[live], pos[live]), wk / ks, tk / ks, dtype, "k")
     assert np.array_equal(_f64(pg.rows(pg.pool, 1, b[live], pos[live])), nearest16(_f64(v)[live] / vs, dtype))
+
+
+# ------------------------------------------------------------------------------ gather rounds once
+def _false_ties(values, dtype, count):
+    """float32 scales whose product with one of `values` rounds to a border of dtype in 32 bits, while the
+    exact product lies beside it."""
+    bits = {BF16: 8, F16: 11}[dtype]
+    rng = np.random.default_rng(bits)
+    found = []
+    while len(found) < count:
+        c = float(rng.choice(values))
+        border = (2 * int(rng.integers(2 ** (bits - 1), 2 ** bits)) + 1) * 2.0 ** -bits
+        s = np.float32(border / c)
+        if np.float32(c) * s == np.float32(border) and c * float(s) != border:
+            found.append(float(s))
+    return found
+
+
+@pytest.mark.parametrize("kv,out_dtype", [("same", BF16), ("same", F16), ("e4m3", BF16), ("e4m3", F16), ("e2m1", BF16), ("e2m1", F16)])
+def test_gather_rounds_once(kv, out_dtype):
+    """Every stored value times the scale, rounded once from the exact product."""
+    from paged_kv_decode_23_gb300 import gather_paged_kv
+    n, hkv, d = 64, 2, 128
+    pg = Pages([n], 16, hkv, d, kv, "NHD", seed=4, dtype=out_dtype)
+    if kv == "same":  # values of few bits, so that they occur
+        pg.pool.copy_((torch.randint(-63, 64, pg.pool.shape, generator=torch.Generator().manual_seed(1)) * 0.125).cuda())
+    elif kv == "e4m3":
+        pg.pool.copy_((torch.randint(-15, 16, pg.pool.shape, generator=torch.Generator().manual_seed(1)) * 0.25).cuda())
+    vals = pg.values16().double().cuda()
+    stored = np.unique(np.abs(_f64(vals[pg.indices.long()])))
+    b, pos = _idx([0] * n), _idx(np.arange(n))
+    want = [_f64(pg.rows(vals, i, [0] * n, np.arange(n))) for i in range(2)]
+    scales = _false_ties(stored[stored > 0], out_dtype, 40)
+    for ks, vs in zip(scales[::2], scales[1::2]):
+        got = gather_paged_kv(b, pos, pg.pool, pg.indptr, pg.indices, kv_block_scales=pg.scales, k_scale=ks, v_scale=vs,
+                              out_dtype=out_dtype)
+        for x, w, s in zip(got, want, (ks, vs)):
+            bad = _f64(x) != nearest16(w * s, out_dtype)
+            assert not bad.any(), f"{bad.sum()} of {bad.size} rounded twice at scale {s}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 1e-13, 0.3, 1.0, 3.3, 1e10, 2.0 ** 64])
+def test_gather_of_any_16_bit_value(dtype, scale):
+    """Products of every magnitude: into the subnormals and past the largest value; infinities and NaNs."""
+    from paged_kv_decode_23_gb300 import gather_paged_kv
+    n, hkv, d = 256, 2, 64
+    pg = Pages([n], 16, hkv, d, "same", "HND", seed=2, dtype=dtype)
+    raw = torch.randint(-32768, 32768, pg.pool.shape, generator=torch.Generator().manual_seed(7), dtype=torch.int32)
+    pg.pool = raw.to(torch.int16).view(dtype).cuda()
+    got = gather_paged_kv(_idx([0] * n), _idx(np.arange(n)), pg.pool, pg.indptr, pg.indices, "HND", k_scale=scale, v_scale=scale)
+    for i in range(2):
+        want = nearest16(_f64(pg.rows(pg.pool, i, [0] * n, np.arange(n))) * float(np.float32(scale)), dtype)
+        assert np.array_equal(_f64(got[i]), want, equal_nan=True), f"{(_f64(got[i]) != want).sum()} differ"
