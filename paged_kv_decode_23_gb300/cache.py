@@ -17,8 +17,8 @@ import numpy as np
 import torch
 
 from . import _lib as L
-from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, _host_i32, current_device, new_output,
-                     pool_views, raw_stream)
+from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, current_device, new_output, pool_views,
+                     raw_stream)
 
 _POOL = "4Pq3q3q2Pq5i2fi"  # pkd_paged_pool
 _APPEND = struct.Struct("@" + _POOL + "4P8q3P2PPqPqd6i")  # pkd_append_args
@@ -251,13 +251,22 @@ def gather_paged_kv(batch_indices: torch.Tensor, positions: torch.Tensor, paged_
     return k, v
 
 
+def _page_ids(x, name: str) -> np.ndarray:
+    """Host page ids as contiguous int32, refused where a value would change on the way."""
+    a = x.detach().cpu().numpy() if isinstance(x, torch.Tensor) else np.asarray(x)
+    if a.dtype != np.int32 and a.size:
+        if a.dtype.kind not in "iu" or a.min() < -2 ** 31 or a.max() >= 2 ** 31:
+            raise ValueError(f"{name} must be 32-bit integers")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
 def _host_ids(x, name: str):
     """(address, count, what to keep alive) of host page ids."""
     if isinstance(x, torch.Tensor) and x.dtype is _INT32 and x.device.type == "cpu" and x.is_contiguous():
         if x.dim() != 1:
             raise ValueError(f"{name} must be a list of page ids")
         return x.data_ptr(), x.shape[0], x
-    a = _host_i32(x)
+    a = _page_ids(x, name)
     if a.ndim != 1:
         raise ValueError(f"{name} must be a list of page ids")
     return a.ctypes.data, a.shape[0], a
@@ -353,7 +362,7 @@ class PageAllocator:
 
     def free(self, pages) -> None:
         """One use less of each page; PkdError, and nothing changed, if one is not in use."""
-        p = _host_i32(pages)
+        p = _page_ids(pages, "pages")
         L.check(L.lib().pkd_pages_free(self._h, p.ctypes.data, p.size))
 
     def fork(self, pages, kv_len: int, page_size: int):
@@ -361,7 +370,7 @@ class PageAllocator:
         ``(its pages, src, dst)``.  Full pages are shared; a partly filled last page gets a page of
         its own, and src / dst (arrays of one id, else empty) is the copy to make with
         ``copy_pages`` before either sequence appends."""
-        p = _host_i32(pages)
+        p = _page_ids(pages, "pages")
         if kv_len < 0 or page_size < 1:
             raise ValueError("kv_len must be >= 0 and page_size >= 1")
         out = np.empty(-(-kv_len // page_size) if kv_len <= p.size * page_size else 0, dtype=np.int32)

@@ -288,3 +288,25 @@ def test_packed_structs_have_the_header_s_sizes(tmp_path):
     sizes = [struct.Struct("@" + C._POOL).size, C._APPEND.size, C._GATHER.size, D._SCALED_RUN.size]
     assert got[:4] == sizes
     assert got[4:] == [C._APPEND.size - 8 - 24, C._GATHER.size - 8, D._SCALED_RUN.size - 16]
+
+
+@pytest.mark.parametrize("kind", ["list", "numpy", "tensor"])
+@pytest.mark.parametrize("ids", [[2 ** 32], [2 ** 32 + 1, 0], [-2 ** 32], [0.5], [1.0], [2 ** 31]])
+def test_page_ids_of_more_than_32_bits_are_refused(kind, ids):
+    """Not taken modulo 2^32, nor cut to whole numbers: page 0 would lose a use, or be copied."""
+    from paged_kv_decode_23_gb300 import PageAllocator, copy_pages
+    x = {"list": lambda: ids, "numpy": lambda: np.array(ids), "tensor": lambda: torch.tensor(ids)}[kind]()
+    a = PageAllocator(4)
+    a.alloc(2)
+    with pytest.raises(ValueError):
+        a.free(x)
+    with pytest.raises(ValueError):
+        a.fork(x, 3, 16)
+    assert a.uses().tolist() == [1, 1, 0, 0]
+    for pair in ((x, list(range(2, 2 + len(ids)))), (list(range(2, 2 + len(ids))), x)):
+        with pytest.raises(ValueError, match="32-bit"):
+            copy_pages([torch.zeros(4, 8)], *pair)
+    a.free(np.array([1], dtype=np.int64))
+    a.free(torch.tensor([0], dtype=torch.int16))
+    a.free([])
+    assert a.num_free == 4
