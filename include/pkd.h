@@ -451,10 +451,11 @@ typedef struct pkd_paged_pool {
  *     appends to with another: see pkd_pages_fork).
  * eps: 0 or a normal 32-bit number.
  * q may be NULL (num_qo_heads 0), and k with v NULL (only q is normed and rotated).  q_out may be
- * q itself; its rows must not overlap.  All of q, k, v, q_out: in_dtype F16 or BF16, head_dim contiguous, 16-byte aligned,
- * strides {token, head} in elements, multiples of 8.  Weights: head_dim values of in_dtype, or
- * float32 with weight_f32; 16-byte aligned.  rotary_dim: 0 or a multiple of 16 up to head_dim;
- * cos_sin float32 [cos_sin_rows, rotary_dim], contiguous, 16-byte aligned.
+ * q itself; else its rows must overlap neither each other nor those of q, k and v (INVALID_ARG).  All
+ * of q, k, v, q_out: in_dtype F16 or BF16, head_dim contiguous, 16-byte aligned, strides {token, head}
+ * in elements, multiples of 8.  Weights: head_dim values of in_dtype, or float32 with weight_f32;
+ * 16-byte aligned.  rotary_dim: 0 or a multiple of 16 up to head_dim; cos_sin float32
+ * [cos_sin_rows, rotary_dim], contiguous, 16-byte aligned.
  * status (device, NULL to leave out) receives the PKD_STATUS_* bits by OR; nothing clears it.
  */
 typedef struct pkd_append_args {
@@ -492,7 +493,7 @@ int pkd_append(const pkd_append_args* args, void* stream);
  * BF16; for a 16-bit cache its own type).  Rows of padding (negative batch index) and rows with no
  * slot are left as they were, the latter with a status bit as in pkd_append.
  * k_out / v_out: head_dim contiguous, 16-byte aligned, strides {token, head} in elements,
- * multiples of 8, without overlap; either may be NULL.  A row may be listed any number of times.
+ * multiples of 8, without overlap, of each other neither; either may be NULL.  A row may be listed any number of times.
  */
 typedef struct pkd_gather_args {
   pkd_paged_pool pool;

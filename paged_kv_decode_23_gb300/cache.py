@@ -137,8 +137,8 @@ def append_paged_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opt
     ``paged_kv_cache`` (5-D, or a (k, v) pair) receives k / k_scale and v / v_scale in the rows' type
     or float8_e4m3fn, rounded once, or as 4-bit codes with ``kv_block_scales`` as
     ``BatchDecodePagedKV.run`` reads them.
-    Returns q's rows (``out``, which may be ``q``; a fresh tensor's padding rows are undefined), or
-    None without q.  ``q`` may be None, or ``k`` and ``v`` with the cache and page table.
+    Returns q's rows (``out``, which may be ``q``, but overlap neither other rows of it nor k or v; a
+    fresh tensor's padding rows are undefined), or None without q.  ``q`` may be None, or ``k`` and ``v`` with the cache and page table.
 
     ``status`` (one int32 on the device) receives STATUS_BAD_TOKEN for a row that has no slot in
     its sequence or no entry in ``cos_sin_cache``, STATUS_BAD_PAGE for a page id outside the pool;

@@ -104,6 +104,39 @@ int check_out(const void* p, const int64_t (&st)[2], int64_t tokens, int64_t hea
   return PKD_OK;
 }
 
+// Whether a row of a and a row of b (n tokens of ha and hb heads, checked strides) share bytes; where
+// their tokens lie at different distances (or it would take long to tell), whether the memory that they
+// span does.
+bool rows_overlap(const void* a, const int64_t (&sa)[2], int64_t ha, const void* b, const int64_t (&sb)[2],
+                  int64_t hb, int64_t n, int64_t D) {
+  if (ha == 0 || hb == 0) return false;
+  const int64_t a0 = n > 1 ? sa[0] : 0, b0 = n > 1 ? sb[0] : 0, a1 = ha > 1 ? sa[1] : 0, b1 = hb > 1 ? sb[1] : 0;
+  const int64_t off = (static_cast<const char*>(b) - static_cast<const char*>(a)) / 2;
+  if (off >= (n - 1) * a0 + (ha - 1) * a1 + D || -off >= (n - 1) * b0 + (hb - 1) * b1 + D) return false;
+  const bool even = a1 == b1 || ha == 1 || hb == 1;
+  if (a0 != b0 || (!even && ha * hb > 65536)) return true;
+  // two rows start off + jb * b1 - ja * a1 + i * a0 elements apart, |i| < n
+  auto meet = [&](int64_t x) {
+    const int64_t i = a0 > 0 ? (x < 0 ? -((a0 - 1 - x) / a0) : x / a0) : 0;  // x - i * a0 in [0, a0)
+    return (i < n && -i < n && x - i * a0 < D && x - i * a0 > -D) ||
+           (a0 > 0 && i + 1 < n && -(i + 1) < n && (i + 1) * a0 - x < D);
+  };
+  if (even) {
+    const int64_t st = ha == 1 ? b1 : a1;
+    for (int64_t j = 1 - ha; j < hb; ++j)
+      if (meet(off + j * st)) return true;
+    return false;
+  }
+  for (int64_t ja = 0; ja < ha; ++ja)
+    for (int64_t jb = 0; jb < hb; ++jb)
+      if (meet(off + jb * b1 - ja * a1)) return true;
+  return false;
+}
+
+bool same_rows(const void* a, const int64_t (&sa)[2], const void* b, const int64_t (&sb)[2], int64_t n, int64_t heads) {
+  return a == b && (n <= 1 || sa[0] == sb[0]) && (heads <= 1 || sa[1] == sb[1]);
+}
+
 }  // namespace
 
 extern "C" int pkd_append(const pkd_append_args* args, void* stream) {
@@ -126,6 +159,14 @@ extern "C" int pkd_append(const pkd_append_args* args, void* stream) {
     if (kv) {
       if (int rc = check_rows(a.k, a.k_strides, "k")) return rc;
       if (int rc = check_rows(a.v, a.v_strides, "v")) return rc;
+    }
+    if (a.q) {
+      const int64_t n = a.num_tokens, hq = a.num_qo_heads, hkv = a.pool.num_kv_heads, D = a.pool.head_dim;
+      if ((!same_rows(a.q_out, a.q_out_strides, a.q, a.q_strides, n, hq) &&
+           rows_overlap(a.q_out, a.q_out_strides, hq, a.q, a.q_strides, hq, n, D)) ||
+          (kv && (rows_overlap(a.q_out, a.q_out_strides, hq, a.k, a.k_strides, hkv, n, D) ||
+                  rows_overlap(a.q_out, a.q_out_strides, hq, a.v, a.v_strides, hkv, n, D))))
+        return bad("q_out overlaps rows of q (other than being q), k or v");
     }
     if (!a.batch_indices || !a.positions) return bad("null batch_indices / positions");
     if ((a.q_weight && !on16(a.q_weight)) || (a.k_weight && !on16(a.k_weight)))
@@ -154,6 +195,10 @@ extern "C" int pkd_gather(const pkd_gather_args* args, void* stream) {
     if (a.v_out)
       if (int rc = check_out(a.v_out, a.v_out_strides, a.num_tokens, a.pool.num_kv_heads, a.pool.head_dim, "v_out"))
         return rc;
+    if (a.k_out && a.v_out &&
+        rows_overlap(a.k_out, a.k_out_strides, a.pool.num_kv_heads, a.v_out, a.v_out_strides, a.pool.num_kv_heads,
+                     a.num_tokens, a.pool.head_dim))
+      return bad("k_out overlaps v_out");
     if (!a.batch_indices || !a.positions) return bad("null batch_indices / positions");
     return done(launch_gather(a, static_cast<cudaStream_t>(stream)), "gather kernel launch");
   });

@@ -310,3 +310,89 @@ def test_page_ids_of_more_than_32_bits_are_refused(kind, ids):
     a.free(torch.tensor([0], dtype=torch.int16))
     a.free([])
     assert a.num_free == 4
+
+
+# ------------------------------------------------------------------------------ rows that overlap
+def _starts(at, st, n, heads):
+    return (at // 2 + st[0] * np.arange(n)[:, None] + st[1] * np.arange(heads)).ravel()
+
+
+def _meet(a, b, d):
+    return bool((np.abs(a[:, None] - b) < d).any())
+
+
+@pytest.mark.parametrize("over", APPEND_REFUSALS, ids=lambda o: ",".join(f"{k}={v}" for k, v in o.items()))
+def test_append_refuses_where_rows_lie_apart(over):
+    """As above, with k and v away from q: it is the argument that is refused."""
+    from paged_kv_decode_23_gb300 import _lib as L
+    args = _append_args(**{**dict(kr=1 << 20, vr=2 << 20, out=256), **over})
+    assert L.lib().pkd_append(args, None) in (-1, -5)
+    assert b"q_out overlaps" not in L.lib().pkd_last_error()
+
+
+def test_append_rows_that_overlap():
+    """q_out against q, k and v in layouts of many kinds, against all pairs of rows.  (Without batch
+    indices: no call gets as far as a launch.)"""
+    from paged_kv_decode_23_gb300 import _lib as L
+    rng = np.random.default_rng(2)
+    d, base, seen = 64, 1 << 22, [0, 0]
+    for step in range(3000):
+        n, hq, hkv = (int(x) for x in rng.integers(1, 5, 3))
+        kind = rng.integers(4)
+        if kind == 0:  # one projection's output
+            row = (hq + 2 * hkv) * d
+            st = {x: (row, d) for x in "qkvo"}
+            at = dict(q=0, k=hq * d, v=(hq + hkv) * d, o=0)
+        elif kind == 1:  # q, k and v of a kv head together
+            hq = hkv
+            st = {x: (3 * hkv * d, 3 * d) for x in "qkvo"}
+            at = dict(q=0, k=d, v=2 * d, o=0)
+        elif kind == 2:  # heads first
+            st = {x: (d, n * d) for x in "qkvo"}
+            at = dict(q=0, k=hq * n * d, v=(hq + hkv) * n * d, o=0)
+        else:
+            st = {x: (int(rng.integers(hq + hkv, 12)) * d, d) for x in "qkvo"}
+            at = {x: int(rng.integers(0, 40)) * d for x in "qkvo"}
+        if rng.random() < 0.5:
+            at["o"] += int(rng.integers(-40, 40)) * d // 2 // 8 * 8
+        if rng.random() < 0.3:
+            at["o"] += 100 * d
+        if rng.random() < 0.2:
+            st["o"] = (hq * d, d)
+        at = {x: base + 2 * v for x, v in at.items()}
+        out = _starts(at["o"], st["o"], n, hq)
+        own = [_meet(out[:i], out[i:i + 1], d) for i in range(1, len(out))]
+        if any(own):
+            continue
+        same = at["o"] == at["q"] and (n == 1 or st["o"][0] == st["q"][0]) and (hq == 1 or st["o"][1] == st["q"][1])
+        want = (not same and _meet(out, _starts(at["q"], st["q"], n, hq), d)) or any(
+            _meet(out, _starts(at[x], st[x], n, hkv), d) for x in "kv")
+        args = _append_args(n=n, hq=hq, hkv=hkv, d=d, st=(1 << 14, 1 << 10, d), q=at["q"], kr=at["k"], vr=at["v"],
+                            out=at["o"], qst=st["q"], kst=st["k"], vst=st["v"], ost=st["o"], bi=0)
+        assert L.lib().pkd_append(args, None) == -1
+        msg = L.lib().pkd_last_error()
+        got = b"q_out overlaps" in msg
+        assert got or b"null batch_indices" in msg, msg
+        seen[want] += 1
+        if want:
+            assert got
+        elif got:  # refused unread: tokens at different distances in the memory of another's
+            assert n > 1 and len({st["o"][0], st["q"][0], st["k"][0], st["v"][0]}) > 1
+    assert min(seen) > 300
+
+
+def test_gather_outputs_that_overlap():
+    from paged_kv_decode_23_gb300 import _lib as L
+    from paged_kv_decode_23_gb300 import cache as C
+    pool = (4096, 8192, 0, 0, 8, 4096, 256, 128, 0, 0, 0, 64, 64, 8, 1, 1, 2, 128, 16, 1.0, 1.0, 0)
+
+    def call(k, v, kst, vst, n=3):  # (no batch indices: no call gets as far as a launch)
+        assert L.lib().pkd_gather(C._GATHER.pack(*pool, k, v, *kst, *vst, 0, 64, 0, n, 1, 0), None) == -1
+        return L.lib().pkd_last_error()
+    for k, v, kst, vst in ((4096, 4096, (256, 128), (256, 128)), (4096, 4352, (256, 128), (256, 128)),
+                           (4096, 4096 + 2 * 384, (512, 128), (512, 128)), (4096, 4112, (1024, 128), (1024, 128)),
+                           (8192, 4096 + 2 * 300 // 8 * 8 * 8, (512, 128), (512, 256))):
+        assert b"overlaps v_out" in call(k, v, kst, vst)
+    for k, v, kst, vst in ((4096, 4096 + 2 * 768, (256, 128), (256, 128)), (4096, 4096 + 512, (512, 128), (512, 128)),
+                           (4096, 4096 + 256, (512, 256), (512, 256)), (1 << 20, 4096, (256, 128), (256, 128))):
+        assert b"null batch_indices" in call(k, v, kst, vst)
