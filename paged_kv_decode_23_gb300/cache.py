@@ -17,8 +17,8 @@ import numpy as np
 import torch
 
 from . import _lib as L
-from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, current_device, new_output, pool_views,
-                     raw_stream)
+from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, current_device, forward_ad, new_output,
+                     pool_views, raw_stream, refuse_gradients)
 
 _POOL = "4Pq3q3q2Pq5i2fi"  # pkd_paged_pool
 _APPEND = struct.Struct("@" + _POOL + "4P8q3P2PPqPqd6i")  # pkd_append_args
@@ -151,10 +151,12 @@ def append_paged_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opt
     dev, dtype = first.get_device(), first.dtype
     if dev < 0:
         raise ValueError("q, k and v must be CUDA tensors")
-    if torch.is_grad_enabled() and (first.requires_grad or (k is not None and (k.requires_grad or v.requires_grad))
-                                    or (q_weight is not None and q_weight.requires_grad)
-                                    or (k_weight is not None and k_weight.requires_grad)):
-        raise NotImplementedError("append has no backward pass (detach its inputs)")
+    if (torch.is_grad_enabled()
+            and (first.requires_grad or (k is not None and (k.requires_grad or v.requires_grad))
+                 or (q_weight is not None and q_weight.requires_grad)
+                 or (k_weight is not None and k_weight.requires_grad)
+                 or (cos_sin_cache is not None and cos_sin_cache.requires_grad))) or forward_ad._current_level >= 0:
+        refuse_gradients("append", q, k, v, q_weight, k_weight, cos_sin_cache)
     n, hq, d = first.shape
     if k is not None:
         pool, hkv, pd = _pool_fields(paged_kv_cache, kv_block_scales, kv_indptr, kv_indices, kv_layout,
@@ -228,6 +230,10 @@ def gather_paged_kv(batch_indices: torch.Tensor, positions: torch.Tensor, paged_
     dev = first.get_device()
     if dev < 0:
         raise ValueError("the cache must be a CUDA tensor")
+    second = None if first is paged_kv_cache else paged_kv_cache[1]
+    if (torch.is_grad_enabled() and (first.requires_grad or (second is not None and second.requires_grad))
+            ) or forward_ad._current_level >= 0:
+        refuse_gradients("gather", first, second)
     if out is not None:
         k, v = out
         if out_dtype is not None and out_dtype != k.dtype:

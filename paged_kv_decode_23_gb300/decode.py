@@ -89,6 +89,21 @@ raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+forward_ad = torch.autograd.forward_ad  # (_current_level: 0 or more inside a dual level)
+
+
+def refuse_gradients(what: str, *tensors) -> None:
+    """Raises where a derivative of `tensors` (None among them) would be lost: there is no backward pass
+    and no forward mode.  Callers look first whether any can be (a call of some us of host time)."""
+    for t in tensors:
+        if t is None:
+            continue
+        if torch.is_grad_enabled() and t.requires_grad:
+            raise NotImplementedError(f"{what} has no backward pass (detach its inputs)")
+        if forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward mode (unpack its dual inputs)")
+
+
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         return stream.cuda_stream
@@ -343,6 +358,8 @@ class BatchDecodePagedKV:
     def _run_scaled(self, q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse, stream,
                     timing_events, enable_pdl):
         """run() on a plan with a 4-bit cache; q's shape and dtype are checked."""
+        if (torch.is_grad_enabled() and q.requires_grad) or forward_ad._current_level >= 0:
+            refuse_gradients("decode over a 4-bit cache", q)
         a = self._plan_args
         rows, hq, d, ps, hkv = a["rows"], a["num_qo_heads"], a["head_dim"], a["page_size"], a["num_kv_heads"]
         dev = q.get_device()

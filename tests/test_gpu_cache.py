@@ -735,3 +735,44 @@ def test_gather_of_any_16_bit_value(dtype, scale):
     for i in range(2):
         want = nearest16(_f64(pg.rows(pg.pool, i, [0] * n, np.arange(n))) * float(np.float32(scale)), dtype)
         assert np.array_equal(_f64(got[i]), want, equal_nan=True), f"{(_f64(got[i]) != want).sum()} differ"
+
+
+# ------------------------------------------------------------------------------ derivatives
+def test_derivatives_are_refused_not_dropped():
+    """Inputs that need a gradient, and dual tensors of forward mode, wherever they come in."""
+    import torch.autograd.forward_ad as fwAD
+    from paged_kv_decode_23_gb300 import append_paged_kv, gather_paged_kv
+    n, d = 3, 128
+    pg = Pages([10], 16, 2, d, "same", "NHD")
+    q, k, v = _qkv(n, 4, 2, d, BF16, seed=1, fused=False)
+    b, pos = _idx([0] * n), _idx(np.arange(n))
+    w, table = torch.ones(d, device="cuda"), _table(10, d)
+
+    def append(**kw):
+        a = dict(q=q, k=k, v=v, pool=pg.pool, qw=w, kw=w, cs=table, out=torch.zeros_like(q))
+        a.update(kw)
+        return append_paged_kv(a["q"], a["k"], a["v"], b, pos, a["pool"], pg.indptr, pg.indices, q_weight=a["qw"],
+                               k_weight=a["kw"], cos_sin_cache=a["cs"], out=a["out"])
+
+    def gather(pool):
+        return gather_paged_kv(b, pos, pool, pg.indptr, pg.indices)
+    calls = [(lambda t, x=x: append(**{x: t}), t) for x, t in
+             (("q", q), ("k", k), ("v", v), ("qw", w), ("kw", w), ("cs", table))]
+    kc, vc = (pg.pool[:, i].clone() for i in range(2))
+    calls += [(gather, pg.pool), (lambda t: gather((t, vc)), kc), (lambda t: gather((kc, t)), vc)]
+    before = pg.pool.clone()
+    for call, t in calls:
+        leaf = t.detach().clone().requires_grad_()
+        with pytest.raises(NotImplementedError, match="backward"):
+            call(leaf)
+        with fwAD.dual_level():
+            dual = fwAD.make_dual(t.detach().clone(), torch.ones_like(t))
+            with pytest.raises(NotImplementedError, match="forward"):
+                call(dual)
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="forward"):
+                call(dual)  # (no_grad does not switch forward mode off)
+            call(fwAD.unpack_dual(dual).primal)
+        pg.pool.copy_(before)
+    with torch.no_grad():
+        got = append(q=q.clone().requires_grad_())
+    assert torch.equal(got, append())

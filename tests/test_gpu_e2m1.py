@@ -509,3 +509,20 @@ def test_the_sum_of_small_weights_next_to_a_dominant_one(hq, d, depth):
     _, lse = _dec(pg, hq, F16, disable_split_kv=True).run(q, pg.pool, kv_block_scales=pg.scales, return_lse=True)
     _, ref = _ref(pg, q, hq)
     assert np.abs(lse.double().cpu().numpy() - ref).max() <= n / 128 * 2.0 ** -24 + 1e-5
+
+
+def test_derivatives_are_refused_not_dropped():
+    import torch.autograd.forward_ad as fwAD
+    pg = Pages([50], 16, 2, 128, "e2m1", "NHD", seed=2)
+    q = _q(1, 8, 128, BF16)
+    dec = _dec(pg, 8, BF16)
+    want = dec.run(q, pg.pool, kv_block_scales=pg.scales)
+    leaf = q.clone().requires_grad_()
+    with pytest.raises(NotImplementedError, match="backward"):
+        dec.run(leaf, pg.pool, kv_block_scales=pg.scales)
+    with torch.no_grad():
+        assert torch.equal(dec.run(leaf, pg.pool, kv_block_scales=pg.scales), want)
+    with fwAD.dual_level():
+        dual = fwAD.make_dual(q.clone(), torch.ones_like(q))
+        with pytest.raises(NotImplementedError, match="forward"):
+            dec.run(dual, pg.pool, kv_block_scales=pg.scales)
