@@ -630,9 +630,12 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
 template <typename T, int KV, int D>
 cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
   // Heads a group takes: one while the call leaves SMs idle, two once there is work for every SM
-  // several times over, which keeps more bytes under way.  Replayed graphs with one and with two: one
-  // token of 32 + 2 * 8 heads of 128 4.8 and 5.5 us, 340 MB of prompts 83 and 66 us, the chunk into
-  // e4m3 36.3 and 36.0 us, twice its tokens into 4 bits (and read back) 90.3 and 88.9 us.
+  // several times over, which keeps more bytes under way.  One token of 32 + 2 * 8 heads of 128, a
+  // replayed graph: 4.8 us with one, 5.5 with two.  Calls in a stream, with one and with two: the 8,190
+  // tokens above 82.0 and 63.5 us, into e4m3 106 and 96, into 4 bits 153 and 137; the chunk above 32.5
+  // and 32.9, into 4 bits 43.8 and 41.0; 8,192 tokens of 16 + 2 * 16 heads of 64 into 16, 8 and 4 bits
+  // 28.5 and 23.2, 41.8 and 39.7, 58.9 and 56.4.  (Two heads' instances for codes spill: 64 to 72
+  // bytes a thread into e4m3, 264 to 324 into 4 bits; one head's 0 and 128 to 136.)
   const int64_t rows = a.num_tokens * (a.num_qo_heads + 2 * (int64_t)a.pool.num_kv_heads);
   if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, 2>(a, s);
   return launch_r<T, KV, D, 1>(a, s);
