@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kernel(const __grid_co
 }
 
 template <typename T, int KV, int D, int R>
-cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
+cudaError_t launch_r(const pkd_append_args& a, int sms, cudaStream_t s) {
   constexpr int PER = R * 32 / (D / 16);  // heads of a warp
   AppendParams p;
   p.a = a;
@@ -616,7 +616,7 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
     p.token0 = t0;
     p.items = (uint32_t)(n * p.chunks);
     // as many warps as fit at once, and no more than there are items
-    uint32_t room = 152u * kCtas * (kThreads / 32);
+    uint32_t room = (uint32_t)sms * kCtas * (kThreads / 32);
     if (is16<KV>()) room = (room < p.chunks ? 1 : room / p.chunks) * p.chunks;
     p.warps = p.items < room ? p.items : room;
     p.parallel = p.warps / p.chunks;
@@ -628,7 +628,7 @@ cudaError_t launch_r(const pkd_append_args& a, cudaStream_t s) {
 }
 
 template <typename T, int KV, int D>
-cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
+cudaError_t launch_d(const pkd_append_args& a, int sms, cudaStream_t s) {
   // Heads a group takes: one while the call leaves SMs idle, two once there is work for every SM
   // several times over, which keeps more bytes under way.  One token of 32 + 2 * 8 heads of 128, a
   // replayed graph: 4.8 us with one, 5.5 with two.  Calls in a stream, with one and with two: the 8,190
@@ -637,34 +637,38 @@ cudaError_t launch_d(const pkd_append_args& a, cudaStream_t s) {
   // 28.5 and 23.2, 41.8 and 39.7, 58.9 and 56.4.  (Two heads' instances for codes spill: 64 to 72
   // bytes a thread into e4m3, 264 to 324 into 4 bits; one head's 0 and 128 to 136.)
   const int64_t rows = a.num_tokens * (a.num_qo_heads + 2 * (int64_t)a.pool.num_kv_heads);
-  if (rows * (D / 8) >= 4 * 152 * 2048) return launch_r<T, KV, D, 2>(a, s);
-  return launch_r<T, KV, D, 1>(a, s);
+  if (rows * (D / 8) >= (int64_t)8192 * sms) return launch_r<T, KV, D, 2>(a, sms, s);
+  return launch_r<T, KV, D, 1>(a, sms, s);
 }
 
 template <typename T, int KV>
-cudaError_t launch_kv(const pkd_append_args& a, cudaStream_t s) {
+cudaError_t launch_kv(const pkd_append_args& a, int sms, cudaStream_t s) {
   switch (a.pool.head_dim) {
-    case 64: return launch_d<T, KV, 64>(a, s);
-    case 128: return launch_d<T, KV, 128>(a, s);
-    default: return launch_d<T, KV, 256>(a, s);
+    case 64: return launch_d<T, KV, 64>(a, sms, s);
+    case 128: return launch_d<T, KV, 128>(a, sms, s);
+    default: return launch_d<T, KV, 256>(a, sms, s);
   }
 }
 
 template <typename T>
-cudaError_t launch_t(const pkd_append_args& a, cudaStream_t s) {
+cudaError_t launch_t(const pkd_append_args& a, int sms, cudaStream_t s) {
   switch (a.pool.dtype) {
-    case PKD_DTYPE_E4M3: return launch_kv<T, kFp8>(a, s);
-    case PKD_DTYPE_E2M1: return launch_kv<T, kFp4>(a, s);
+    case PKD_DTYPE_E4M3: return launch_kv<T, kFp8>(a, sms, s);
+    case PKD_DTYPE_E2M1: return launch_kv<T, kFp4>(a, sms, s);
     default:
-      if (a.pool.k_scale != 1.f || a.pool.v_scale != 1.f) return launch_kv<T, kOver16>(a, s);
-      return launch_kv<T, kSame16>(a, s);
+      if (a.pool.k_scale != 1.f || a.pool.v_scale != 1.f) return launch_kv<T, kOver16>(a, sms, s);
+      return launch_kv<T, kSame16>(a, sms, s);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_append(const pkd_append_args& a, cudaStream_t s) {
-  return a.in_dtype == PKD_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<__half>(a, s);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return a.in_dtype == PKD_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, sms, s) : launch_t<__half>(a, sms, s);
 }
 
 }  // namespace pkd
