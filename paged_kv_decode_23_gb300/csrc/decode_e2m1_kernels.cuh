@@ -313,7 +313,7 @@ __device__ __forceinline__ void load_q_e2m1(const DecodeParams& p, const BlockCo
     amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
     const int qexp = amax > 0.f ? max(ilogbf(amax) - 13, -100) : 0;
-    const float down = exp2f(static_cast<float>(-qexp)), up = exp2f(static_cast<float>(qexp));
+    const float down = __int_as_float((127 - qexp) << 23), up = __int_as_float((127 + qexp) << 23);
     qmul[0] = __shfl_sync(~0u, up, 8 * tig);
     qmul[1] = __shfl_sync(~0u, up, 8 * tig + 4);
 #pragma unroll
