@@ -442,7 +442,7 @@ typedef struct pkd_paged_pool {
  * the cache's type: 16-bit caches of the input's type to nearest, E4M3 to nearest within +-448,
  * E2M1 as described at the top.  The codes of E4M3 and E2M1 are those of exact arithmetic.
  * Sums and products are held in 32 bits (64 where a code's rounding is in doubt).
- *   - A row whose batch index is negative is padding: nothing of it is written or used.
+ *   - A row whose batch index is negative is padding: nothing of it is written or used (it is read).
  *   - A row with no slot (batch index >= batch, position negative or past the sequence's pages)
  *     writes no k and v and sets PKD_STATUS_BAD_TOKEN; a page id outside [0, num_pages) likewise,
  *     with PKD_STATUS_BAD_PAGE.  Its q is still written.  A rotation position outside

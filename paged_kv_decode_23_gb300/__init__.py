@@ -15,5 +15,5 @@ from .decode import (BatchDecodePagedKV, BatchMLAPagedAttention,  # noqa: F401
 
 __all__ = ["BatchDecodePagedKV", "BatchMLAPagedAttention", "CUDAGraphBatchDecodePagedKV",
            "PageAllocator", "PkdError", "append_paged_kv", "check_page_table", "copy_pages",
-           "gather_paged_kv", "graph_workspace_bytes", "mla_graph_workspace_bytes",
+           "gather_paged_kv", "graph_workspace_bytes", "make_cos_sin_cache", "mla_graph_workspace_bytes",
            "mla_plan_host", "noalloc_check_status", "plan_host", "workspace_bytes"]

@@ -124,8 +124,9 @@ def append_paged_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opt
     ``q [tokens, num_qo_heads, head_dim]``, ``k`` / ``v [tokens, num_kv_heads, head_dim]``, fp16 or
     bf16, may be views of one projection's output (any token and head stride, head_dim contiguous).
     Row t is token ``positions[t]`` of sequence ``batch_indices[t]`` (device int32); a negative
-    batch index marks padding: its rows are neither read nor written.  ``kv_indptr [batch + 1]``
-    and ``kv_indices`` (device int32) are the page table that ``BatchDecodePagedKV.plan`` takes.
+    batch index marks padding: its rows are not written, and whatever they hold is not used (they may
+    be read).  ``kv_indptr [batch + 1]`` and ``kv_indices`` (device int32) are the page table that
+    ``BatchDecodePagedKV.plan`` takes.
 
     Each head of q (k) is divided by its root mean square and multiplied by ``q_weight``
     (``k_weight``, ``[head_dim]``, the rows' type or float32) if that is given.  With

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   if (c >= p.hc) c -= p.hc;
   const int h0 = c * R, n = min(R, a.pool.num_kv_heads - h0);
   // heads follow each other at fixed strides
-  const char* src = row_addr<KV>(is_v ? a.pool.v : a.pool.k, a.pool.strides, slot, h0, 2 * gl);
+  const char* src = row_addr<KV>(is_v ? a.pool.v : a.pool.k, a.pool.strides, slot, h0, 16 * gl);
   const int64_t step = a.pool.strides[2] * (KV == kSame16 ? 2 : 1);
   uint4 raw[R][KV == kSame16 ? 2 : 1];
   uint32_t sf[R];
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     }
   }
   if constexpr (KV == kFp4) {
-    const uint8_t* at = scale_addr(is_v ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot, h0, 2 * gl);
+    const uint8_t* at = scale_addr(is_v ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_strides, slot, h0, 16 * gl);
 #pragma unroll
     for (int j = 0; j < R; ++j) sf[j] = j < n ? at[j * a.pool.scale_strides[2]] : 0u;
   }

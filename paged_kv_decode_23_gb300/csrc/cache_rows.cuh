@@ -1,5 +1,5 @@
-// cache_rows.cuh -- device code shared by the kernels that write and read rows of a paged cache:
-// rows of head_dim values spread over head_dim / 8 lanes, eight consecutive values a lane.
+// cache_rows.cuh -- device code shared by the kernels that write and read rows of a paged cache: a
+// row of one head lies over head_dim / 16 lanes, two pieces of eight consecutive values a lane.
 #pragma once
 
 #include "cache_ops.cuh"
@@ -50,19 +50,16 @@ __device__ __forceinline__ Slot find_slot(const pkd_paged_pool& p, int page_log,
   return s;
 }
 
-// Address of eight values (lane gl of the row) of one head in the K or V pool.
+// Address of dim d (a multiple of 8) of one head's row in the K or V pool ...
 template <int KV>
-__device__ __forceinline__ char* row_addr(void* base, const int64_t (&st)[3], const Slot& s, int head,
-                                          int gl) {
+__device__ __forceinline__ char* row_addr(void* base, const int64_t (&st)[3], const Slot& s, int head, int d) {
   constexpr int kUnit = KV == kSame16 ? 2 : 1;  // bytes a stride unit
   return static_cast<char*>(base) +
-         (s.page * st[0] + (int64_t)s.slot * st[1] + (int64_t)head * st[2]) * kUnit +
-         gl * bytes8<KV>();
+         (s.page * st[0] + (int64_t)s.slot * st[1] + (int64_t)head * st[2]) * kUnit + d / 8 * bytes8<KV>();
 }
-__device__ __forceinline__ uint8_t* scale_addr(void* base, const int64_t (&st)[3], const Slot& s,
-                                               int head, int gl) {
-  return static_cast<uint8_t*>(base) + s.page * st[0] + (int64_t)s.slot * st[1] +
-         (int64_t)head * st[2] + (gl >> 1);
+// ... and of the scale byte of its block of a 4-bit cache.
+__device__ __forceinline__ uint8_t* scale_addr(void* base, const int64_t (&st)[3], const Slot& s, int head, int d) {
+  return static_cast<uint8_t*>(base) + s.page * st[0] + (int64_t)s.slot * st[1] + (int64_t)head * st[2] + d / 16;
 }
 
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
