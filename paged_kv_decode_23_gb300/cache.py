@@ -335,6 +335,8 @@ class PageAllocator:
 
     def __init__(self, num_pages: int):
         h = ctypes.c_void_p()
+        if num_pages >= 2 ** 31:  # (ctypes would take it modulo 2^64)
+            raise ValueError("num_pages must lie in [0, 2^31)")
         L.check(L.lib().pkd_pages_create(ctypes.byref(h), int(num_pages)))
         self._h, self.num_pages = h, int(num_pages)
 
@@ -378,8 +380,8 @@ class PageAllocator:
         its own, and src / dst (arrays of one id, else empty) is the copy to make with
         ``copy_pages`` before either sequence appends."""
         p = _page_ids(pages, "pages")
-        if kv_len < 0 or page_size < 1:
-            raise ValueError("kv_len must be >= 0 and page_size >= 1")
+        if not 0 <= kv_len < 2 ** 63 or not 1 <= page_size < 2 ** 31:  # (ctypes would cut them to size)
+            raise ValueError("kv_len must lie in [0, 2^63) and page_size in [1, 2^31)")
         out = np.empty(-(-kv_len // page_size) if kv_len <= p.size * page_size else 0, dtype=np.int32)
         s, d = ctypes.c_int32(), ctypes.c_int32()
         L.check(L.lib().pkd_pages_fork(self._h, p.ctypes.data, p.size, kv_len, page_size,

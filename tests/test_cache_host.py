@@ -396,3 +396,20 @@ def test_gather_outputs_that_overlap():
     for k, v, kst, vst in ((4096, 4096 + 2 * 768, (256, 128), (256, 128)), (4096, 4096 + 512, (512, 128), (512, 128)),
                            (4096, 4096 + 256, (512, 256), (512, 256)), (1 << 20, 4096, (256, 128), (256, 128))):
         assert b"null batch_indices" in call(k, v, kst, vst)
+
+
+def test_allocator_arguments_of_more_bits_than_the_library_s():
+    """Cut to the library's types they would be other, valid numbers: fork would write more page ids than
+    its output holds."""
+    from paged_kv_decode_23_gb300 import PageAllocator, PkdError
+    a = PageAllocator(8)
+    p = a.alloc(8)
+    for kv_len, page_size in ((2 ** 64 + 5, 16), (2 ** 63, 16), (5, 2 ** 32 + 1), (5, 2 ** 31), (100, 2 ** 32 + 16)):
+        with pytest.raises(ValueError):
+            a.fork(p, kv_len, page_size)
+    with pytest.raises(PkdError):
+        a.fork(p, 2 ** 63 - 1, 2 ** 31 - 1)
+    for n in (2 ** 31, 2 ** 64 + 4):
+        with pytest.raises(ValueError):
+            PageAllocator(n)
+    assert a.uses().tolist() == [1] * 8
