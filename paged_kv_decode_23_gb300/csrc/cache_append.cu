@@ -24,10 +24,13 @@
 //
 // Bound: every input byte is read once and every output byte written once.  A 16-bit cache comes
 // near that: 8,190 tokens of 64 + 2 * 8 heads of 128, fp16, norm and rotation, 340 MB: 63 us, 5.4 TB/s.
-// An 8- or 4-bit cache is bound by instructions (two conversions a computed value, the products
-// rounded to odd of the others): 4,095 tokens of 16 + 2 * 2 heads of 256, bf16 into e4m3, 81 MB:
-// 33 us, 2.5 TB/s, 0.53 warp instructions issued per cycle and scheduler, 44 % of the ALU pipe.  A decode
-// step's call is latency: 3.5 us (4.8 us a replayed graph of one call).
+// Into 8 or 4 bits no pipe is full: the same rows take 96 us into e4m3 (issue 0.57 per cycle and
+// scheduler, ALU pipe 38 %) and 137 us into 4 bits (0.48, 30 %), 4,095 tokens of 16 + 2 * 2 heads of 256
+// from bf16 into e4m3, 81 MB, 33 us (0.53, 44 %).  What bounds them is latency at 16 warps an SM: 128
+// registers a thread are all that four CTAs leave, instances for codes spill (launch_d), and each
+// instruction waits for its warp's last.  The instructions themselves are two conversions a computed
+// value and the products rounded to odd of the others.  A decode step's call is latency: 3.5 us (4.8 us
+// a replayed graph of one call).
 #include <type_traits>
 
 #include "cache_rows.cuh"

@@ -5,7 +5,7 @@
 // pool; pieces of all pools count up within a pair, so that pools of different page sizes (codes
 // and scales) mix.  The lists' 24 KB cost nothing that shows: with a second instance for lists of
 // up to 64 pools and pairs, a copy of 4 pages in 16 pools took the same time on the host
-// (16 us, most of it spent on looking at the tensors) and in a replayed graph (4.15 us).
+// (16 to 17 us, most of it spent on looking at the tensors) and in a replayed graph (4.15 us).
 // Bound: bytes.  786 MB of pages, read and written: 229 us, 6.87 TB/s, what a plain copy reaches.
 #include "cache_ops.cuh"
 
