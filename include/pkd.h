@@ -447,6 +447,7 @@ typedef struct pkd_paged_pool {
  *     writes no k and v and sets PKD_STATUS_BAD_TOKEN; a page id outside [0, num_pages) likewise,
  *     with PKD_STATUS_BAD_PAGE.  Its q is still written.  A rotation position outside
  *     [0, cos_sin_rows) leaves the whole row out, with PKD_STATUS_BAD_TOKEN.
+ *   - The pool's rows must not overlap, nor K and V be one pool (INVALID_ARG).
  *   - Two rows of one call must not have the same slot (nor one sequence share a page that it
  *     appends to with another: see pkd_pages_fork).
  * eps: 0 or a normal 32-bit number.

@@ -7,6 +7,7 @@
 #include <exception>
 #include <new>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "cache_ops.cuh"
@@ -84,6 +85,31 @@ int check_pool(const pkd_paged_pool& p, int io_dtype, bool used) {
   return PKD_OK;
 }
 
+// Whether rows of `row` units at these strides of (page, slot, head) lie apart: each axis clears what the
+// shorter ones span.
+bool rows_apart(const pkd_paged_pool& p, const int64_t (&st)[3], int64_t row) {
+  int64_t axis[3][2] = {{st[0], p.num_pages}, {st[1], p.page_size}, {st[2], p.num_kv_heads}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (axis[j][0] > axis[j + 1][0]) std::swap(axis[j], axis[j + 1]);
+  for (auto& a : axis) {
+    if (a[1] <= 1) continue;
+    if (a[0] < row) return false;
+    row += (a[1] - 1) * a[0];
+  }
+  return true;
+}
+
+// A pool that is written: no two of its rows may share bytes.
+int check_written(const pkd_paged_pool& p) {
+  const bool codes = p.dtype == PKD_DTYPE_E2M1;
+  if (p.k == p.v || !rows_apart(p, p.strides, codes ? p.head_dim / 2 : p.head_dim))
+    return bad("the K and V pools are one, or their rows overlap");
+  if (codes && (p.k_scales == p.v_scales || !rows_apart(p, p.scale_strides, p.head_dim / 16)))
+    return bad("the scale pools are one, or their rows overlap");
+  return PKD_OK;
+}
+
 int check_rows(const void* p, const int64_t (&st)[2], const char* name) {
   if (!p) return bad(std::string(name) + " is null");
   if (!on16(p)) return bad(std::string(name) + " must be 16-byte aligned");
@@ -157,6 +183,7 @@ extern "C" int pkd_append(const pkd_append_args* args, void* stream) {
       if (int rc = check_out(a.q_out, a.q_out_strides, a.num_tokens, a.num_qo_heads, a.pool.head_dim, "q_out")) return rc;
     }
     if (kv) {
+      if (int rc = check_written(a.pool)) return rc;
       if (int rc = check_rows(a.k, a.k_strides, "k")) return rc;
       if (int rc = check_rows(a.v, a.v_strides, "v")) return rc;
     }

@@ -413,3 +413,26 @@ def test_allocator_arguments_of_more_bits_than_the_library_s():
         with pytest.raises(ValueError):
             PageAllocator(n)
     assert a.uses().tolist() == [1] * 8
+
+
+@pytest.mark.parametrize("over", [
+    dict(v=4096), dict(st=(4096, 128, 128)), dict(st=(2048, 256, 128)), dict(st=(4096, 256, 64)), dict(st=(128, 2048, 512)),
+    dict(dtype=3, st=(4096, 128, 32), ks=64, vs=4096, sst=(512, 16, 8)),
+    dict(dtype=3, st=(4096, 128, 64), ks=64, vs=4096, sst=(512, 8, 8)),
+    dict(dtype=3, st=(4096, 128, 64), ks=64, vs=64, sst=(512, 16, 8)),
+], ids=str)
+def test_append_into_a_pool_that_overlaps_itself(over):
+    from paged_kv_decode_23_gb300 import _lib as L
+    # (without batch indices: no call gets as far as a launch)
+    assert L.lib().pkd_append(_append_args(**{**dict(kr=1 << 20, vr=2 << 20, bi=0), **over}), None) == -1
+    assert b"overlap" in L.lib().pkd_last_error()
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(st=(4096, 128, 2048)), dict(st=(256, 4096, 128)), dict(st=(128, 2048, 1024)), dict(hkv=1, st=(4096, 256, 8)),
+    dict(pages=1, st=(8, 256, 128)), dict(dtype=2, st=(4096, 256, 128)), dict(dtype=3, st=(2048, 128, 64), ks=64, vs=4096, sst=(256, 16, 8)),
+], ids=str)
+def test_append_into_pools_of_any_axis_order(over):
+    from paged_kv_decode_23_gb300 import _lib as L
+    assert L.lib().pkd_append(_append_args(**{**dict(kr=1 << 20, vr=2 << 20, bi=0), **over}), None) == -1
+    assert b"null batch_indices" in L.lib().pkd_last_error()
