@@ -38,8 +38,8 @@
  *   request has no page); token t of request i is slot t % page_size of page
  *   indices[indptr[i] + t / page_size]; qo head g reads kv head g / (Hq / Hkv);
  *   x_t = sm_scale * q_scale * k_scale * <q, K_t>; s_t = cap * tanh(x_t / cap) if cap > 0
- *   else x_t; the attended keys are t >= kv_len - 1 - window_left (all keys if
- *   window_left < 0); o = v_scale * sum_t softmax(s)_t V_t; lse = ln(sum_t exp(s_t)).
+ *   else x_t; the attended keys are t >= kv_len - 1 - window_left, and t < num_sink_tokens (all
+ *   keys if window_left < 0); o = v_scale * sum_t softmax(s)_t V_t; lse = ln(sum_t exp(s_t)).
  *   A request with no attended key gets o = 0 and lse = -inf.
  */
 #ifndef PKD_H_
@@ -327,6 +327,55 @@ int pkd_workspace_bytes(const int32_t* indptr_host, const int32_t* last_page_len
                         int page_size, int window_left, int fixed_split_size,
                         int disable_split_kv, int kv_dtype, int use_tensor_cores, int num_sms,
                         int q_len_per_req, size_t* float_ws_bytes, size_t* int_ws_bytes);
+
+/*
+ * pkd_plan with its arguments in one struct, and what pkd_plan does not have:
+ *   num_sink_tokens  with window_left >= 0: a row at position p (kv_len - 1 with one query token per
+ *                    request) attends the keys t < num_sink_tokens beside those with
+ *                    t >= p - window_left.  Keys in between are not read: their pages may be freed
+ *                    and their entries of `indices` may hold anything.  Positions (ALiBi, RoPE)
+ *                    stay the tokens' own.  No effect with window_left < 0.
+ * pkd_plan(...) is pkd_plan_with with 0 for these.
+ */
+typedef struct pkd_plan_args {
+  const int32_t* indptr_host;
+  const int32_t* last_page_len_host;
+  const int32_t* indices_dev;
+  int64_t num_indices;
+  float sm_scale; /* NaN: 1 / sqrt(head_dim) */
+  float logits_soft_cap;
+  float rope_scale;
+  float rope_theta;
+  int32_t batch;
+  int32_t num_qo_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t window_left;
+  int32_t fixed_split_size;
+  int32_t disable_split_kv;
+  int32_t q_dtype;
+  int32_t kv_dtype;
+  int32_t o_dtype;
+  int32_t use_tensor_cores;
+  int32_t q_len_per_req;
+  int32_t pos_encoding_mode;
+  int32_t num_sink_tokens;
+  int32_t reserved;
+} pkd_plan_args;
+int pkd_plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream);
+
+/*
+ * The work list (as pkd_plan_host gives it, below) and the workspaces of such a plan, on the host
+ * alone (device pointers and the stream are not used; num_sms <= 0 means 152).  A task has 14 int32:
+ * pkd_plan_host's 12, then the sinks that it attends before its piece of the window, tokens
+ * [sink_begin, sink_end), both 0 for none.
+ */
+int pkd_plan_tasks(const pkd_plan_args* args, int num_sms, int work_capacity, int32_t* tasks_out,
+                   int max_tasks, int32_t* merges_out, int max_merges, int* n_tasks, int* n_merges,
+                   int* n_slots);
+int pkd_plan_workspace_bytes(const pkd_plan_args* args, int num_sms, size_t* float_ws_bytes,
+                             size_t* int_ws_bytes);
 
 /*
  * The decode planner alone (host-only; no CUDA call), for inspection and tests.  The plan

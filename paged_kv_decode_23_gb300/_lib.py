@@ -42,7 +42,12 @@ SIGNATURES = {
                          _vp, _vp, _vp]),
     "pkd_run_timed": (_c_int, [_vp, _vp, _vp, _vp, ctypes.c_int64, _i64p, _c_float, _c_float,
                                _c_float, _vp, _vp, _vp, _vp, _vp]),
-    # the argument structs of these three travel as packed bytes (decode.py, cache.py)
+    # the argument structs of these travel as packed bytes (decode.py, cache.py)
+    "pkd_plan_with": (_c_int, [_vp, ctypes.c_char_p, _vp]),
+    "pkd_plan_tasks": (_c_int, [ctypes.c_char_p, _c_int, _c_int, _vp, _c_int, _vp, _c_int] +
+                       [ctypes.POINTER(_c_int)] * 3),
+    "pkd_plan_workspace_bytes": (_c_int, [ctypes.c_char_p, _c_int, ctypes.POINTER(_c_size),
+                                          ctypes.POINTER(_c_size)]),
     "pkd_run_scaled": (_c_int, [_vp, ctypes.c_char_p, _vp]),
     "pkd_append": (_c_int, [ctypes.c_char_p, _vp]),
     "pkd_gather": (_c_int, [ctypes.c_char_p, _vp]),

@@ -158,18 +158,20 @@ __device__ __forceinline__ int e2m1_tok(int j) {
   return j;
 }
 
-// The ids of a task's pages, 32 at a time over the lanes, the next 32 under way: page ids would
-// otherwise be a load that every tile's copies wait for.  The pages of a tile never straddle two
-// windows (a tile holds a power of two of them, at most 32).
+// The ids of the pages of a run of tokens (a task's sinks, or its window), 32 at a time over the lanes,
+// the next 32 under way: page ids would otherwise be a load that every tile's copies wait for.  The
+// pages of a tile never straddle two windows (a tile holds a power of two of them, at most 32).
 struct PageWindow {
-  const int32_t* ids;  // the chunk's first page id
-  int n;               // pages of the chunk
+  const int32_t* ids;  // the run's first page id
+  int n;               // its pages
   int w;               // cur holds pages 32w .. 32w + 31
   int cur, nxt;
   __device__ __forceinline__ int load(int at) const { return at < n ? __ldg(ids + at) : 0; }
-  __device__ __forceinline__ PageWindow(const DecodeParams& p, const BlockCoords& b, int first, int lane)
-      : ids(p.indices + b.it.page_base + b.it.chunk_tok0 / p.page_size),
-        n((b.it.tok_end - b.it.chunk_tok0 + p.page_size - 1) / p.page_size), w(first >> 5) {
+  // tokens [tok0, end), tok0 a page boundary; the first page wanted is the run's page `first`
+  __device__ __forceinline__ PageWindow(const DecodeParams& p, const BlockCoords& b, int tok0, int end,
+                                        int first, int lane)
+      : ids(p.indices + b.it.page_base + tok0 / p.page_size),
+        n((end - tok0 + p.page_size - 1) / p.page_size), w(first >> 5) {
     cur = load(32 * w + lane);
     nxt = load(32 * w + 32 + lane);
   }
@@ -202,25 +204,32 @@ __device__ __forceinline__ void produce_e2m1(const DecodeE2m1Params& p, const Bl
   // pages of up to 32 slots put a lane's tokens into one slot, tile after tile
   const int64_t lane_slot = (int64_t)(lane & (ps - 1)) * p.sf_stride[1];
   if (lane == 0) prefetch_tmap(&p.tmap_k);
-  PageWindow win(p, b, b.j0 * TS / ps, lane);
+  const bool sinks = b.ns > 0;
+  int run0 = sinks ? b.it.sink_begin : b.it.chunk_tok0;  // first token of the window's run of pages
+  PageWindow win(p, b, run0, sinks ? b.it.sink_end : b.it.tok_end, (tile_span<TS>(b, 0).t0 - run0) / ps, lane);
   int issued = 0, s = 0;
   uint32_t phase = 1;
   bool ok = true, bad_page = false;
   for (int i = 0; i < b.ntiles; ++i) {
-    const int tile0 = (b.j0 + i) * TS;  // from the chunk's first token
-    const int t0 = b.it.chunk_tok0 + tile0;
+    const TileSpan ts = tile_span<TS>(b, i);
+    const int t0 = ts.t0;
+    if (sinks && i == b.ns) {  // from the sinks to the window
+      run0 = b.it.chunk_tok0;
+      win = PageWindow(p, b, run0, b.it.tok_end, (t0 - run0) / ps, lane);
+    }
+    const int tile0 = t0 - run0;
     const int bt0 = t0 + lane * br;
-    const bool need = lane < boxes && bt0 < b.it.tok_end && bt0 + br > b.it.tok_begin;
+    const bool need = lane < boxes && bt0 < ts.hi && bt0 + br > ts.lo;
     win.move(tile0 >> ps_log, lane);
     const int pid = win.id((tile0 + lane * br) >> ps_log);  // (lanes past the boxes: any page)
-    const bool whole = t0 >= b.it.tok_begin && t0 + TS <= b.it.tok_end;
+    const bool whole = t0 >= ts.lo && t0 + TS <= ts.hi;
     const uint8_t* src[TS / 32];
     bool valid[TS / 32];
 #pragma unroll
     for (int k = 0; k < TS / 32; ++k) {
       const int j = lane + 32 * k;
       const uint32_t id = (uint32_t)win.id((tile0 + j) >> ps_log);
-      valid[k] = id < p.num_pages && (whole || (t0 + j >= b.it.tok_begin && t0 + j < b.it.tok_end));
+      valid[k] = id < p.num_pages && (whole || (t0 + j >= ts.lo && t0 + j < ts.hi));
       src[k] = ksf + (valid[k] ? id : 0u) * p.sf_stride[0] +
                (ps <= 32 ? lane_slot : (int64_t)((tile0 + j) & (ps - 1)) * p.sf_stride[1]);
     }
@@ -402,14 +411,15 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
   int s = 0;
   uint32_t phase = 0;
   for (int i = 0; i < b.ntiles; ++i) {
-    const int t_w = b.it.chunk_tok0 + (b.j0 + i) * TS + warp * 16;  // first token of slice 0
+    const TileSpan ts = tile_span<TS>(b, i);
+    const int t_w = ts.t0 + warp * 16;  // first token of slice 0
     if (!__all_sync(~0u, mbar_wait(full0 + 8 * s, phase, abort_flag, p.wait_ns))) {
       *abort_flag = 1;  // warp-uniform: the warp leaves the loop together
       atomicOr(p.status, kStatusTimeout);
       break;
     }
     // attended tokens [lo, hi), counted from t_w
-    const int lo = b.it.tok_begin - t_w, hi = b.it.tok_end - t_w;
+    const int lo = ts.lo - t_w, hi = ts.hi - t_w;
     const uint32_t st = stage_after_wait(smem + s * G::STAGE_BYTES);
     bool work = hi > 0 && lo < 16;
 #pragma unroll

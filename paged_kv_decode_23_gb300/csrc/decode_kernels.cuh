@@ -84,9 +84,21 @@ struct BlockCoords {
   int g0;     // first qo head of this task
   int gcnt;   // qo heads of this task
   int gs;     // which slice of the kv head's qo-head group
-  int j0;     // first tile (relative to the chunk start)
+  int ns;     // tiles of the task's sinks, before those of its window
+  int main0;  // token of tile 0, were the window's tiles counted back to it
   int ntiles;
 };
+
+// Tile i of a task: its first token and the attended tokens [lo, hi) around it.
+struct TileSpan {
+  int t0, lo, hi;
+};
+template <int TS>
+__device__ __forceinline__ TileSpan tile_span(const BlockCoords& b, int i) {
+  const bool sink = i < b.ns;
+  return {(sink ? b.it.sink_begin : b.main0) + i * TS, sink ? b.it.sink_begin : b.it.tok_begin,
+          sink ? b.it.sink_end : b.it.tok_end};
+}
 
 template <int TS, int HEADS>
 __device__ __forceinline__ BlockCoords task_coords(const DecodeParams& p) {
@@ -96,12 +108,13 @@ __device__ __forceinline__ BlockCoords task_coords(const DecodeParams& p) {
   b.gs = b.it.gs;
   b.g0 = b.kvh * p.group + b.gs * HEADS;
   b.gcnt = min(HEADS, p.group - b.gs * HEADS);
+  b.ns = (b.it.sink_end - b.it.sink_begin + TS - 1) / TS;
+  b.main0 = 0;
+  b.ntiles = 0;
   if (b.it.tok_end > b.it.tok_begin) {
-    b.j0 = (b.it.tok_begin - b.it.chunk_tok0) / TS;
-    b.ntiles = (b.it.tok_end - b.it.chunk_tok0 + TS - 1) / TS - b.j0;
-  } else {
-    b.j0 = 0;
-    b.ntiles = 0;
+    const int j0 = (b.it.tok_begin - b.it.chunk_tok0) / TS;  // the window's first tile in the chunk
+    b.main0 = b.it.chunk_tok0 + (j0 - b.ns) * TS;
+    b.ntiles = (b.it.tok_end - b.it.chunk_tok0 + TS - 1) / TS - j0 + b.ns;
   }
   return b;
 }
@@ -131,9 +144,9 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const BlockCoords
       ok = false;
       break;
     }
-    const int t0 = b.it.chunk_tok0 + (b.j0 + i) * TS;
-    const int bt0 = t0 + lane * br;
-    const bool need = lane < boxes && bt0 < b.it.tok_end && bt0 + br > b.it.tok_begin;
+    const TileSpan ts = tile_span<TS>(b, i);
+    const int bt0 = ts.t0 + lane * br;
+    const bool need = lane < boxes && bt0 < ts.hi && bt0 + br > ts.lo;
     int pid = 0;
     if (need) pid = __ldg(p.indices + b.it.page_base + bt0 / ps);
     bad_page |= need && (uint32_t)pid >= p.num_pages;
@@ -584,7 +597,8 @@ __device__ __forceinline__ void consume_tc(const DecodeParams& p, const BlockCoo
 
   for (int i = 0; i < b.ntiles; ++i) {
     const int s = i % NSTAGES;
-    const int t_w = b.it.chunk_tok0 + (b.j0 + i) * TS + warp * 16;  // first token of my slice
+    const TileSpan ts = tile_span<TS>(b, i);
+    const int t_w = ts.t0 + warp * 16;  // first token of my slice
     // ROPE: the slice's q rotation, while the stage may still be loading
     if constexpr (ROPE)
       rope_build_e<D, KV_FP8>(rope_e + (i & 1) * RG::ROW, rope_rates, (float)(b.it.q_pos - t_w), lane);
@@ -593,8 +607,8 @@ __device__ __forceinline__ void consume_tc(const DecodeParams& p, const BlockCoo
       atomicOr(p.status, kStatusTimeout);
       break;
     }
-    const int vlo = max(0, b.it.tok_begin - t_w);
-    const int vhi = min(16, b.it.tok_end - t_w);
+    const int vlo = max(0, ts.lo - t_w);
+    const int vhi = min(16, ts.hi - t_w);
     const uint32_t ktile = stage_after_wait(smem + s * G::STAGE_BYTES);
     uint32_t vtile = ktile + G::TILE_BYTES;
     const int r0 = warp * 16;  // first tile row of my slice
@@ -1113,7 +1127,8 @@ __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoo
 
   for (int i = 0; i < b.ntiles; ++i) {
     const int s = i % NSTAGES;
-    const int t_w = b.it.chunk_tok0 + (b.j0 + i) * TS + warp * 16;  // first token of my slice
+    const TileSpan ts = tile_span<TS>(b, i);
+    const int t_w = ts.t0 + warp * 16;  // first token of my slice
     if constexpr (ROPE)
       cc_rotate_q<TQ, KV_FP8, D, GP, G::NW>(p, b, qr, (float)(b.it.q_pos - t_w - 8), lane);
     if (!__all_sync(~0u, mbar_wait(full0 + 8 * s, (i / NSTAGES) & 1, abort_flag, p.wait_ns))) {
@@ -1121,8 +1136,8 @@ __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoo
       atomicOr(p.status, kStatusTimeout);
       break;
     }
-    const int vlo = max(0, b.it.tok_begin - t_w);
-    const int vhi = min(16, b.it.tok_end - t_w);
+    const int vlo = max(0, ts.lo - t_w);
+    const int vhi = min(16, ts.hi - t_w);
     const uint32_t ktile = stage_after_wait(smem + s * G::STAGE_BYTES);
     const uint32_t vtile = ktile + G::TILE_BYTES;
     if (vlo < vhi) {  // warp-uniform

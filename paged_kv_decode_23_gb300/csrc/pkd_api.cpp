@@ -11,9 +11,12 @@
 
 #include <cmath>
 #include <cstdio>
+#include <algorithm>
 #include <cstring>
+#include <exception>
 #include <limits>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -395,6 +398,72 @@ int plan_decode(const PlanRequest& r, int ctas, ScheduleStore& st, DecodeSchedul
   }
 }
 
+// The request of a plan, its numbers checked as far as they do not depend on a handle.
+int plan_request_of(const pkd_plan_args& a, int num_sms, PlanRequest* r) {
+  int rc = fill_plan_request(r, a.indptr_host, a.last_page_len_host, a.batch, a.num_qo_heads,
+                             a.num_kv_heads, a.head_dim, a.page_size, a.window_left,
+                             a.fixed_split_size, a.disable_split_kv, a.kv_dtype, a.use_tensor_cores,
+                             num_sms, a.q_len_per_req);
+  if (rc) return rc;
+  if (a.num_sink_tokens < 0) return fail(PKD_ERR_INVALID_ARG, "num_sink_tokens must be >= 0");
+  r->num_sinks = a.num_sink_tokens;
+  return PKD_OK;
+}
+
+// The tasks and merge entries of a plan on the host: `width` int32 a task.
+int plan_host(const PlanRequest& r, int num_sms, int width, int32_t* tasks_out, int max_tasks,
+              int32_t* merges_out, int max_merges, int* n_tasks, int* n_merges, int* n_slots,
+              int* kernel_out, int* tile_tokens_out, int* n_ctas) {
+  ScheduleStore st;
+  DecodeSchedule sch;
+  const int rc = plan_decode(r, (num_sms > 0 ? num_sms : 152) * decode_max_ctas(r), st, &sch);
+  if (rc) return rc;
+  if (n_tasks) *n_tasks = (int)sch.n_tasks;
+  if (n_merges) *n_merges = (int)sch.n_merges;
+  if (n_slots) *n_slots = (int)sch.n_slots;
+  if (kernel_out) *kernel_out = sch.kind;
+  if (tile_tokens_out) *tile_tokens_out = sch.tile_tokens;
+  if (n_ctas) *n_ctas = (int)sch.n_tasks;
+  for (int64_t i = 0; tasks_out && i < std::min<int64_t>(sch.n_tasks, max_tasks); ++i) {
+    const DecodeTask& t = st.tasks[(size_t)i];
+    const int32_t v[14] = {t.req,       t.page_base, t.chunk_tok0, t.tok_begin, t.tok_end,
+                           t.out_slot,  t.merge_idx, t.q_pos,      t.kvh,       t.gs,
+                           (int32_t)i,  0,           t.sink_begin, t.sink_end};
+    std::memcpy(tasks_out + i * width, v, (size_t)width * sizeof(int32_t));
+  }
+  if (merges_out)
+    std::memcpy(merges_out, st.merges.data(),
+                sizeof(MergeEntry) *
+                    std::min<size_t>((size_t)sch.n_merges, (size_t)std::max(0, max_merges)));
+  g_last_error.clear();
+  return PKD_OK;
+}
+
+int plan_bytes(const PlanRequest& r, int num_sms, size_t* float_ws_bytes, size_t* int_ws_bytes) {
+  ScheduleStore st;
+  DecodeSchedule sch;
+  const int ctas = (num_sms > 0 ? num_sms : 152) * decode_max_ctas(r);
+  const int rc = plan_decode(r, ctas, st, &sch);
+  if (rc) return rc;
+  DecodeWsLayout lay{(size_t)sch.n_tasks, (size_t)sch.n_merges, (size_t)sch.n_slots};
+  lay.pos_floats = 2 * (size_t)r.head_dim + r.num_qo_heads;  // room for a positional encoding
+  if (float_ws_bytes) *float_ws_bytes = dws_float_bytes(lay, r.head_dim);
+  if (int_ws_bytes) *int_ws_bytes = dws_int_bytes(lay);
+  return PKD_OK;
+}
+
+// A failing call must not throw across the C boundary (plans and messages allocate).
+template <typename F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return fail(PKD_ERR_INVALID_ARG, "out of host memory");
+  } catch (const std::exception& e) {
+    return fail(PKD_ERR_INVALID_ARG, e.what());
+  }
+}
+
 }  // namespace
 
 namespace pkd {
@@ -479,26 +548,31 @@ int pkd_plan_host(const int32_t* indptr_host, const int32_t* last_page_len_host,
                              q_len_per_req);
   if (rc) return rc;
   r.max_items = work_capacity > 0 ? work_capacity : 0;
-  ScheduleStore st;
-  DecodeSchedule sch;
-  rc = plan_decode(r, (num_sms > 0 ? num_sms : 152) * decode_max_ctas(r), st, &sch);
-  if (rc) return rc;
-  if (n_tasks) *n_tasks = (int)sch.n_tasks;
-  if (n_merges) *n_merges = (int)sch.n_merges;
-  if (n_slots) *n_slots = (int)sch.n_slots;
-  if (kernel_out) *kernel_out = sch.kind;
-  if (tile_tokens_out) *tile_tokens_out = sch.tile_tokens;
-  if (n_ctas) *n_ctas = (int)sch.n_tasks;
-  if (tasks_out)
-    std::memcpy(tasks_out, st.tasks.data(),
-                sizeof(DecodeTask) *
-                    std::min<size_t>((size_t)sch.n_tasks, (size_t)std::max(0, max_tasks)));
-  if (merges_out)
-    std::memcpy(merges_out, st.merges.data(),
-                sizeof(MergeEntry) *
-                    std::min<size_t>((size_t)sch.n_merges, (size_t)std::max(0, max_merges)));
-  g_last_error.clear();
-  return PKD_OK;
+  return plan_host(r, num_sms, 12, tasks_out, max_tasks, merges_out, max_merges, n_tasks, n_merges,
+                   n_slots, kernel_out, tile_tokens_out, n_ctas);
+}
+
+int pkd_plan_tasks(const pkd_plan_args* args, int num_sms, int work_capacity, int32_t* tasks_out,
+                   int max_tasks, int32_t* merges_out, int max_merges, int* n_tasks, int* n_merges,
+                   int* n_slots) {
+  return guarded([&]() -> int {
+    if (!args) return fail(PKD_ERR_INVALID_ARG, "args is null");
+    PlanRequest r;
+    if (int rc = plan_request_of(*args, num_sms, &r)) return rc;
+    r.max_items = work_capacity > 0 ? work_capacity : 0;
+    return plan_host(r, num_sms, 14, tasks_out, max_tasks, merges_out, max_merges, n_tasks, n_merges,
+                     n_slots, nullptr, nullptr, nullptr);
+  });
+}
+
+int pkd_plan_workspace_bytes(const pkd_plan_args* args, int num_sms, size_t* float_ws_bytes,
+                             size_t* int_ws_bytes) {
+  return guarded([&]() -> int {
+    if (!args) return fail(PKD_ERR_INVALID_ARG, "args is null");
+    PlanRequest r;
+    if (int rc = plan_request_of(*args, num_sms, &r)) return rc;
+    return plan_bytes(r, num_sms, float_ws_bytes, int_ws_bytes);
+  });
 }
 
 int pkd_workspace_bytes(const int32_t* indptr_host, const int32_t* last_page_len_host, int batch,
@@ -512,25 +586,25 @@ int pkd_workspace_bytes(const int32_t* indptr_host, const int32_t* last_page_len
                              disable_split_kv, kv_dtype, use_tensor_cores, num_sms,
                              q_len_per_req);
   if (rc) return rc;
-  ScheduleStore st;
-  DecodeSchedule sch;
-  const int ctas = (num_sms > 0 ? num_sms : 152) * decode_max_ctas(r);
-  rc = plan_decode(r, ctas, st, &sch);
-  if (rc) return rc;
-  DecodeWsLayout lay{(size_t)sch.n_tasks, (size_t)sch.n_merges, (size_t)sch.n_slots};
-  lay.pos_floats = 2 * (size_t)head_dim + num_qo_heads;  // room for a positional encoding
-  if (float_ws_bytes) *float_ws_bytes = dws_float_bytes(lay, head_dim);
-  if (int_ws_bytes) *int_ws_bytes = dws_int_bytes(lay);
-  return PKD_OK;
+  return plan_bytes(r, num_sms, float_ws_bytes, int_ws_bytes);
 }
 
-int pkd_plan(pkd_handle* h, const int32_t* indptr_host, const int32_t* last_page_len_host,
-             int batch, const int32_t* indices_dev, int64_t num_indices, int num_qo_heads,
-             int num_kv_heads, int head_dim, int page_size, float sm_scale, float logits_soft_cap,
-             int window_left, int fixed_split_size, int disable_split_kv, int q_dtype,
-             int kv_dtype, int o_dtype, int use_tensor_cores, int q_len_per_req,
-             int pos_encoding_mode, float rope_scale, float rope_theta, void* stream) {
-  if (!h) return fail(PKD_ERR_INVALID_ARG, "handle is null");
+}  // extern "C"
+
+namespace {
+
+int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
+  if (!h || !args) return fail(PKD_ERR_INVALID_ARG, "handle or args is null");
+  const int32_t* indptr_host = args->indptr_host;
+  const int32_t* last_page_len_host = args->last_page_len_host;
+  const int32_t* indices_dev = args->indices_dev;
+  const int64_t num_indices = args->num_indices;
+  const int batch = args->batch, num_qo_heads = args->num_qo_heads, num_kv_heads = args->num_kv_heads;
+  const int head_dim = args->head_dim, page_size = args->page_size;
+  const int q_dtype = args->q_dtype, kv_dtype = args->kv_dtype, o_dtype = args->o_dtype;
+  const int q_len_per_req = args->q_len_per_req, pos_encoding_mode = args->pos_encoding_mode;
+  const float sm_scale = args->sm_scale, logits_soft_cap = args->logits_soft_cap;
+  const float rope_scale = args->rope_scale, rope_theta = args->rope_theta;
   h->planned = false;
   if (q_dtype != PKD_DTYPE_F16 && q_dtype != PKD_DTYPE_BF16)
     return fail(PKD_ERR_INVALID_ARG, "q_dtype must be F16 or BF16");
@@ -540,6 +614,8 @@ int pkd_plan(pkd_handle* h, const int32_t* indptr_host, const int32_t* last_page
   if (kv_dtype == PKD_DTYPE_E2M1 && pos_encoding_mode == PKD_POS_ROPE_LLAMA)
     return fail(PKD_ERR_UNSUPPORTED,
                 "ROPE_LLAMA is not built for E2M1 KV (rotate the keys as they are appended)");
+  if (batch > 0 && (!indptr_host || !last_page_len_host))
+    return fail(PKD_ERR_INVALID_ARG, "batch must be >= 0 and the page table pointers non-null");
   if (batch > 0 && !indices_dev) return fail(PKD_ERR_INVALID_ARG, "indices_dev is null");
   if (batch > 0 && num_indices < (int64_t)indptr_host[batch])
     return fail(PKD_ERR_INVALID_ARG, "indices holds fewer than indptr[batch] page ids");
@@ -572,10 +648,7 @@ int pkd_plan(pkd_handle* h, const int32_t* indptr_host, const int32_t* last_page
   }
 
   PlanRequest r;
-  int rc = fill_plan_request(&r, indptr_host, last_page_len_host, batch, num_qo_heads,
-                             num_kv_heads, head_dim, page_size, window_left, fixed_split_size,
-                             disable_split_kv, kv_dtype, use_tensor_cores, h->num_sms,
-                             q_len_per_req);
+  int rc = plan_request_of(*args, h->num_sms, &r);
   if (rc) return rc;
   if (h->graph) r.max_items = h->g_max_items;
   r.rope = pos_encoding_mode == PKD_POS_ROPE_LLAMA ? 1 : 0;
@@ -709,6 +782,47 @@ int pkd_plan(pkd_handle* h, const int32_t* indptr_host, const int32_t* last_page
   h->planned = true;
   g_last_error.clear();
   return PKD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkd_plan(pkd_handle* h, const int32_t* indptr_host, const int32_t* last_page_len_host,
+             int batch, const int32_t* indices_dev, int64_t num_indices, int num_qo_heads,
+             int num_kv_heads, int head_dim, int page_size, float sm_scale, float logits_soft_cap,
+             int window_left, int fixed_split_size, int disable_split_kv, int q_dtype,
+             int kv_dtype, int o_dtype, int use_tensor_cores, int q_len_per_req,
+             int pos_encoding_mode, float rope_scale, float rope_theta, void* stream) {
+  pkd_plan_args a;
+  std::memset(&a, 0, sizeof a);
+  a.indptr_host = indptr_host;
+  a.last_page_len_host = last_page_len_host;
+  a.indices_dev = indices_dev;
+  a.num_indices = num_indices;
+  a.batch = batch;
+  a.num_qo_heads = num_qo_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.page_size = page_size;
+  a.sm_scale = sm_scale;
+  a.logits_soft_cap = logits_soft_cap;
+  a.window_left = window_left;
+  a.fixed_split_size = fixed_split_size;
+  a.disable_split_kv = disable_split_kv;
+  a.q_dtype = q_dtype;
+  a.kv_dtype = kv_dtype;
+  a.o_dtype = o_dtype;
+  a.use_tensor_cores = use_tensor_cores;
+  a.q_len_per_req = q_len_per_req;
+  a.pos_encoding_mode = pos_encoding_mode;
+  a.rope_scale = rope_scale;
+  a.rope_theta = rope_theta;
+  return pkd_plan_with(h, &a, stream);
+}
+
+int pkd_plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
+  return guarded([&]() -> int { return plan_with(h, args, stream); });
 }
 
 }  // extern "C"

@@ -36,9 +36,11 @@ struct MergeEntry {
 };
 static_assert(sizeof(MergeEntry) == 16, "MergeEntry is 4 int32");
 
-// One task of the persistent decode kernel: a chunk of one output row's attended tokens for
-// one kv head and one slice of that head's qo-head group (at most 8 qo heads).  The fields up
-// to q_pos mean what they mean in a WorkItem.  A CTA runs a list of tasks back to back.
+// One task of the decode kernel: a chunk of one output row's attended tokens for one kv head and
+// one slice of that head's qo-head group (at most 8 qo heads).  The fields up to q_pos mean what
+// they mean in a WorkItem.  With sinks (a window's first tokens that stay visible) a task may hold a
+// piece of them before its piece of the window: tokens [sink_begin, sink_end), sink_begin a page
+// boundary; none where both are 0.
 struct DecodeTask {
   int32_t req;         // output row: q / o / lse row index
   int32_t page_base;   // indptr[request]: offset of the request's first page id in `indices`
@@ -51,8 +53,8 @@ struct DecodeTask {
   int32_t q_pos;       // the row's query position (its last key): ALiBi / RoPE
   int32_t kvh;         // kv head
   int32_t gs;          // slice of the kv head's qo-head group
-  int32_t cta;         // the CTA that runs it
-  int32_t pad;
+  int32_t sink_begin;
+  int32_t sink_end;
 };
 static_assert(sizeof(DecodeTask) == 48, "DecodeTask is 12 int32");
 
@@ -199,6 +201,7 @@ struct PlanRequest {
   int head_dim;
   int page_size;
   int window_left;
+  int num_sinks = 0;     // with a window: the first num_sinks tokens are attended as well
   int fixed_split_size;
   int disable_split_kv;
   int kv_dtype;
@@ -235,11 +238,12 @@ int build_plan(const PlanRequest& r, Plan* plan, const char** err);
 // ----------------------------------------------------------------------- decode schedule
 // The decode planner's output, written into storage the caller provides (it allocates
 // nothing: the no-allocation entry point passes static arrays, the handle path vectors).
-// One chunk of one row: [b, e) of its attended tokens (tiles from tile0), chunk q of k; when
-// the row is split (k > 1), unit u of the row takes partial slots slot_base + u k .. + k - 1 and
-// merge entry merge_base + u.
+// One chunk of one row: [b, e) of its attended tokens (tiles from tile0), and before them [sb, se)
+// of its sinks, chunk q of k; when the row is split (k > 1), unit u of the row takes partial slots
+// slot_base + u k .. + k - 1 and merge entry merge_base + u.
 struct DecodeChunk {
-  int32_t row, b, e, tile0, q, k, slot_base, merge_base;
+  int32_t row, b, e, tile0, sb, se, q, k, slot_base, merge_base;
+  int32_t tokens() const { return e - b + se - sb; }
 };
 
 struct DecodeSchedule {

@@ -5,7 +5,7 @@
 //     (across layers);
 //   - indptr / indices / last_page_len describe each request's pages, with
 //     kv_len = page_size * (pages - 1) + last_page_len (batch prefill example);
-//   - window_left keeps the keys t >= kv_len - 1 - window_left;
+//   - window_left keeps the keys t >= kv_len - 1 - window_left, and num_sinks the first tokens;
 //   - fixed_split_size (pages) fixes the split-KV chunk so that the merge, and thus the
 //     output, does not depend on the batch; disable_split_kv keeps one chunk per request.
 // With a fixed split, chunks are cut at multiples of the chunk size counted from the request's
@@ -342,11 +342,24 @@ int64_t request_len(const PlanRequest& r, int i) {
   return pages <= 0 ? 0 : (int64_t)r.page_size * (pages - 1) + r.last_page_len[i];
 }
 
-// Output row `row` (query token j of request i): its key count n, first attended token w and
-// the offset of its request's page ids.
+// Output row `row` (query token j of request i): its key count n, first attended token w of the
+// window, the s sinks before it ([0, s), s < w, or none) and the offset of its request's page ids.
+// The attended tokens are counted through: position v < s is token v, v >= s token w + v - s.
 struct RowSpan {
-  int64_t n, w;
+  int64_t n, w, s;
   int32_t base;
+  int64_t attended() const { return s + n - w; }
+  // the page boundary at or below position v: a position again, s where v's page holds w
+  int64_t snap(int64_t v, int ps) const {
+    if (v <= s) return v == s ? s : v / ps * ps;
+    const int64_t t = (w + v - s) / ps * ps;
+    return t <= w ? s : s + t - w;
+  }
+  // the first page boundary, or border of the sinks, above position v
+  int64_t next(int64_t v, int ps) const {
+    if (v < s) return std::min(s, (v / ps + 1) * ps);
+    return s + ((w + v - s) / ps + 1) * ps - w;
+  }
 };
 RowSpan row_span(const PlanRequest& r, int row) {
   const int ql = r.q_len > 0 ? r.q_len : 1;
@@ -354,16 +367,19 @@ RowSpan row_span(const PlanRequest& r, int row) {
   RowSpan s;
   s.n = std::max<int64_t>(0, request_len(r, i) - (ql - 1 - j));
   s.w = (r.window_left >= 0 && s.n - 1 - r.window_left > 0) ? s.n - 1 - r.window_left : 0;
+  s.s = std::min<int64_t>(r.num_sinks, s.w);
+  if (s.s == s.w) s.s = s.w = 0;  // nothing lies between the sinks and the window
   s.base = r.indptr[i];
   return s;
 }
 
 int rows_of(const PlanRequest& r) { return r.batch * (r.q_len > 0 ? r.q_len : 1); }
 
-// chunks of a row with a fixed chunk of C tokens (C = 0: one)
+// chunks of a row with a fixed chunk of C tokens (C = 0: one): whole chunks of sinks, then the
+// window's, the first of which takes the sinks' rest as well
 int64_t fixed_chunks(const RowSpan& s, int64_t C) {
   if (s.n == 0 || C == 0) return 1;
-  return (s.n - 1) / C - s.w / C + 1;
+  return s.s / C + (s.n - 1) / C - s.w / C + 1;
 }
 
 }  // namespace
@@ -399,6 +415,10 @@ int decode_geometry(const PlanRequest& r, DecodeSchedule* s, const char** err) {
   }
   if (r.q_len < 1) {
     *err = "q_len_per_req must be >= 1";
+    return kErrInvalidD;
+  }
+  if (r.num_sinks < 0) {
+    *err = "num_sink_tokens must be >= 0";
     return kErrInvalidD;
   }
   if ((int64_t)r.batch * r.q_len > (int64_t)std::numeric_limits<int32_t>::max() / 2) {
@@ -462,11 +482,11 @@ struct DecodeChunking {
   int mode;
 };
 
-// End of the first chunk of a row longer than C under kChunkHead (C >= one page).
-int64_t head_cut(const RowSpan& sp, int64_t C, int ps) { return (sp.w + C) / ps * ps; }
+// End (a position) of the first chunk of a row longer than C under kChunkHead (C >= one page).
+int64_t head_cut(const RowSpan& sp, int64_t C, int ps) { return sp.snap(C, ps); }
 
 int64_t chunks_of(const RowSpan& sp, int64_t C, int mode) {
-  const int64_t a = sp.n - sp.w;
+  const int64_t a = sp.attended();
   if (mode == kChunkFixed) return fixed_chunks(sp, C);
   if (sp.n == 0 || C == 0 || a <= C) return 1;
   if (mode == kChunkHead) return 2;
@@ -562,8 +582,8 @@ DecodeChunking choose_chunking(const PlanRequest& r, const DecodeSchedule& g, in
   int64_t total = 0, longest = 0;
   for (int row = 0; row < rows; ++row) {
     const RowSpan sp = row_span(r, row);
-    total += sp.n - sp.w;
-    longest = std::max(longest, sp.n - sp.w);
+    total += sp.attended();
+    longest = std::max(longest, sp.attended());
   }
   const int64_t c_min = (kMinChunk + ps - 1) / ps * ps;
   const int64_t c_max = std::max(c_min, (longest + ps - 1) / ps * ps);
@@ -593,7 +613,7 @@ DecodeChunking choose_chunking(const PlanRequest& r, const DecodeSchedule& g, in
     uint16_t buckets[kSpanBuckets];
     for (int row = 0; row < rows; ++row) {
       const RowSpan sp = row_span(r, row);
-      len[row] = (int32_t)(sp.n - sp.w);
+      len[row] = (int32_t)sp.attended();
     }
     // chunks and partial slots (per unit) of the rows under an equal or a head cut at c
     auto counts = [&](int64_t c, int mode) {
@@ -673,11 +693,11 @@ int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, con
 
   // 1. every row's chunks, its slots and merge entries (row order)
   int64_t n_chunks = 0, n_slots = 0, n_merges = 0;
-  auto add_chunk = [&](int row, int64_t b, int64_t e, int64_t tile0, int64_t q, int64_t k,
-                       int64_t slot_base, int64_t merge_base) {
+  auto add_chunk = [&](int row, int64_t b, int64_t e, int64_t tile0, int64_t sb, int64_t se,
+                       int64_t q, int64_t k, int64_t slot_base, int64_t merge_base) {
     if (n_chunks < s->chunks_cap)
-      s->chunks[n_chunks] = {row, (int32_t)b, (int32_t)e, (int32_t)tile0, (int32_t)q,
-                             (int32_t)k, (int32_t)slot_base, (int32_t)merge_base};
+      s->chunks[n_chunks] = {row, (int32_t)b, (int32_t)e, (int32_t)tile0, (int32_t)sb, (int32_t)se,
+                             (int32_t)q, (int32_t)k, (int32_t)slot_base, (int32_t)merge_base};
     ++n_chunks;
   };
   for (int row = 0; row < rows; ++row) {
@@ -692,32 +712,42 @@ int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, con
       }
       n_slots += per_row * k;
     }
+    // positions [vb, ve) of the row's attended tokens as chunk q of k
+    auto add_positions = [&](int64_t vb, int64_t ve, int64_t q) {
+      const int64_t b = vb < sp.s && ve <= sp.s ? vb : std::max(sp.w, sp.w + vb - sp.s);
+      const int64_t e = ve <= sp.s ? ve : sp.w + ve - sp.s;
+      const bool both = vb < sp.s && ve > sp.s;
+      add_chunk(row, b, e, b / ps * ps, both ? vb : 0, both ? sp.s : 0, q, k, slot_base, merge_base);
+    };
+    const int64_t a = sp.attended();
     if (sp.n == 0 || C == 0 || (k == 1 && ch.mode != kChunkFixed)) {
-      add_chunk(row, sp.n == 0 ? 0 : sp.w, sp.n, sp.n == 0 ? 0 : sp.w / ps * ps, 0, 1, slot_base,
-                merge_base);
+      if (sp.n == 0) add_chunk(row, 0, 0, 0, 0, 0, 0, 1, slot_base, merge_base);
+      else add_positions(0, a, 0);
     } else if (ch.mode == kChunkHead) {
       // the first C tokens (to a page boundary), then the rest
       const int64_t x = head_cut(sp, C, ps);
-      add_chunk(row, sp.w, x, sp.w / ps * ps, 0, 2, slot_base, merge_base);
-      add_chunk(row, x, sp.n, x, 1, 2, slot_base, merge_base);
+      add_positions(0, x, 0);
+      add_positions(x, a, 1);
     } else if (ch.mode == kChunkFixed) {
       // multiples of C counted from token 0
       int64_t q = 0;
-      for (int64_t m = sp.w / C; m <= (sp.n - 1) / C; ++m, ++q)
-        add_chunk(row, std::max(m * C, sp.w), std::min((m + 1) * C, sp.n), m * C, q, k,
-                  slot_base, merge_base);
+      const int64_t whole = sp.s / C;
+      for (; q < whole; ++q)
+        add_chunk(row, q * C, (q + 1) * C, q * C, 0, 0, q, k, slot_base, merge_base);
+      for (int64_t m = sp.w / C; m <= (sp.n - 1) / C; ++m, ++q) {
+        const bool rest = q == whole && sp.s > whole * C;
+        add_chunk(row, std::max(m * C, sp.w), std::min((m + 1) * C, sp.n), m * C,
+                  rest ? whole * C : 0, rest ? sp.s : 0, q, k, slot_base, merge_base);
+      }
     } else {
       // k equal page-aligned parts, so no short remainder chunk launches last.  Every part gets a
-      // page at least (the merge counts k of them): k <= ceil(a / ps), so the parts before the
-      // last end below n also where parts shorter than a page were rounded up
-      const int64_t a = sp.n - sp.w;
-      int64_t b = sp.w, tile0 = sp.w / ps * ps, q = 0;
+      // page, or what the sinks hold of one, at least (the merge counts k of them): k <= ceil(a / ps),
+      // so the parts before the last end below n also where parts shorter than a page were rounded up
+      int64_t b = 0;
       for (int64_t m = 1; m <= k; ++m) {
-        const int64_t e =
-            m == k ? sp.n : std::max((sp.w + a * m / k) / ps * ps, (b / ps + 1) * ps);
-        add_chunk(row, b, e, tile0, q++, k, slot_base, merge_base);
+        const int64_t e = m == k ? a : std::max(sp.snap(a * m / k, ps), sp.next(b, ps));
+        add_positions(b, e, m - 1);
         b = e;
-        tile0 = e;
       }
     }
   }
@@ -737,7 +767,7 @@ int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, con
   }
   // 2. chunks longest first, ties in row and chunk order (a total order, so an in-place sort)
   std::sort(s->chunks, s->chunks + n_chunks, [](const DecodeChunk& x, const DecodeChunk& y) {
-    const int32_t lx = x.e - x.b, ly = y.e - y.b;
+    const int32_t lx = x.tokens(), ly = y.tokens();
     if (lx != ly) return lx > ly;
     return x.row != y.row ? x.row < y.row : x.q < y.q;
   });
@@ -757,8 +787,8 @@ int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, con
       t.q_pos = sp.n > 0 ? (int32_t)(sp.n - 1) : 0;
       t.kvh = u / gsl;
       t.gs = u % gsl;
-      t.cta = (int32_t)(c * per_row + u);
-      t.pad = 0;
+      t.sink_begin = ck.sb;
+      t.sink_end = ck.se;
     }
   }
   s->n_chunks = n_chunks;

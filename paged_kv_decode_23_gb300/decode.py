@@ -79,6 +79,7 @@ def _i32p(a: np.ndarray) -> int:
     return a.ctypes.data
 
 
+_PLAN = struct.Struct("@3Pq4f16i")  # pkd_plan_args
 _SCALED_RUN = struct.Struct("@5Pq3q3q4P3fi")  # pkd_scaled_run
 
 # The current stream's handle on a device.  torch's own accessor of the handle takes a tenth of the
@@ -116,6 +117,13 @@ def new_output(shape, like, dtype, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _plan_args(*fields) -> bytes:
+    try:
+        return _PLAN.pack(*fields)
+    except struct.error as e:
+        raise ValueError(f"a number of the plan does not fit 32 bits ({e})") from None
 
 
 _POS_CODE = {"NONE": 0, "ROPE_LLAMA": 1, "ALIBI": 2}
@@ -225,7 +233,7 @@ class BatchDecodePagedKV:
              use_tensor_cores: Optional[bool] = None, stream=None,
              q_len_per_req: int = 1, rope_scale: Optional[float] = None,
              rope_theta: Optional[float] = None, block_tables: Optional[torch.Tensor] = None,
-             seq_lens: Optional[torch.Tensor] = None) -> None:
+             seq_lens: Optional[torch.Tensor] = None, num_sink_tokens: int = 0) -> None:
         """Plan a batch; ``indptr`` / ``last_page_len`` may live on the host or the device
         (a device copy is read back once here), ``indices`` must be a CUDA int32 tensor and
         stay unchanged while runs of this plan are in flight.  ``q_len_per_req`` query tokens
@@ -234,7 +242,12 @@ class BatchDecodePagedKV:
         ``batch * q_len_per_req`` rows, request-major.  ``pos_encoding_mode``: "NONE",
         "ROPE_LLAMA" (with ``rope_scale`` / ``rope_theta``, defaults 1 and 1e4) or
         "ALIBI".  ``kv_data_type``: q's type, float8_e4m3fn, or "e2m1" (torch's float4_e2m1fn_x2)
-        for a cache in 4 bits, which runs on the tensor-core kernel without ROPE_LLAMA."""
+        for a cache in 4 bits, which runs on the tensor-core kernel without ROPE_LLAMA.
+
+        ``num_sink_tokens``: with a window, the first tokens of each request that stay visible
+        beside it (attention sinks): a row at position p attends t < num_sink_tokens and
+        t >= p - window_left.  What lies in between is not read, so its pages may go back to the
+        allocator and their entries of ``indices`` hold anything."""
         if block_tables is not None or seq_lens is not None:
             raise NotImplementedError("block_tables / seq_lens (the trtllm-gen backend's page "
                                       "table form) are not built; pass indptr / indices / "
@@ -258,14 +271,14 @@ class BatchDecodePagedKV:
         utc = use_tensor_cores if use_tensor_cores is not None else self._use_tc
         kernel = L.KERNEL_AUTO if utc is None else (L.KERNEL_TENSOR_CORE if utc else L.KERNEL_CUDA_CORE)
         sm = float("nan") if sm_scale is None else float(sm_scale)
-        L.check(L.lib().pkd_plan(
-            self._h, _i32p(ip), _i32p(lpl), batch, indices.data_ptr(), indices.numel(),
-            num_qo_heads, num_kv_heads, head_dim, page_size, sm,
-            float(logits_soft_cap or 0.0), int(window_left), int(fixed_split_size or 0),
+        args = _plan_args(
+            _i32p(ip), _i32p(lpl), indices.data_ptr(), indices.numel(), sm,
+            float(logits_soft_cap or 0.0), 1.0 if rope_scale is None else float(rope_scale),
+            1e4 if rope_theta is None else float(rope_theta), batch, num_qo_heads, num_kv_heads,
+            head_dim, page_size, int(window_left), int(fixed_split_size or 0),
             int(bool(disable_split_kv)), _DTYPE_CODE[q_dt], _DTYPE_CODE[kv_dt], _DTYPE_CODE[o_dt],
-            kernel, int(q_len_per_req), pos_code,
-            1.0 if rope_scale is None else float(rope_scale),
-            1e4 if rope_theta is None else float(rope_theta), _stream_ptr(stream)))
+            kernel, int(q_len_per_req), pos_code, int(num_sink_tokens), 0)
+        L.check(L.lib().pkd_plan_with(self._h, args, _stream_ptr(stream)))
         self._indices = indices
         self._plan_args = dict(batch=batch, q_len=int(q_len_per_req), rows=batch * int(q_len_per_req),
                                num_qo_heads=num_qo_heads, num_kv_heads=num_kv_heads,
@@ -453,15 +466,22 @@ def plan_host(indptr, last_page_len, num_qo_heads: int, num_kv_heads: int, head_
               page_size: int, window_left: int = -1, fixed_split_size: int = 0,
               disable_split_kv: bool = False, kv_dtype: int = L.DTYPE_F16,
               use_tensor_cores: int = L.KERNEL_AUTO, num_sms: int = 152,
-              work_capacity: int = 0, q_len_per_req: int = 1):
+              work_capacity: int = 0, q_len_per_req: int = 1, num_sink_tokens: int = 0):
     """Run the decode planner alone (no GPU): returns a dict with the tasks ``[n, 12]``
     (row, first page index, chunk start, begin, end, slot, merge entry, query position,
     kv head, slice, CTA, 0) grouped by CTA, the merge entries ``[m, 4]`` (row, first slot,
     chunk count, unit), the slot count, the CTAs with work, the chosen kernel and the tile
-    size.  ``work_capacity`` > 0 bounds the work list as CUDA-graph mode does."""
+    size.  ``work_capacity`` > 0 bounds the work list as CUDA-graph mode does.  With
+    ``num_sink_tokens`` the tasks are ``[n, 14]``: the sinks' begin and end follow, and the dict
+    holds the tasks, the merge entries and the slot count."""
     ip = _host_i32(indptr)
     lpl = _host_i32(last_page_len)
     batch = len(lpl)
+    if num_sink_tokens:
+        return _plan_tasks(_host_plan_args(ip, lpl, num_qo_heads, num_kv_heads, head_dim, page_size,
+                                           window_left, fixed_split_size, disable_split_kv, kv_dtype,
+                                           use_tensor_cores, q_len_per_req, num_sink_tokens),
+                           num_sms, work_capacity)
     n_tasks, n_merges, n_slots = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
     kern, tile, n_ctas = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
     args = (_i32p(ip), _i32p(lpl), batch, num_qo_heads, num_kv_heads, head_dim, page_size,
@@ -480,6 +500,27 @@ def plan_host(indptr, last_page_len, num_qo_heads: int, num_kv_heads: int, head_
     return dict(tasks=tasks[:n_tasks.value], merges=merges[:n_merges.value],
                 num_slots=n_slots.value, num_ctas=n_ctas.value, kernel=kern.value,
                 tile_tokens=tile.value)
+
+
+def _host_plan_args(ip, lpl, num_qo_heads, num_kv_heads, head_dim, page_size, window_left,
+                    fixed_split_size, disable_split_kv, kv_dtype, use_tensor_cores, q_len_per_req,
+                    num_sink_tokens) -> bytes:
+    """pkd_plan_args for the host-only calls (ip and lpl stay alive with the caller)."""
+    return _plan_args(_i32p(ip), _i32p(lpl), 0, 0, float("nan"), 0.0, 1.0, 1e4, len(lpl), num_qo_heads,
+                      num_kv_heads, head_dim, page_size, int(window_left), int(fixed_split_size),
+                      int(bool(disable_split_kv)), L.DTYPE_F16, kv_dtype, L.DTYPE_F16, use_tensor_cores,
+                      int(q_len_per_req), 0, int(num_sink_tokens), 0)
+
+
+def _plan_tasks(args: bytes, num_sms: int, work_capacity: int) -> dict:
+    n_tasks, n_merges, n_slots = (ctypes.c_int() for _ in range(3))
+    outs = (ctypes.byref(n_tasks), ctypes.byref(n_merges), ctypes.byref(n_slots))
+    L.check(L.lib().pkd_plan_tasks(args, num_sms, int(work_capacity), None, 0, None, 0, *outs))
+    tasks = np.zeros((max(1, n_tasks.value), 14), dtype=np.int32)
+    merges = np.zeros((max(1, n_merges.value), 4), dtype=np.int32)
+    L.check(L.lib().pkd_plan_tasks(args, num_sms, int(work_capacity), _i32p(tasks), n_tasks.value,
+                                   _i32p(merges), n_merges.value, *outs))
+    return dict(tasks=tasks[:n_tasks.value], merges=merges[:n_merges.value], num_slots=n_slots.value)
 
 
 def mla_graph_workspace_bytes(max_items: int, num_heads: int, backend: str = "auto"):
@@ -525,15 +566,15 @@ def workspace_bytes(indptr, last_page_len, num_qo_heads: int, num_kv_heads: int,
                     page_size: int, window_left: int = -1, fixed_split_size: int = 0,
                     disable_split_kv: bool = False, kv_dtype: int = L.DTYPE_F16,
                     use_tensor_cores: int = L.KERNEL_AUTO, num_sms: int = 152,
-                    q_len_per_req: int = 1):
+                    q_len_per_req: int = 1, num_sink_tokens: int = 0):
+    """(float, int) workspace bytes of a plan."""
     ip = _host_i32(indptr)
     lpl = _host_i32(last_page_len)
     fb, ib = ctypes.c_size_t(), ctypes.c_size_t()
-    L.check(L.lib().pkd_workspace_bytes(_i32p(ip), _i32p(lpl), len(lpl), num_qo_heads,
-                                        num_kv_heads, head_dim, page_size, window_left,
-                                        fixed_split_size, int(disable_split_kv), kv_dtype,
-                                        use_tensor_cores, num_sms, int(q_len_per_req),
-                                        ctypes.byref(fb), ctypes.byref(ib)))
+    args = _host_plan_args(ip, lpl, num_qo_heads, num_kv_heads, head_dim, page_size, window_left,
+                           fixed_split_size, disable_split_kv, kv_dtype, use_tensor_cores,
+                           q_len_per_req, num_sink_tokens)
+    L.check(L.lib().pkd_plan_workspace_bytes(args, num_sms, ctypes.byref(fb), ctypes.byref(ib)))
     return fb.value, ib.value
 
 
