@@ -207,6 +207,32 @@ typedef struct pkd_scaled_run {
 int pkd_run_scaled(pkd_handle* h, const pkd_scaled_run* run, void* stream);
 
 /*
+ * pkd_run / pkd_run_scaled of a plan with key_weights: the same o and lse, and for every attended key t
+ * of request i and every kv head
+ *   key_weights[page, head, slot of t] += sum over the request's query rows and the head's qo heads
+ *                                         of softmax(s)_t
+ * (two launches; ev_end is recorded behind the second).  run's k_scales and v_scales are NULL unless
+ * the cache is E2M1.  key_weights: device float32, element (page, head, slot) at page*weight_strides[0]
+ * + head*weight_strides[1] + slot*weight_strides[2]; entries must not overlap.  Entries of slots that
+ * no row attends are left as they are.  Sums are taken in 32 bits in the order of rows and heads; a page
+ * that several requests share takes their sums in no fixed order, which may change the last bit.  A key whose page id
+ * lies outside the pool has no entry (PKD_STATUS_BAD_PAGE); nothing is added after PKD_STATUS_TIMEOUT.
+ */
+typedef struct pkd_key_weights_run {
+  pkd_scaled_run run;
+  float* key_weights;
+  int64_t weight_strides[3];
+} pkd_key_weights_run;
+int pkd_run_key_weights(pkd_handle* h, const pkd_key_weights_run* run, void* stream);
+
+/*
+ * What a plan with key_weights needs at most beside pkd_graph_workspace_bytes in CUDA-graph mode, for
+ * requests of max_pages pages in all.
+ */
+int pkd_key_weights_workspace_bytes(int64_t max_pages, int page_size, int max_batch, int q_len_per_req,
+                                    int num_qo_heads, size_t* float_ws_bytes, size_t* int_ws_bytes);
+
+/*
  * Programmatic dependent launch (the page's run(enable_pdl=...)), on by default.  When on, the
  * decode kernel is launched with programmatic stream serialization: the GPU may schedule it
  * while the previous kernel in the stream is still finishing, and the kernel waits
@@ -335,6 +361,10 @@ int pkd_workspace_bytes(const int32_t* indptr_host, const int32_t* last_page_len
  *                    t >= p - window_left.  Keys in between are not read: their pages may be freed
  *                    and their entries of `indices` may hold anything.  Positions (ALiBi, RoPE)
  *                    stay the tokens' own.  No effect with window_left < 0.
+ *   key_weights      1: the plan's runs are pkd_run_key_weights, which also adds every key's softmax
+ *                    weight to a pool of sums.  The workspaces then hold the scores of all attended
+ *                    keys (4 bytes a key, row and qo head) as well.  Tensor-core kernel, without
+ *                    ROPE_LLAMA (UNSUPPORTED otherwise); CUDA-graph mode: fixed by the first plan.
  * pkd_plan(...) is pkd_plan_with with 0 for these.
  */
 typedef struct pkd_plan_args {
@@ -361,7 +391,7 @@ typedef struct pkd_plan_args {
   int32_t q_len_per_req;
   int32_t pos_encoding_mode;
   int32_t num_sink_tokens;
-  int32_t reserved;
+  int32_t key_weights;
 } pkd_plan_args;
 int pkd_plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream);
 

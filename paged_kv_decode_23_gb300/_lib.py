@@ -44,6 +44,9 @@ SIGNATURES = {
                                _c_float, _vp, _vp, _vp, _vp, _vp]),
     # the argument structs of these travel as packed bytes (decode.py, cache.py)
     "pkd_plan_with": (_c_int, [_vp, ctypes.c_char_p, _vp]),
+    "pkd_run_key_weights": (_c_int, [_vp, ctypes.c_char_p, _vp]),
+    "pkd_key_weights_workspace_bytes": (_c_int, [ctypes.c_int64, _c_int, _c_int, _c_int, _c_int,
+                                                 ctypes.POINTER(_c_size), ctypes.POINTER(_c_size)]),
     "pkd_plan_tasks": (_c_int, [ctypes.c_char_p, _c_int, _c_int, _vp, _c_int, _vp, _c_int] +
                        [ctypes.POINTER(_c_int)] * 3),
     "pkd_plan_workspace_bytes": (_c_int, [ctypes.c_char_p, _c_int, ctypes.POINTER(_c_size),

@@ -362,7 +362,7 @@ __device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t s, bool high) {
   return *reinterpret_cast<const uint32_t*>(&z);
 }
 
-template <typename TQ, class G>
+template <typename TQ, class G, bool SCORES>
 __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const BlockCoords& b,
                                              uint32_t smem, uint32_t full0, uint32_t empty0,
                                              volatile int* abort_flag, int warp, int lane,
@@ -485,6 +485,14 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
         for (int e = 0; e < 4 * SL; ++e) {
           const int t = ((e & 2) ? tok_b : tok_a) + (e >> 2) * G::SLICE;
           if (t < lo || t >= hi) sc[e] = kNegInf;
+        }
+      }
+      if constexpr (SCORES) {
+        const ScoreOut so(p, b, 2 * tig, HEADS);  // (HEADS 4: lanes of tig >= 2 repeat the others' scores)
+#pragma unroll
+        for (int e = 0; e < 4 * SL; e += 2) {
+          const int t = ((e & 2) ? tok_b : tok_a) + (e >> 2) * G::SLICE;
+          if (t >= lo && t < hi) so.put(t_w + t, sc[e], sc[e + 1]);
         }
       }
       float top[2] = {fmaxf(sc[0], sc[2]), fmaxf(sc[1], sc[3])};
@@ -636,7 +644,7 @@ __device__ __forceinline__ void stash_e2m1(const EpiView<G::D>& e, int warp, int
 }
 
 // ------------------------------------------------------------------------------ kernel
-template <typename TQ, class G, int CTAS>
+template <typename TQ, class G, int CTAS, bool SCORES>
 __global__ void __launch_bounds__(G::THREADS, CTAS)
     decode_e2m1_kernel(const __grid_constant__ DecodeE2m1Params p) {
   using namespace dev;
@@ -682,7 +690,7 @@ __global__ void __launch_bounds__(G::THREADS, CTAS)
   float acc[G::ACC][4];
 #pragma unroll
   for (int mb = 0; mb < G::ACC; ++mb) acc[mb][0] = acc[mb][1] = acc[mb][2] = acc[mb][3] = 0.f;
-  consume_e2m1<TQ, G>(p, b, smem, full0, empty0, abort_flag, warp, lane, m2, lsum, acc);
+  consume_e2m1<TQ, G, SCORES>(p, b, smem, full0, empty0, abort_flag, warp, lane, m2, lsum, acc);
   // every consumer is done with the stages; one shared decision whether any wait gave up
   if (named_bar_or(1, G::NCONS, *abort_flag != 0)) return;
   stash_e2m1<G>(epi, warp, lane, m2, lsum, acc);
@@ -691,7 +699,7 @@ __global__ void __launch_bounds__(G::THREADS, CTAS)
   if (b.it.out_slot >= 0) merge_unit<TQ, D, G::NCONS>(p, b, threadIdx.x, &merge_last_s);
 }
 
-template <typename TQ, class G, int CTAS>
+template <typename TQ, class G, int CTAS, bool SCORES>
 DecodeKernel make_decode_e2m1(int q_dtype) {
   DecodeKernel k;
   k.kind = kTensorCore;
@@ -699,7 +707,8 @@ DecodeKernel make_decode_e2m1(int q_dtype) {
   k.kv_dtype = kE2M1;
   k.head_dim = G::D;
   k.heads_per_cta = G::HEADS;
-  k.fn = reinterpret_cast<const void*>(&decode_e2m1_kernel<TQ, G, CTAS>);
+  k.fn = reinterpret_cast<const void*>(&decode_e2m1_kernel<TQ, G, CTAS, SCORES>);
+  k.scores = SCORES ? 1 : 0;
   k.threads = G::THREADS;
   k.smem_bytes = G::SMEM_BYTES;
   k.tile_tokens = G::TS;
@@ -708,6 +717,20 @@ DecodeKernel make_decode_e2m1(int q_dtype) {
   k.max_ctas = CTAS;
   k.box_rows = G::SLICE;
   return k;
+}
+
+// The geometries that are built, for tasks of up to 4 or up to 8 qo heads: 4 where a kv head has no
+// more.  Groups of 4 heads through the 8-head instance took 52.1 us for 45.4 (64 contexts of 512 to
+// 4,096, head_dim 128), and 123 for 113 (4 of 131,072).  At head_dim 64 these cases take 30.3 and 75.9 us.
+template <typename TQ, bool SCORES>
+void register_e2m1_geometries(std::vector<DecodeKernel>& out, int q) {
+  //                                  D  heads warps slices stages  CTAs per SM
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<64, 4, 4, 2, 5>, 4, SCORES>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<128, 4, 4, 2, 3>, 4, SCORES>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<256, 4, 4, 2, 3>, 2, SCORES>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<64, 8, 4, 2, 4>, 4, SCORES>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<128, 8, 4, 2, 4>, 3, SCORES>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<256, 8, 4, 2, 3>, 2, SCORES>(q));
 }
 
 }  // namespace pkd

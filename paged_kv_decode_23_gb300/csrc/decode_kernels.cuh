@@ -241,6 +241,8 @@ __device__ __forceinline__ void store_task(const DecodeParams& p, const BlockCoo
       TQ* dst = reinterpret_cast<TQ*>(p.o) + ((size_t)b.it.req * p.num_qo_heads + qo) * D + d0;
       *reinterpret_cast<uint4*>(dst) = v;
       if (d0 == 0 && p.lse) p.lse[(size_t)b.it.req * p.num_qo_heads + qo] = lse2 * kLn2;
+      if (d0 == 0 && p.stats)
+        p.stats[(size_t)b.it.req * p.num_qo_heads + qo] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
     } else {
       float* dst = p.part_o + ((size_t)b.it.out_slot * kSlotHeads + g) * D + d0;
       reinterpret_cast<float4*>(dst)[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
@@ -335,6 +337,7 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, const BlockCoo
     *reinterpret_cast<uint4*>(dst) = v;
     if (d0 == 0 && p.lse)
       p.lse[(size_t)me.req * hq + qo] = L > 0.f ? (M + log2f(L)) * kLn2 : kNegInf;
+    if (d0 == 0 && p.stats) p.stats[(size_t)me.req * hq + qo] = make_float2(M, inv);
   }
 }
 
@@ -543,10 +546,33 @@ __device__ __forceinline__ void rope_qk_step(float (&c)[4], float (&c2)[4], uint
   mma_16816<__half>(c2, h, p0, p1);
 }
 
+// Where the scores of this lane's two S^T columns (qo heads g0 + col, + 1 of the task's row) go.
+struct ScoreOut {
+  float* base;
+  int stride, sink, shift;
+  bool live0, live1;
+  __device__ __forceinline__ ScoreOut(const DecodeParams& p, const BlockCoords& b, int col, int heads) {
+    const KeyRow kr = p.key_rows[b.it.req];
+    base = p.scores + kr.base + (int64_t)(b.g0 + col) * kr.stride;
+    stride = kr.stride;
+    sink = kr.sink;
+    shift = kr.shift;
+    live0 = col < min(b.gcnt, heads);
+    live1 = col + 1 < min(b.gcnt, heads);
+  }
+  // the scores of key t
+  __device__ __forceinline__ void put(int t, float s0, float s1) const {
+    float* at = base + t + (t < sink ? 0 : shift);
+    if (live0) at[0] = s0;
+    if (live1) at[stride] = s1;
+  }
+};
+
 // ROPE: per tile, q is rotated by the warp slice's E entries and each K row by its R entries
 // (the two halves of a rotation pair are k steps kk and kk + D/32 of the same lane), in fp16
 // arithmetic, so QK runs in fp16; P*V keeps V's type.
-template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, bool ROPE = false>
+// SCORES: every attended key's score is left in p.scores as well.
+template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, bool ROPE = false, bool SCORES = false>
 __device__ __forceinline__ void consume_tc(const DecodeParams& p, const BlockCoords& b, uint32_t smem,
                                            uint32_t full0, uint32_t empty0, volatile int* abort_flag,
                                            int warp, int lane, float (&m2)[2], float (&lsum)[2],
@@ -696,6 +722,11 @@ __device__ __forceinline__ void consume_tc(const DecodeParams& p, const BlockCoo
         const float bias = ((e & 1) ? slope1 : slope0) * (float)(t_w + t - b.it.q_pos);
         const float sv = score_log2(c[e], scale_qk, bias, cap_log2);
         sc[e] = (t >= vlo && t < vhi) ? sv : kNegInf;
+      }
+      if constexpr (SCORES) {
+        const ScoreOut so(p, b, 2 * tig, 8);
+        if (tok_a >= vlo && tok_a < vhi) so.put(t_w + tok_a, sc[0], sc[1]);
+        if (tok_b >= vlo && tok_b < vhi) so.put(t_w + tok_b, sc[2], sc[3]);
       }
       // The reference m2 of a column only moves when one of its scores exceeds it by more
       // than kLazyMax: until then p = 2^(s - m2) <= 2^kLazyMax, far inside the 16-bit P
@@ -1337,8 +1368,9 @@ __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoo
 
 // ------------------------------------------------------------------------------ kernel
 // KIND: kTensorCore (HEADS = 8 qo heads per task) or kCudaCore (HEADS = GP).  ROPE: ROPE_LLAMA
-// applied to q and K.  CTA blockIdx.x runs task blockIdx.x.
-template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int KIND, int GP, bool ROPE = false>
+// applied to q and K.  SCORES: see consume_tc.  CTA blockIdx.x runs task blockIdx.x.
+template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int KIND, int GP, bool ROPE = false,
+          bool SCORES = false>
 __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREADS,
                                   KIND == kTensorCore ? 2 : 1)
     __maxnreg__((KIND == kTensorCore ? 255
@@ -1400,7 +1432,7 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
     float acc[D / 16][4];
 #pragma unroll
     for (int mb = 0; mb < D / 16; ++mb) acc[mb][0] = acc[mb][1] = acc[mb][2] = acc[mb][3] = 0.f;
-    consume_tc<TQ, KV_FP8, D, TS, NSTAGES, ROPE>(p, b, smem, full0, empty0, abort_flag, warp,
+    consume_tc<TQ, KV_FP8, D, TS, NSTAGES, ROPE, SCORES>(p, b, smem, full0, empty0, abort_flag, warp,
                                                  lane, m2, lsum, acc);
     // every consumer is done with the stages; one shared decision whether any wait gave up
     if (named_bar_or(1, G::NCONS, *abort_flag != 0)) return;
@@ -1418,7 +1450,8 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
 }
 
 // ------------------------------------------------------------------------------ registry
-template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int KIND, int GP, bool ROPE = false>
+template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int KIND, int GP, bool ROPE = false,
+          bool SCORES = false>
 DecodeKernel make_decode_kernel(int q_dtype, int kv_dtype) {
   using G = DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>;
   DecodeKernel k;
@@ -1428,8 +1461,9 @@ DecodeKernel make_decode_kernel(int q_dtype, int kv_dtype) {
   k.head_dim = D;
   k.heads_per_cta = KIND == kTensorCore ? 8 : GP;
   k.fn = reinterpret_cast<const void*>(
-      &decode_paged_kernel<TQ, KV_FP8, D, TS, NSTAGES, KIND, GP, ROPE>);
+      &decode_paged_kernel<TQ, KV_FP8, D, TS, NSTAGES, KIND, GP, ROPE, SCORES>);
   k.rope = ROPE ? 1 : 0;
+  k.scores = SCORES ? 1 : 0;
   k.nstages = NSTAGES;
   k.threads = G::THREADS;
   k.smem_bytes = G::SMEM_BYTES + (KIND == kTensorCore

@@ -1,0 +1,25 @@
+// decode_weights.cu -- the tensor-core decode kernels that also leave every attended key's score (the
+// first half of a plan with key weights; key_weights.cu is the second), 16-bit and e4m3 caches.
+#include "decode_kernels.cuh"
+
+namespace pkd {
+
+template <typename TQ, bool KV_FP8, int D, int TS>
+DecodeKernel with_scores(int q, int kv) {
+  return make_decode_kernel<TQ, KV_FP8, D, TS, 3, kTensorCore, 8, false, true>(q, kv);
+}
+
+void register_decode_weights(std::vector<DecodeKernel>& out) {
+  out.push_back(with_scores<__half, false, 64, 128>(kF16, kF16));
+  out.push_back(with_scores<__half, false, 128, 64>(kF16, kF16));
+  out.push_back(with_scores<__half, false, 256, 32>(kF16, kF16));
+  out.push_back(with_scores<__nv_bfloat16, false, 64, 128>(kBF16, kBF16));
+  out.push_back(with_scores<__nv_bfloat16, false, 128, 64>(kBF16, kBF16));
+  out.push_back(with_scores<__nv_bfloat16, false, 256, 32>(kBF16, kBF16));
+  out.push_back(with_scores<__half, true, 128, 128>(kF16, kE4M3));
+  out.push_back(with_scores<__half, true, 256, 64>(kF16, kE4M3));
+  out.push_back(with_scores<__nv_bfloat16, true, 128, 128>(kBF16, kE4M3));
+  out.push_back(with_scores<__nv_bfloat16, true, 256, 64>(kBF16, kE4M3));
+}
+
+}  // namespace pkd

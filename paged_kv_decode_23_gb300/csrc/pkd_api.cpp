@@ -50,6 +50,8 @@ void init_registry() {
     register_decode_rope_cc(g_decode);
     register_decode_rope_cc_e4m3(g_decode);
     register_decode_e2m1(g_decode);
+    register_decode_weights(g_decode);
+    register_decode_e2m1_weights(g_decode);
     register_mla(g_mla);
     register_mla_tc(g_mla);
   });
@@ -63,11 +65,11 @@ const MlaKernel* find_mla(int dtype, int variant) {
 }
 
 const DecodeKernel* find_decode(int kind, int q_dtype, int kv_dtype, int head_dim, int heads,
-                                int rope) {
+                                int rope, int scores) {
   init_registry();
   for (const auto& k : g_decode)
     if (k.kind == kind && k.q_dtype == q_dtype && k.kv_dtype == kv_dtype &&
-        k.head_dim == head_dim && k.heads_per_cta == heads && k.rope == rope)
+        k.head_dim == head_dim && k.heads_per_cta == heads && k.rope == rope && k.scores == scores)
       return &k;
   return nullptr;
 }
@@ -153,6 +155,9 @@ struct pkd_handle {
   size_t tmap_next = 0;
   int gslices = 1;
   int64_t n_tasks = 0;
+  bool key_weights = false;  // the plan's runs sum their keys' weights
+  KeyWsLayout klayout{};
+  int n_key_tiles = 0;
 
   // Pinned copies of the work list for the async uploads, used in turn: plan() waits only for
   // the upload of kStagingSlots plans ago, so a host that plans ahead of the GPU is not held up.
@@ -407,6 +412,11 @@ int plan_request_of(const pkd_plan_args& a, int num_sms, PlanRequest* r) {
   if (rc) return rc;
   if (a.num_sink_tokens < 0) return fail(PKD_ERR_INVALID_ARG, "num_sink_tokens must be >= 0");
   r->num_sinks = a.num_sink_tokens;
+  if (a.key_weights && a.use_tensor_cores == PKD_KERNEL_CUDA_CORE)
+    return fail(PKD_ERR_UNSUPPORTED, "key weights run on the tensor-core kernel alone");
+  if (a.key_weights && a.pos_encoding_mode == PKD_POS_ROPE_LLAMA)
+    return fail(PKD_ERR_UNSUPPORTED,
+                "key weights are not built with ROPE_LLAMA (rotate the keys as they are appended)");
   return PKD_OK;
 }
 
@@ -439,7 +449,22 @@ int plan_host(const PlanRequest& r, int num_sms, int width, int32_t* tasks_out, 
   return PKD_OK;
 }
 
-int plan_bytes(const PlanRequest& r, int num_sms, size_t* float_ws_bytes, size_t* int_ws_bytes) {
+// The workspaces of a plan with key weights, behind those of `lay`; the lists are counted, not made.
+KeyWsLayout key_layout_of(const PlanRequest& r, const DecodeWsLayout& lay, int64_t* n_tiles) {
+  KeyWsLayout k;
+  int64_t floats = 0;
+  key_weight_lists(r, nullptr, nullptr, 0, n_tiles, &floats);
+  k.rows = (size_t)r.batch * r.q_len;
+  k.tiles = (size_t)*n_tiles;
+  k.row_heads = k.rows * (size_t)r.num_qo_heads;
+  k.scores = (size_t)floats;
+  k.int_off = align256(dws_int_bytes(lay));
+  k.float_off = align256(dws_float_bytes(lay, r.head_dim));
+  return k;
+}
+
+int plan_bytes(const PlanRequest& r, int num_sms, bool key_weights, size_t* float_ws_bytes,
+               size_t* int_ws_bytes) {
   ScheduleStore st;
   DecodeSchedule sch;
   const int ctas = (num_sms > 0 ? num_sms : 152) * decode_max_ctas(r);
@@ -447,8 +472,10 @@ int plan_bytes(const PlanRequest& r, int num_sms, size_t* float_ws_bytes, size_t
   if (rc) return rc;
   DecodeWsLayout lay{(size_t)sch.n_tasks, (size_t)sch.n_merges, (size_t)sch.n_slots};
   lay.pos_floats = 2 * (size_t)r.head_dim + r.num_qo_heads;  // room for a positional encoding
-  if (float_ws_bytes) *float_ws_bytes = dws_float_bytes(lay, r.head_dim);
-  if (int_ws_bytes) *int_ws_bytes = dws_int_bytes(lay);
+  int64_t n_tiles = 0;
+  const KeyWsLayout k = key_weights ? key_layout_of(r, lay, &n_tiles) : KeyWsLayout();
+  if (float_ws_bytes) *float_ws_bytes = key_weights ? k.float_end() : dws_float_bytes(lay, r.head_dim);
+  if (int_ws_bytes) *int_ws_bytes = key_weights ? k.int_end() : dws_int_bytes(lay);
   return PKD_OK;
 }
 
@@ -571,7 +598,7 @@ int pkd_plan_workspace_bytes(const pkd_plan_args* args, int num_sms, size_t* flo
     if (!args) return fail(PKD_ERR_INVALID_ARG, "args is null");
     PlanRequest r;
     if (int rc = plan_request_of(*args, num_sms, &r)) return rc;
-    return plan_bytes(r, num_sms, float_ws_bytes, int_ws_bytes);
+    return plan_bytes(r, num_sms, args->key_weights != 0, float_ws_bytes, int_ws_bytes);
   });
 }
 
@@ -586,7 +613,7 @@ int pkd_workspace_bytes(const int32_t* indptr_host, const int32_t* last_page_len
                              disable_split_kv, kv_dtype, use_tensor_cores, num_sms,
                              q_len_per_req);
   if (rc) return rc;
-  return plan_bytes(r, num_sms, float_ws_bytes, int_ws_bytes);
+  return plan_bytes(r, num_sms, false, float_ws_bytes, int_ws_bytes);
 }
 
 }  // extern "C"
@@ -605,6 +632,7 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   const int q_len_per_req = args->q_len_per_req, pos_encoding_mode = args->pos_encoding_mode;
   const float sm_scale = args->sm_scale, logits_soft_cap = args->logits_soft_cap;
   const float rope_scale = args->rope_scale, rope_theta = args->rope_theta;
+  const bool key_weights = args->key_weights != 0;
   h->planned = false;
   if (q_dtype != PKD_DTYPE_F16 && q_dtype != PKD_DTYPE_BF16)
     return fail(PKD_ERR_INVALID_ARG, "q_dtype must be F16 or BF16");
@@ -645,6 +673,8 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
                   "CUDA-graph mode: q_len_per_req is fixed by the first plan");
     if (h->g_batch >= 0 && h->mla)
       return fail(PKD_ERR_INVALID_ARG, "CUDA-graph mode: the handle holds MLA plans");
+    if (h->g_batch >= 0 && key_weights != h->key_weights)
+      return fail(PKD_ERR_INVALID_ARG, "CUDA-graph mode: key_weights is fixed by the first plan");
   }
 
   PlanRequest r;
@@ -657,7 +687,8 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   rc = decode_geometry(r, &sch, &err);
   if (rc) return fail(rc, err);
   const DecodeKernel* k =
-      find_decode(sch.kind, q_dtype, kv_dtype, head_dim, sch.heads_per_cta, r.rope);
+      find_decode(sch.kind, q_dtype, kv_dtype, head_dim, sch.heads_per_cta, r.rope,
+                  key_weights ? 1 : 0);
   if (!k) return fail(PKD_ERR_UNSUPPORTED, "no decode kernel built for this dtype / head_dim");
   cudaError_t e = set_smem_limit_once(k, h->device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
@@ -687,8 +718,19 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
                                 : DecodeWsLayout{(size_t)sch.n_tasks, (size_t)sch.n_merges,
                                                  (size_t)sch.n_slots};
   if (pos_encoding_mode != PKD_POS_NONE) lay.pos_floats = 2 * (size_t)head_dim + num_qo_heads;
-  const size_t need_f = dws_float_bytes(lay, head_dim);
-  const size_t need_i = dws_int_bytes(lay);
+  // (CUDA-graph mode: the lists of key weights lie behind the capacity's layout with a table, so that
+  // they keep their place; what they hold may grow to the workspaces' end)
+  int64_t n_key_tiles = 0;
+  KeyWsLayout klay;
+  if (key_weights) {
+    DecodeWsLayout before = lay;
+    if (h->graph) before.pos_floats = 2 * (size_t)head_dim + num_qo_heads;
+    klay = key_layout_of(r, before, &n_key_tiles);
+    if (n_key_tiles * num_kv_heads > std::numeric_limits<int32_t>::max())
+      return fail(PKD_ERR_INVALID_ARG, "too many keys for one plan with key weights");
+  }
+  const size_t need_f = key_weights ? klay.float_end() : dws_float_bytes(lay, head_dim);
+  const size_t need_i = key_weights ? klay.int_end() : dws_int_bytes(lay);
   if (need_f > h->float_bytes || need_i > h->int_bytes) {
     char buf[200];
     std::snprintf(buf, sizeof buf, "workspace too small: need %zu float / %zu int bytes", need_f,
@@ -706,8 +748,9 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   const size_t pos_off = dws_pos_offset(lay);
   const size_t tasks_b = (size_t)sch.n_tasks * sizeof(DecodeTask);
   const size_t merges_b = (size_t)sch.n_merges * sizeof(MergeEntry);
-  const size_t img_bytes = lay.pos_floats ? pos_off + lay.pos_floats * sizeof(float)
-                                          : merges_off + merges_b;
+  const size_t img_bytes = key_weights      ? klay.int_end()
+                           : lay.pos_floats ? pos_off + lay.pos_floats * sizeof(float)
+                                            : merges_off + merges_b;
   const size_t table_b = h->graph ? (size_t)(2 * batch + 1) * sizeof(int32_t) : 0;
   const size_t bytes = img_bytes + table_b;
   char* img = nullptr;
@@ -715,8 +758,14 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   if (int rc2 = staging_acquire(h, bytes, &img, &slot)) return rc2;
   std::memset(img, 0, tasks_off);
   if (h->graph) {
-    const int32_t count = (int32_t)sch.n_tasks;
+    const int32_t count = (int32_t)sch.n_tasks, tiles = (int32_t)n_key_tiles;
     std::memcpy(img + kItemCountOffset, &count, sizeof count);
+    std::memcpy(img + kTileCountOffset, &tiles, sizeof tiles);
+  }
+  if (key_weights) {
+    int64_t floats = 0;
+    key_weight_lists(r, reinterpret_cast<KeyRow*>(img + klay.int_off),
+                     reinterpret_cast<KeyTile*>(img + klay.tiles_off()), n_key_tiles, &n_key_tiles, &floats);
   }
   if (tasks_b) std::memcpy(img + tasks_off, h->tasks.data(), tasks_b);
   if (merges_b) std::memcpy(img + merges_off, h->dmerges.data(), merges_b);
@@ -775,6 +824,9 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   h->cap = logits_soft_cap > 0.f ? logits_soft_cap : 0.f;
   h->indices = h->graph ? h->g_indices : indices_dev;
   h->dlayout = lay;
+  h->key_weights = key_weights;
+  h->klayout = klay;
+  h->n_key_tiles = (int)n_key_tiles;
   if (h->graph) h->g_batch = batch;
   h->kernel = k;
   h->pos_mode = pos_encoding_mode;
@@ -869,10 +921,30 @@ struct ScalePools {
   const int64_t* strides;
 };
 
-// pkd_run_timed (sf null) and pkd_run_scaled.
+// Where a run of a plan with key weights adds them: element (page, kv head, slot).
+struct WeightPool {
+  float* base;
+  const int64_t* strides;
+};
+
+// Whether the `n` entries of each axis at these strides lie apart: each axis clears what the shorter
+// ones span.
+bool entries_apart(const int64_t strides[3], const int64_t n[3]) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return strides[a] < strides[b]; });
+  int64_t span = 1;
+  for (int i : order) {
+    if (n[i] <= 1) continue;
+    if (strides[i] < span) return false;
+    span += (n[i] - 1) * strides[i];
+  }
+  return true;
+}
+
+// pkd_run_timed (sf and kw null), pkd_run_scaled and pkd_run_key_weights.
 int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
-               int64_t num_pages, const int64_t kv_strides[3], const ScalePools* sf, float q_scale,
-               float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
+               int64_t num_pages, const int64_t kv_strides[3], const ScalePools* sf,
+               const WeightPool* kw, float q_scale, float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
                void* ev_end) {
   if (!h) return fail(PKD_ERR_INVALID_ARG, "handle is null");
   if (!h->planned || h->mla)
@@ -880,6 +952,9 @@ int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_b
   if ((h->kv_dtype == kE2M1) != (sf != nullptr))
     return fail(PKD_ERR_INVALID_ARG,
                 "a plan with E2M1 KV runs with pkd_run_scaled, every other plan without scale pools");
+  if (h->key_weights != (kw != nullptr))
+    return fail(PKD_ERR_INVALID_ARG,
+                "a plan with key weights runs with pkd_run_key_weights, every other plan without");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (h->n_tasks == 0 && !h->graph) return PKD_OK;  // empty batch
   if (!q || !k_base || !v_base || !o || !kv_strides)
@@ -913,6 +988,15 @@ int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_b
       if (sf->strides[i] <= 0 || sf->strides[i] % sb != 0)
         return fail(PKD_ERR_INVALID_ARG,
                     "scale strides must be positive multiples of head_dim / 16 bytes");
+  }
+
+  if (kw) {
+    if (!kw->base || !aligned(kw->base, 4)) return fail(PKD_ERR_INVALID_ARG, "key_weights is null or not aligned");
+    const int64_t n[3] = {num_pages, h->num_kv_heads, h->page_size};
+    for (int i = 0; i < 3; ++i)
+      if (kw->strides[i] < 0 || (n[i] > 1 && kw->strides[i] > (int64_t(1) << 60) / n[i]))
+        return fail(PKD_ERR_INVALID_ARG, "key_weights strides must be positive, within 2^60 elements");
+    if (!entries_apart(kw->strides, n)) return fail(PKD_ERR_INVALID_ARG, "entries of key_weights overlap");
   }
 
   // the E2M1 kernels take the decode parameters followed by their scale pools
@@ -973,6 +1057,11 @@ int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_b
     prm.cap_log2 = 0.f;
   }
   prm.v_scale = v_scale;
+  if (kw) {
+    prm.stats = reinterpret_cast<float2*>(fws + h->klayout.float_off);
+    prm.scores = reinterpret_cast<float*>(fws + h->klayout.scores_off());
+    prm.key_rows = reinterpret_cast<const KeyRow*>(iws + h->klayout.int_off);
+  }
 
   const int64_t grid = h->grid;  // persistent CTAs (CUDA-graph mode: the fixed grid)
   void* args[] = {&prm};
@@ -994,6 +1083,44 @@ int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_b
     e = cudaLaunchKernelExC(&cfg, h->kernel->fn, args);
   }
   if (e != cudaSuccess) return cuda_fail(e, "decode kernel launch");
+  if (kw) {
+    KeyWeightParams kp;
+    std::memset(&kp, 0, sizeof kp);
+    kp.tiles = reinterpret_cast<const KeyTile*>(iws + h->klayout.tiles_off());
+    kp.tile_count = h->graph ? reinterpret_cast<const int32_t*>(iws + kTileCountOffset) : nullptr;
+    kp.rows = prm.key_rows;
+    kp.scores = prm.scores;
+    kp.stats = prm.stats;
+    kp.indices = prm.indices;
+    kp.status = prm.status;
+    kp.weights = kw->base;
+    for (int i = 0; i < 3; ++i) kp.strides[i] = kw->strides[i];
+    kp.num_tiles = h->n_key_tiles;
+    kp.num_pages = prm.num_pages;
+    kp.num_qo_heads = h->num_qo_heads;
+    kp.num_kv_heads = h->num_kv_heads;
+    kp.page_size = h->page_size;
+    kp.q_len = h->q_len;
+    // units of (tile, kv head), at most as many CTAs as the GPU holds at once, which take them in turn;
+    // CUDA-graph mode: that many for every plan
+    const int64_t units = (int64_t)h->n_key_tiles * h->num_kv_heads, most = (int64_t)h->num_sms * 8;
+    const int64_t ctas = h->graph ? most : std::min(units, most);
+    if (ctas > 0) {
+      void* kargs[] = {&kp};
+      cudaLaunchConfig_t cfg;
+      std::memset(&cfg, 0, sizeof cfg);
+      cfg.gridDim = dim3((unsigned)ctas);
+      cfg.blockDim = dim3(kKeyTileTokens);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = h->pdl ? 1 : 0;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaLaunchKernelExC(&cfg, key_weights_fn(), kargs);
+      if (e != cudaSuccess) return cuda_fail(e, "key weights kernel launch");
+    }
+  }
   if (ev_end && (e = cudaEventRecord(static_cast<cudaEvent_t>(ev_end), s)) != cudaSuccess)
     return cuda_fail(e, "cudaEventRecord");
 
@@ -1008,15 +1135,42 @@ extern "C" {
 int pkd_run_timed(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
                   int64_t num_pages, const int64_t kv_strides[3], float q_scale, float k_scale,
                   float v_scale, void* o, float* lse, void* stream, void* ev_start, void* ev_end) {
-  return run_decode(h, q, k_base, v_base, num_pages, kv_strides, nullptr, q_scale, k_scale, v_scale,
-                    o, lse, stream, ev_start, ev_end);
+  return run_decode(h, q, k_base, v_base, num_pages, kv_strides, nullptr, nullptr, q_scale, k_scale,
+                    v_scale, o, lse, stream, ev_start, ev_end);
 }
 
 int pkd_run_scaled(pkd_handle* h, const pkd_scaled_run* r, void* stream) {
   if (!r) return fail(PKD_ERR_INVALID_ARG, "run is null");
   const ScalePools sf{r->k_scales, r->v_scales, r->scale_strides};
-  return run_decode(h, r->q, r->k, r->v, r->num_pages, r->strides, &sf, r->q_scale, r->k_scale,
+  return run_decode(h, r->q, r->k, r->v, r->num_pages, r->strides, &sf, nullptr, r->q_scale, r->k_scale,
                     r->v_scale, r->o, r->lse, stream, r->ev_start, r->ev_end);
+}
+
+int pkd_run_key_weights(pkd_handle* h, const pkd_key_weights_run* w, void* stream) {
+  return guarded([&]() -> int {
+    if (!w) return fail(PKD_ERR_INVALID_ARG, "run is null");
+    const pkd_scaled_run& r = w->run;
+    const ScalePools sf{r.k_scales, r.v_scales, r.scale_strides};
+    const WeightPool kw{w->key_weights, w->weight_strides};
+    return run_decode(h, r.q, r.k, r.v, r.num_pages, r.strides, r.k_scales || r.v_scales ? &sf : nullptr, &kw,
+                      r.q_scale, r.k_scale, r.v_scale, r.o, r.lse, stream, r.ev_start, r.ev_end);
+  });
+}
+
+int pkd_key_weights_workspace_bytes(int64_t max_pages, int page_size, int max_batch, int q_len_per_req,
+                                    int num_qo_heads, size_t* float_ws_bytes, size_t* int_ws_bytes) {
+  if (max_pages < 0 || page_size < 8 || page_size > 256 || max_batch < 0 || q_len_per_req < 1 || num_qo_heads < 1 ||
+      max_pages > (int64_t(1) << 40))
+    return fail(PKD_ERR_INVALID_ARG, "bad capacity or head count");
+  // a row's scores: at most its request's tokens, and less than a page each for the rounded start of
+  // its window and end of its sinks, and of the whole (16 keys, at most two pages)
+  const size_t rows = (size_t)max_batch * q_len_per_req;
+  const size_t keys = ((size_t)max_pages * q_len_per_req + 4 * rows) * page_size;
+  if (float_ws_bytes) *float_ws_bytes = 512 + 512 + (keys + 2 * rows) * num_qo_heads * sizeof(float);
+  // two runs of tiles a request, each with a last one that is not full
+  const size_t tiles = (size_t)max_pages * page_size / kKeyTileTokens + 3 * (size_t)max_batch;
+  if (int_ws_bytes) *int_ws_bytes = 512 + 256 + rows * sizeof(KeyRow) + tiles * sizeof(KeyTile);
+  return PKD_OK;
 }
 
 int pkd_run(pkd_handle* h, const void* q, const void* k_base, const void* v_base,

@@ -71,6 +71,20 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 int noalloc_check_status(uint32_t* status, cudaStream_t stream);
 enum KernelKind { kCudaCore = 0, kTensorCore = 1 };
 
+// Plans with key weights.  Where the scores of one output row's attended keys lie: key t of qo head g
+// at base + g * stride + t for the sinks, t + shift for the window (both parts start at a page's first
+// slot, so that a warp's 16 keys fill whole 32-byte sectors).  The row attends t < sink and win <= t < n.
+struct KeyRow {
+  int64_t base;
+  int32_t stride, sink, win, n, shift, pad;
+};
+static_assert(sizeof(KeyRow) == 32, "KeyRow is 8 int32");
+// Keys [t0, t1) of a request that at least one of its rows may attend, at most kKeyTileTokens of them.
+struct KeyTile {
+  int32_t req, t0, t1, page_base;
+};
+constexpr int kKeyTileTokens = 256;
+
 // Kernel parameters, passed by value as a __grid_constant__ so the tensor maps stay in
 // parameter space (where the TMA unit may read them).
 struct DecodeParams {
@@ -107,7 +121,29 @@ struct DecodeParams {
                         // cap or divided by the cap with one
   float cap_log2;       // cap * log2(e), 0 = no cap
   float v_scale;
+  // plans with key weights, else null: per row and qo head the softmax statistics {M, 1 / L}; the
+  // attended keys' scores (base 2), and where a row's lie
+  float2* stats;
+  float* scores;
+  const KeyRow* key_rows;
 };
+
+// A decode with key weights, its second kernel (key_weights.cu).
+struct KeyWeightParams {
+  const KeyTile* tiles;
+  const int32_t* tile_count;  // CUDA-graph mode: the plan's tiles, read on the device; else null
+  const KeyRow* rows;
+  const float* scores;
+  const float2* stats;
+  const int32_t* indices;
+  const uint32_t* status;
+  float* weights;
+  int64_t strides[3];  // of page, kv head, slot
+  int num_tiles;
+  uint32_t num_pages;
+  int num_qo_heads, num_kv_heads, page_size, q_len;
+};
+const void* key_weights_fn();
 
 // The parameters of a kernel over a 4-bit cache: 5-D maps over the code pools (d, head and slot in
 // the layout's order, K/V, page) and the e4m3 scale of (page, slot, head, block) at base +
@@ -137,6 +173,7 @@ struct DecodeKernel {
   int nstages;      // pipeline stages
   int max_ctas = kDecodeCtasPerSm;  // CTAs per SM it is sized for
   int box_rows = 0;                 // rows of a tensor-map box at most; 0: tile_tokens
+  int scores = 0;                   // 1: leaves the attended keys' scores (plans with key weights)
 };
 
 // Registries filled by the kernel translation units.
@@ -147,6 +184,8 @@ void register_decode_rope(std::vector<DecodeKernel>& out);
 void register_decode_rope_cc(std::vector<DecodeKernel>& out);
 void register_decode_rope_cc_e4m3(std::vector<DecodeKernel>& out);
 void register_decode_e2m1(std::vector<DecodeKernel>& out);
+void register_decode_weights(std::vector<DecodeKernel>& out);
+void register_decode_e2m1_weights(std::vector<DecodeKernel>& out);
 
 // MLA decode kernel parameters (pkd_mla_run -> mla_decode_kernel).
 struct MlaParams {
@@ -268,6 +307,11 @@ int decode_geometry(const PlanRequest& r, DecodeSchedule* s, const char** err);
 // Cuts every row's attended tokens into tasks per (kv head, slice), one per CTA, longest first.
 int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, const char** err);
 
+// The lists of a plan with key weights: every row's KeyRow (rows of them), the tiles (up to tiles_cap
+// are written, *n_tiles counts all) and the floats that the scores take.
+void key_weight_lists(const PlanRequest& r, KeyRow* rows, KeyTile* tiles, int64_t tiles_cap,
+                      int64_t* n_tiles, int64_t* score_floats);
+
 // CTAs per SM the decode kernel of a request is sized for (DecodeKernel::max_ctas): two, but for
 // some kernels over a 4-bit cache.
 int decode_max_ctas(const PlanRequest& r);
@@ -301,6 +345,16 @@ inline size_t dws_part_lse_offset(const DecodeWsLayout& l, int head_dim) {
 inline size_t dws_float_bytes(const DecodeWsLayout& l, int head_dim) {
   return dws_part_lse_offset(l, head_dim) + align256(l.slots * kSlotHeads * sizeof(float)) + 256;
 }
+// A plan with key weights keeps more behind these.  int: [rows | tiles]; float: [stats (float2 per row
+// and qo head) | scores].
+struct KeyWsLayout {
+  size_t rows = 0, tiles = 0, row_heads = 0, scores = 0;
+  size_t int_off = 0, float_off = 0;  // bytes of the parts above
+  size_t tiles_off() const { return int_off + align256(rows * sizeof(KeyRow)); }
+  size_t int_end() const { return tiles_off() + align256(tiles * sizeof(KeyTile)); }
+  size_t scores_off() const { return float_off + align256(row_heads * sizeof(float2)); }
+  size_t float_end() const { return scores_off() + align256(scores * sizeof(float)); }
+};
 // CUDA-graph mode: a work list of at most max_items chunks per row (summed over rows) holds at
 // most max_items x Hkv x slices tasks (the fixed grid), half as many merge entries, as many
 // slots.
@@ -312,6 +366,7 @@ inline DecodeWsLayout decode_capacity_layout(size_t max_items, int num_kv_heads,
 // Byte offsets inside the int workspace.
 constexpr size_t kStatusBytes = 256;
 constexpr size_t kItemCountOffset = 64;  // int32 inside the status block (CUDA-graph mode)
+constexpr size_t kTileCountOffset = 68;  // likewise: the tiles of a plan with key weights
 
 // Capacities the workspaces are cut for: a plan's own counts, or in CUDA-graph mode fixed
 // maxima, so that every address a captured launch holds stays valid for later plans.

@@ -799,4 +799,33 @@ int build_decode_schedule(const PlanRequest& r, int ctas, DecodeSchedule* s, con
   return 0;
 }
 
+void key_weight_lists(const PlanRequest& r, KeyRow* rows, KeyTile* tiles, int64_t tiles_cap,
+                      int64_t* n_tiles, int64_t* score_floats) {
+  const int ps = r.page_size, ql = r.q_len > 0 ? r.q_len : 1;
+  int64_t floats = 0, n = 0;
+  for (int row = 0; row < rows_of(r); ++row) {
+    const RowSpan sp = row_span(r, row);
+    const int64_t first = sp.w / ps * ps, sinks = (sp.s + ps - 1) / ps * ps;
+    const int64_t stride = (sinks + sp.n - first + 15) / 16 * 16;
+    if (rows)
+      rows[row] = {floats, (int32_t)stride, (int32_t)sp.s, (int32_t)sp.w, (int32_t)sp.n,
+                   (int32_t)(sinks - first), 0};
+    floats += stride * r.num_qo_heads;
+  }
+  auto add = [&](int req, int64_t from, int64_t to) {
+    for (int64_t t = from; t < to; t += kKeyTileTokens, ++n)
+      if (n < tiles_cap)
+        tiles[n] = {req, (int32_t)t, (int32_t)std::min<int64_t>(to, t + kKeyTileTokens), r.indptr[req]};
+  };
+  for (int i = 0; i < r.batch; ++i) {
+    // the first row's window begins first and the last row's ends last; a row without a gap attends
+    // all before its end, and its window begins at 0
+    const RowSpan a = row_span(r, i * ql), z = row_span(r, i * ql + ql - 1);
+    if (a.w > 0) add(i, 0, a.s);
+    add(i, std::max(a.w / ps * ps, a.s), z.n);
+  }
+  *n_tiles = n;
+  *score_floats = floats;
+}
+
 }  // namespace pkd

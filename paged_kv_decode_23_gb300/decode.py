@@ -61,6 +61,15 @@ def pool_views(paged_kv_cache, kv_layout: str, what: str = "paged_kv_cache"):
     return kp, vp, (st[0], st[2], st[1]), shape[2], shape[1]
 
 
+def weight_views(weights, pages: int, num_kv_heads: int, page_size: int, dev: int):
+    """(address, strides of page, kv head and slot) of a pool of key weights."""
+    if (not isinstance(weights, torch.Tensor) or weights.dtype is not torch.float32
+            or weights.shape != (pages, num_kv_heads, page_size) or weights.get_device() != dev):
+        raise ValueError(f"key_weights must be a float32 tensor [{pages} pages, {num_kv_heads} kv heads, "
+                         f"{page_size} slots] on cuda:{dev}")
+    return (weights.data_ptr(), *weights.stride())
+
+
 def _host_i32(t) -> np.ndarray:
     """A contiguous host int32 array of `t` (no copy when it already is one)."""
     if isinstance(t, torch.Tensor):
@@ -81,6 +90,7 @@ def _i32p(a: np.ndarray) -> int:
 
 _PLAN = struct.Struct("@3Pq4f16i")  # pkd_plan_args
 _SCALED_RUN = struct.Struct("@5Pq3q3q4P3fi")  # pkd_scaled_run
+_KEY_WEIGHTS_RUN = struct.Struct("@P3q")  # what follows it in pkd_key_weights_run
 
 # The current stream's handle on a device.  torch's own accessor of the handle takes a tenth of the
 # time of building a Stream object for it; where torch has none, the object does.
@@ -233,7 +243,8 @@ class BatchDecodePagedKV:
              use_tensor_cores: Optional[bool] = None, stream=None,
              q_len_per_req: int = 1, rope_scale: Optional[float] = None,
              rope_theta: Optional[float] = None, block_tables: Optional[torch.Tensor] = None,
-             seq_lens: Optional[torch.Tensor] = None, num_sink_tokens: int = 0) -> None:
+             seq_lens: Optional[torch.Tensor] = None, num_sink_tokens: int = 0,
+             key_weights: bool = False) -> None:
         """Plan a batch; ``indptr`` / ``last_page_len`` may live on the host or the device
         (a device copy is read back once here), ``indices`` must be a CUDA int32 tensor and
         stay unchanged while runs of this plan are in flight.  ``q_len_per_req`` query tokens
@@ -247,7 +258,11 @@ class BatchDecodePagedKV:
         ``num_sink_tokens``: with a window, the first tokens of each request that stay visible
         beside it (attention sinks): a row at position p attends t < num_sink_tokens and
         t >= p - window_left.  What lies in between is not read, so its pages may go back to the
-        allocator and their entries of ``indices`` hold anything."""
+        allocator and their entries of ``indices`` hold anything.
+
+        ``key_weights=True``: runs of this plan take a ``key_weights`` pool and add every key's
+        softmax weight to it (tensor-core kernel, without ROPE_LLAMA).  The float workspace then also
+        holds the attended keys' scores, 4 bytes a key, row and query head (``workspace_bytes``)."""
         if block_tables is not None or seq_lens is not None:
             raise NotImplementedError("block_tables / seq_lens (the trtllm-gen backend's page "
                                       "table form) are not built; pass indptr / indices / "
@@ -277,13 +292,13 @@ class BatchDecodePagedKV:
             1e4 if rope_theta is None else float(rope_theta), batch, num_qo_heads, num_kv_heads,
             head_dim, page_size, int(window_left), int(fixed_split_size or 0),
             int(bool(disable_split_kv)), _DTYPE_CODE[q_dt], _DTYPE_CODE[kv_dt], _DTYPE_CODE[o_dt],
-            kernel, int(q_len_per_req), pos_code, int(num_sink_tokens), 0)
+            kernel, int(q_len_per_req), pos_code, int(num_sink_tokens), int(bool(key_weights)))
         L.check(L.lib().pkd_plan_with(self._h, args, _stream_ptr(stream)))
         self._indices = indices
         self._plan_args = dict(batch=batch, q_len=int(q_len_per_req), rows=batch * int(q_len_per_req),
                                num_qo_heads=num_qo_heads, num_kv_heads=num_kv_heads,
                                head_dim=head_dim, page_size=page_size, q_dtype=q_dt,
-                               kv_dtype=kv_dt, o_dtype=o_dt)
+                               kv_dtype=kv_dt, o_dtype=o_dt, key_weights=bool(key_weights))
 
     # ------------------------------------------------------------------ run
     def _kv_pointers(self, paged_kv_cache):
@@ -320,7 +335,8 @@ class BatchDecodePagedKV:
             v_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
             lse: Optional[torch.Tensor] = None, return_lse: bool = False, stream=None,
             timing_events=None, enable_pdl: Optional[bool] = None,
-            q_len_per_req: Optional[int] = None, kv_block_scales=None):
+            q_len_per_req: Optional[int] = None, kv_block_scales=None,
+            key_weights: Optional[torch.Tensor] = None):
         """Decode attention for the planned batch on one layer's pool: returns ``o`` or
         ``(o, lse)`` (lse: float32 natural log, ``[batch, num_qo_heads]``).  ``enable_pdl``
         switches programmatic dependent launch for this and later runs (on by default).
@@ -328,7 +344,12 @@ class BatchDecodePagedKV:
         A plan with ``kv_data_type="e2m1"`` (4 bits) takes the codes as ``paged_kv_cache`` (uint8
         or float4_e2m1fn_x2, last axis head_dim / 2) and their e4m3 scales, one per 16 values, as
         ``kv_block_scales`` (float8_e4m3fn or uint8, last axis head_dim / 16; a 5-D tensor or a
-        (k, v) pair in the same layout)."""
+        (k, v) pair in the same layout).
+
+        A plan with ``key_weights=True`` takes ``key_weights``, float32 ``[pages, num_kv_heads,
+        page_size]`` in either layout, and adds to each attended key's entry its softmax weight, summed
+        over the query heads of its kv head and the request's query tokens.  Other entries are left as
+        they are; a page that several requests share takes all their sums (in no fixed order)."""
         a = self._plan_args
         if a is None:
             raise RuntimeError("plan() must be called before run()")
@@ -341,9 +362,14 @@ class BatchDecodePagedKV:
         if (kv_block_scales is not None) != (a["kv_dtype"] == E2M1):
             raise ValueError("kv_block_scales belongs to a plan with kv_data_type 'e2m1', and such "
                              "a plan needs it")
-        if kv_block_scales is not None:
+        if (key_weights is not None) != a["key_weights"]:
+            raise ValueError("key_weights belongs to a plan with key_weights=True, and such a plan "
+                             "needs it")
+        if key_weights is not None and not isinstance(key_weights, torch.Tensor):
+            raise ValueError("key_weights must be a CUDA float32 tensor")
+        if kv_block_scales is not None or key_weights is not None:
             return self._run_scaled(q, paged_kv_cache, kv_block_scales, q_scale, k_scale, v_scale, out,
-                                    lse, return_lse, stream, timing_events, enable_pdl)
+                                    lse, return_lse, stream, timing_events, enable_pdl, key_weights)
         kv, k_ptr, v_ptr, num_pages, strides = self._kv_pointers(paged_kv_cache)
         if kv.dtype != a["kv_dtype"]:
             raise ValueError(f"KV dtype {kv.dtype} does not match the plan ({a['kv_dtype']})")
@@ -369,29 +395,38 @@ class BatchDecodePagedKV:
         return (out, lse) if return_lse else out
 
     def _run_scaled(self, q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse, stream,
-                    timing_events, enable_pdl):
-        """run() on a plan with a 4-bit cache; q's shape and dtype are checked."""
-        if (torch.is_grad_enabled() and q.requires_grad) or forward_ad._current_level >= 0:
-            refuse_gradients("decode over a 4-bit cache", q)
+                    timing_events, enable_pdl, weights=None):
+        """run() on a plan with a 4-bit cache or with key weights; q's shape and dtype are checked."""
+        if (torch.is_grad_enabled() and (q.requires_grad or (weights is not None and weights.requires_grad))
+                ) or forward_ad._current_level >= 0:
+            refuse_gradients("decode over a 4-bit cache" if weights is None else "decode with key weights", q, weights)
         a = self._plan_args
         rows, hq, d, ps, hkv = a["rows"], a["num_qo_heads"], a["head_dim"], a["page_size"], a["num_kv_heads"]
         dev = q.get_device()
         if dev >= 0 and current_device() != dev:
             with torch.cuda.device(dev):
                 return self._run_scaled(q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse,
-                                        stream, timing_events, enable_pdl)
+                                        stream, timing_events, enable_pdl, weights)
         kv = cache[0] if isinstance(cache, (tuple, list)) else cache
-        sf = scales[0] if isinstance(scales, (tuple, list)) else scales
         k_ptr, v_ptr, strides, kv_ps, kv_hkv = pool_views(cache, self.kv_layout)
-        ks, vs, sf_strides, sf_ps, sf_hkv = pool_views(scales, self.kv_layout, "kv_block_scales")
         pages = kv.shape[0]
-        if kv.dtype not in CODE_DTYPES or (kv_ps, kv_hkv, 2 * kv.shape[-1]) != (ps, hkv, d):
-            raise ValueError(f"paged_kv_cache of {kv.dtype} {tuple(kv.shape)} does not match the plan: "
-                             f"4-bit codes, {d // 2} bytes a row")
-        if sf.dtype not in SCALE_DTYPES or (sf.shape[0], sf_ps, sf_hkv, 16 * sf.shape[-1]) != (pages, ps, hkv, d):
-            raise ValueError("kv_block_scales must be float8_e4m3fn (or uint8) of the cache's shape "
-                             "with a last axis of head_dim / 16")
-        if not (dev == kv.get_device() == sf.get_device() == self._float_ws.get_device()):
+        if scales is None:
+            if kv.dtype is not a["kv_dtype"] or (kv_ps, kv_hkv, kv.shape[-1]) != (ps, hkv, d):
+                raise ValueError(f"paged_kv_cache of {kv.dtype} {tuple(kv.shape)} does not match the plan")
+            ks = vs = 0
+            sf_strides = (0, 0, 0)
+        else:
+            sf = scales[0] if isinstance(scales, (tuple, list)) else scales
+            ks, vs, sf_strides, sf_ps, sf_hkv = pool_views(scales, self.kv_layout, "kv_block_scales")
+            if kv.dtype not in CODE_DTYPES or (kv_ps, kv_hkv, 2 * kv.shape[-1]) != (ps, hkv, d):
+                raise ValueError(f"paged_kv_cache of {kv.dtype} {tuple(kv.shape)} does not match the plan: "
+                                 f"4-bit codes, {d // 2} bytes a row")
+            if sf.dtype not in SCALE_DTYPES or (sf.shape[0], sf_ps, sf_hkv, 16 * sf.shape[-1]) != (pages, ps, hkv, d):
+                raise ValueError("kv_block_scales must be float8_e4m3fn (or uint8) of the cache's shape "
+                                 "with a last axis of head_dim / 16")
+            if sf.get_device() != dev:
+                raise ValueError("q, the cache, its scales and the workspace must be on one device")
+        if not (dev == kv.get_device() == self._float_ws.get_device()):
             raise ValueError("q, the cache, its scales and the workspace must be on one device")
         if out is None:
             out = torch.empty_like(q) if stream is None else new_output((rows, hq, d), q, q.dtype, stream)
@@ -413,7 +448,11 @@ class BatchDecodePagedKV:
             0 if lse is None else lse.data_ptr(), 0 if ev0 is None else ev0.cuda_event,
             0 if ev1 is None else ev1.cuda_event, 1.0 if q_scale is None else q_scale,
             1.0 if k_scale is None else k_scale, 1.0 if v_scale is None else v_scale, 0)
-        rc = L.lib().pkd_run_scaled(self._h, args, raw_stream(dev) if stream is None else stream.cuda_stream)
+        call = L.lib().pkd_run_scaled
+        if weights is not None:
+            call = L.lib().pkd_run_key_weights
+            args += _KEY_WEIGHTS_RUN.pack(*weight_views(weights, pages, hkv, ps, dev))
+        rc = call(self._h, args, raw_stream(dev) if stream is None else stream.cuda_stream)
         if rc:
             L.check(rc)
         return (out, lse) if return_lse else out
@@ -504,12 +543,12 @@ def plan_host(indptr, last_page_len, num_qo_heads: int, num_kv_heads: int, head_
 
 def _host_plan_args(ip, lpl, num_qo_heads, num_kv_heads, head_dim, page_size, window_left,
                     fixed_split_size, disable_split_kv, kv_dtype, use_tensor_cores, q_len_per_req,
-                    num_sink_tokens) -> bytes:
+                    num_sink_tokens, key_weights=False) -> bytes:
     """pkd_plan_args for the host-only calls (ip and lpl stay alive with the caller)."""
     return _plan_args(_i32p(ip), _i32p(lpl), 0, 0, float("nan"), 0.0, 1.0, 1e4, len(lpl), num_qo_heads,
                       num_kv_heads, head_dim, page_size, int(window_left), int(fixed_split_size),
                       int(bool(disable_split_kv)), L.DTYPE_F16, kv_dtype, L.DTYPE_F16, use_tensor_cores,
-                      int(q_len_per_req), 0, int(num_sink_tokens), 0)
+                      int(q_len_per_req), 0, int(num_sink_tokens), int(bool(key_weights)))
 
 
 def _plan_tasks(args: bytes, num_sms: int, work_capacity: int) -> dict:
@@ -566,21 +605,31 @@ def workspace_bytes(indptr, last_page_len, num_qo_heads: int, num_kv_heads: int,
                     page_size: int, window_left: int = -1, fixed_split_size: int = 0,
                     disable_split_kv: bool = False, kv_dtype: int = L.DTYPE_F16,
                     use_tensor_cores: int = L.KERNEL_AUTO, num_sms: int = 152,
-                    q_len_per_req: int = 1, num_sink_tokens: int = 0):
+                    q_len_per_req: int = 1, num_sink_tokens: int = 0, key_weights: bool = False):
     """(float, int) workspace bytes of a plan."""
     ip = _host_i32(indptr)
     lpl = _host_i32(last_page_len)
     fb, ib = ctypes.c_size_t(), ctypes.c_size_t()
     args = _host_plan_args(ip, lpl, num_qo_heads, num_kv_heads, head_dim, page_size, window_left,
                            fixed_split_size, disable_split_kv, kv_dtype, use_tensor_cores,
-                           q_len_per_req, num_sink_tokens)
+                           q_len_per_req, num_sink_tokens, key_weights)
     L.check(L.lib().pkd_plan_workspace_bytes(args, num_sms, ctypes.byref(fb), ctypes.byref(ib)))
     return fb.value, ib.value
 
 
 def graph_workspace_bytes(max_items: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
-                          use_tensor_cores: int = L.KERNEL_AUTO):
-    """(float, int) workspace bytes that CUDA-graph mode needs for ``max_items`` chunks."""
+                          use_tensor_cores: int = L.KERNEL_AUTO, key_weights_pages: Optional[int] = None,
+                          page_size: int = 0, max_batch: int = 0, q_len_per_req: int = 1):
+    """(float, int) workspace bytes that CUDA-graph mode needs for ``max_items`` chunks; for plans with
+    key weights also ``key_weights_pages``, the most pages that a plan's requests own together, with
+    ``page_size`` and ``max_batch``."""
+    if key_weights_pages is not None:
+        f0, i0 = graph_workspace_bytes(max_items, num_qo_heads, num_kv_heads, head_dim, use_tensor_cores)
+        fb, ib = ctypes.c_size_t(), ctypes.c_size_t()
+        L.check(L.lib().pkd_key_weights_workspace_bytes(int(key_weights_pages), int(page_size), int(max_batch),
+                                                        int(q_len_per_req), num_qo_heads, ctypes.byref(fb),
+                                                        ctypes.byref(ib)))
+        return f0 + fb.value, i0 + ib.value
     fb, ib = ctypes.c_size_t(), ctypes.c_size_t()
     L.check(L.lib().pkd_graph_workspace_bytes(int(max_items), num_qo_heads, num_kv_heads,
                                               head_dim, use_tensor_cores, ctypes.byref(fb),

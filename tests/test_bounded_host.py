@@ -132,3 +132,41 @@ def test_workspace_bytes_of_a_plan_with_sinks_are_those_of_what_it_attends():
     whole = workspace_bytes(indptr, last, 32, 8, 128, 16)
     part = workspace_bytes(indptr, last, 32, 8, 128, 16, window_left=1000, num_sink_tokens=16)
     assert 0 < part[0] <= whole[0] and 0 < part[1] <= whole[1]
+
+
+def test_key_weight_plans_that_are_refused_and_what_they_take():
+    from paged_kv_decode_23_gb300 import PkdError, graph_workspace_bytes, workspace_bytes
+    lens = [5000, 0, 77]
+    indptr, last = _table(lens, 16)
+    plain = workspace_bytes(indptr, last, 32, 8, 128, 16)
+    with_keys = workspace_bytes(indptr, last, 32, 8, 128, 16, key_weights=True)
+    scores = 32 * sum(-(-n // 16) * 16 for n in lens) * 4
+    assert scores <= with_keys[0] - plain[0] <= scores + 2048 and with_keys[1] > plain[1]
+    bounded = workspace_bytes(indptr, last, 32, 8, 128, 16, key_weights=True, window_left=255, num_sink_tokens=4)
+    assert bounded[0] < plain[0] + 32 * 4 * (5000 // 4)
+    with pytest.raises(PkdError, match="UNSUPPORTED"):
+        workspace_bytes(indptr, last, 32, 8, 128, 16, key_weights=True, use_tensor_cores=0)
+    a, b = graph_workspace_bytes(400, 32, 8, 128), graph_workspace_bytes(400, 32, 8, 128, key_weights_pages=500, page_size=16, max_batch=8)
+    assert b[0] - a[0] >= 500 * 16 * 32 * 4 and b[1] > a[1]
+    for bad in (dict(key_weights_pages=-1, page_size=16, max_batch=8), dict(key_weights_pages=5, page_size=0, max_batch=8)):
+        with pytest.raises(PkdError):
+            graph_workspace_bytes(400, 32, 8, 128, **bad)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_the_graph_workspace_covers_every_plan(seed):
+    """What plans of a capacity need stays inside the two bounds together."""
+    from paged_kv_decode_23_gb300 import graph_workspace_bytes, workspace_bytes
+    rng = np.random.default_rng(seed)
+    page, q_len, group = int(rng.choice([8, 16, 256])), int(rng.choice([1, 3])), int(rng.choice([1, 4, 12]))
+    batch = int(rng.integers(1, 9))
+    lens = rng.integers(0, 3000, batch)
+    indptr, last = _table(lens, page)
+    items = batch * q_len + 304
+    kw = dict(window_left=int(rng.integers(0, 2000)), num_sink_tokens=int(rng.choice([0, 3, 100])), q_len_per_req=q_len)
+    need = workspace_bytes(indptr, last, 2 * group, 2, 128, page, key_weights=True, **kw)
+    base = workspace_bytes(indptr, last, 2 * group, 2, 128, page, **kw)
+    have = graph_workspace_bytes(items, 2 * group, 2, 128, key_weights_pages=int(indptr[-1]), page_size=page, max_batch=batch,
+                                 q_len_per_req=q_len)
+    floor = graph_workspace_bytes(items, 2 * group, 2, 128)
+    assert have[0] - floor[0] >= need[0] - base[0] and have[1] - floor[1] >= need[1] - base[1]
