@@ -591,6 +591,46 @@ typedef struct pkd_gather_args {
 int pkd_gather(const pkd_gather_args* args, void* stream);
 
 /*
+ * Cut every sequence of a cache back to `budget` tokens, in place and for each kv head by itself: its
+ * first num_sink_tokens (S), its newest num_recent (R), and of the tokens between them the
+ * budget - S - R (B - S - R) with the largest key_weights stay (the sums that pkd_run_key_weights
+ * adds to; equal ones by slot, NaN above all).  kv_lens (device [batch]) are the lengths n.  A
+ * sequence of at most `budget` tokens is left alone.  Else its slots then hold
+ *   [0, S)        what they held;
+ *   [S, B - R)    the tokens chosen: those that lie there stay, the i-th other slot takes the i-th
+ *                 chosen token of [B - R, n - R);
+ *   [B - R, B)    the newest, in order;
+ *   [B, n)        what they held, now free: the sequence's length is min(n, budget), and the pages
+ *                 behind it may be given back.
+ * Key weights move with their tokens; those of [B, n) become 0, so that slots without a token hold 0.
+ * Keys keep the rotation that they were appended with (pkd_append's rope_positions), and their order
+ * means nothing to attention; ROPE_LLAMA, ALIBI and window_left, which count slots, do not go with it.
+ *   kept   device [batch, num_kv_heads, budget] or NULL: the slot whose token now lies in each slot, -1
+ *          behind the sequence's end.
+ *   moves  device workspace of batch * num_kv_heads * (budget - S - R) pairs of int32, 8-byte aligned
+ *          (NULL if that is 0).
+ * A sequence with a negative length, or more tokens than its pages hold, sets PKD_STATUS_BAD_TOKEN in
+ * status (may be NULL), one whose page ids lie outside the pool PKD_STATUS_BAD_PAGE; it is left alone, its kept entries -1.
+ * Sequences must not share pages of tokens that move or whose places are taken (none that are evicted
+ * should: see pkd_pages_fork).  The pool's rows must not overlap, nor key_weights' entries (strides of
+ * page, head, slot in elements).  k_scale and v_scale are not used.
+ */
+typedef struct pkd_evict_args {
+  pkd_paged_pool pool;
+  float* key_weights;
+  int64_t weight_strides[3];
+  const int32_t* kv_lens;
+  int32_t* kept;
+  int32_t* moves;
+  uint32_t* status;
+  int32_t budget;
+  int32_t num_sink_tokens;
+  int32_t num_recent;
+  int32_t reserved;
+} pkd_evict_args;
+int pkd_evict(const pkd_evict_args* args, void* stream);
+
+/*
  * Copy pages dst_pages[i] <- src_pages[i] in every one of n_pools pools (every layer's K, V and
  * scales): page p of pool j is the page_bytes[j] bytes at bases[j] + p * page_strides[j].
  * src_pages / dst_pages: host arrays, travelling with the launch (nothing is uploaded, and they

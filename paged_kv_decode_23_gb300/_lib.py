@@ -54,6 +54,7 @@ SIGNATURES = {
     "pkd_run_scaled": (_c_int, [_vp, ctypes.c_char_p, _vp]),
     "pkd_append": (_c_int, [ctypes.c_char_p, _vp]),
     "pkd_gather": (_c_int, [ctypes.c_char_p, _vp]),
+    "pkd_evict": (_c_int, [ctypes.c_char_p, _vp]),
     "pkd_copy_pages": (_c_int, [_vp, _vp, _vp, _c_int, ctypes.c_int64, _vp, _vp, ctypes.c_int64, _vp]),
     "pkd_pages_create": (_c_int, [ctypes.POINTER(_vp), ctypes.c_int64]),
     "pkd_pages_destroy": (_c_int, [_vp]),

@@ -18,11 +18,12 @@ import torch
 
 from . import _lib as L
 from .decode import (_DTYPE_CODE, CODE_DTYPES, SCALE_DTYPES, current_device, forward_ad, new_output,
-                     pool_views, raw_stream, refuse_gradients)
+                     pool_views, raw_stream, refuse_gradients, weight_views)
 
 _POOL = "4Pq3q3q2Pq5i2fi"  # pkd_paged_pool
 _APPEND = struct.Struct("@" + _POOL + "4P8q3P2PPqPqd6i")  # pkd_append_args
 _GATHER = struct.Struct("@" + _POOL + "2P4q2PPq2i")  # pkd_gather_args
+_EVICT = struct.Struct("@" + _POOL + "P3q4P4i")  # pkd_evict_args
 _IO_DTYPES = (torch.float16, torch.bfloat16)
 
 
@@ -256,6 +257,54 @@ def gather_paged_kv(batch_indices: torch.Tensor, positions: torch.Tensor, paged_
                         _DTYPE_CODE[out_dtype], 0)
     _launch(L.lib().pkd_gather, dev, stream, args)
     return k, v
+
+
+def evict_paged_kv(paged_kv_cache, key_weights: torch.Tensor, kv_lens: torch.Tensor, kv_indptr: torch.Tensor,
+                   kv_indices: torch.Tensor, budget: int, kv_layout: str = "NHD", *, num_sink_tokens: int = 0,
+                   num_recent: int = 0, kv_block_scales=None, return_kept: bool = False,
+                   status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Cut every sequence back to ``budget`` tokens, in place (pkd_evict): each kv head keeps its first
+    ``num_sink_tokens``, its newest ``num_recent`` and the tokens with the largest ``key_weights``
+    (float32 ``[pages, num_kv_heads, page_size]``, what ``BatchDecodePagedKV.run`` adds to).
+    ``kv_lens`` (device int32 ``[batch]``) are the sequences' lengths; afterwards they are
+    ``min(kv_lens, budget)``, and the pages behind may be freed (``PageAllocator.free``).
+
+    The first tokens stay in place, the newest lie at the end in order, the others in any slots
+    between (those that can stay do), so append later keys with ``rope_positions`` of their own and
+    decode without window, ALIBI or ROPE_LLAMA.  Weights move with their tokens, and slots without a
+    token have weight 0 afterwards.  ``return_kept=True`` returns int32 ``[batch, num_kv_heads,
+    budget]``: the slot whose token each slot now holds, -1 behind the end.
+
+    ``status`` receives STATUS_BAD_TOKEN for a sequence longer than its pages (or of negative length),
+    STATUS_BAD_PAGE for one with a page id outside the pool; it is left alone.  The sequences must
+    own their pages alone."""
+    first = paged_kv_cache[0] if isinstance(paged_kv_cache, (tuple, list)) else paged_kv_cache
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("the cache must be a CUDA tensor")
+    if not isinstance(key_weights, torch.Tensor):
+        raise ValueError("key_weights must be a CUDA float32 tensor")
+    second = None if first is paged_kv_cache else paged_kv_cache[1]
+    if (torch.is_grad_enabled() and (first.requires_grad or key_weights.requires_grad
+                                     or (second is not None and second.requires_grad))
+            ) or forward_ad._current_level >= 0:
+        refuse_gradients("evict", first, second, key_weights)
+    io = first.dtype if first.dtype in _IO_DTYPES else torch.bfloat16
+    pool, hkv, _ = _pool_fields(paged_kv_cache, kv_block_scales, kv_indptr, kv_indices, kv_layout, None, None, dev, io)
+    batch, ps = pool[14], pool[18]
+    budget, sinks, recent = int(budget), int(num_sink_tokens), int(num_recent)
+    if not (1 <= budget < 2 ** 31 and 0 <= sinks and 0 <= recent and sinks + recent <= budget):
+        raise ValueError("budget must be a positive 32-bit number, num_sink_tokens and num_recent must be "
+                         ">= 0 and fit it together")
+    lens = _index(kv_lens, "kv_lens", dev, batch)
+    weights = weight_views(key_weights, first.shape[0], hkv, ps, dev)
+    heads, middle = batch * hkv, budget - sinks - recent
+    kept = new_output((batch, hkv, budget), first, _INT32, stream) if return_kept else None
+    moves = new_output((heads * middle, 2), first, _INT32, stream)
+    args = _EVICT.pack(*pool, *weights, lens, 0 if kept is None else kept.data_ptr(), moves.data_ptr(),
+                       _status(status, dev), budget, sinks, recent, 0)
+    _launch(L.lib().pkd_evict, dev, stream, args)
+    return kept
 
 
 def _page_ids(x, name: str) -> np.ndarray:

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <cstdint>
 #include <cstring>
 #include <exception>
 #include <new>
@@ -228,6 +229,32 @@ extern "C" int pkd_gather(const pkd_gather_args* args, void* stream) {
       return bad("k_out overlaps v_out");
     if (!a.batch_indices || !a.positions) return bad("null batch_indices / positions");
     return done(launch_gather(a, static_cast<cudaStream_t>(stream)), "gather kernel launch");
+  });
+}
+
+extern "C" int pkd_evict(const pkd_evict_args* args, void* stream) {
+  return guarded([&]() -> int {
+    if (!args) return bad("args is null");
+    const pkd_evict_args& a = *args;
+    const int dt = a.pool.dtype;
+    if (int rc = check_pool(a.pool, dt == PKD_DTYPE_BF16 ? PKD_DTYPE_BF16 : PKD_DTYPE_F16, true)) return rc;
+    if (int rc = check_written(a.pool)) return rc;
+    if (a.budget < 1) return bad("budget must be >= 1");
+    if (a.num_sink_tokens < 0 || a.num_recent < 0 || (int64_t)a.num_sink_tokens + a.num_recent > a.budget)
+      return bad("num_sink_tokens and num_recent must be >= 0 and fit the budget together");
+    if (a.pool.batch == 0) return done(cudaSuccess, "");
+    if ((int64_t)a.pool.batch * a.pool.num_kv_heads > INT32_MAX) return bad("batch * num_kv_heads is too large");
+    if (!a.kv_lens) return bad("null kv_lens");
+    if (!a.key_weights || reinterpret_cast<uintptr_t>(a.key_weights) % 4) return bad("key_weights is null or not aligned");
+    const int64_t n[3] = {a.pool.num_pages, a.pool.num_kv_heads, a.pool.page_size};
+    for (int i = 0; i < 3; ++i)
+      if (a.weight_strides[i] < 0 || (n[i] > 1 && a.weight_strides[i] > (int64_t(1) << 60) / n[i]))
+        return bad("key_weights strides must be positive, within 2^60 elements");
+    const int64_t st[3] = {a.weight_strides[0], a.weight_strides[2], a.weight_strides[1]};
+    if (!rows_apart(a.pool, st, 1)) return bad("entries of key_weights overlap");
+    if (!a.moves && a.num_sink_tokens + a.num_recent < a.budget) return bad("moves is null");
+    if (reinterpret_cast<uintptr_t>(a.moves) % 8) return bad("moves must be 8-byte aligned");
+    return done(launch_evict(a, static_cast<cudaStream_t>(stream)), "evict kernel launch");
   });
 }
 

@@ -8,9 +8,10 @@
 
 namespace pkd {
 
-// Launchers (cache_append.cu, cache_gather.cu, cache_copy.cu); arguments are checked.
+// Launchers (cache_append.cu, cache_gather.cu, cache_evict.cu, cache_copy.cu); arguments are checked.
 cudaError_t launch_append(const pkd_append_args& a, cudaStream_t s);
 cudaError_t launch_gather(const pkd_gather_args& a, cudaStream_t s);
+cudaError_t launch_evict(const pkd_evict_args& a, cudaStream_t s);
 
 // One pool of a page copy: page p is the `bytes` bytes at base + p * stride.
 struct CopyPool {

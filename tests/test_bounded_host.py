@@ -170,3 +170,32 @@ def test_the_graph_workspace_covers_every_plan(seed):
                                  q_len_per_req=q_len)
     floor = graph_workspace_bytes(items, 2 * group, 2, 128)
     assert have[0] - floor[0] >= need[0] - base[0] and have[1] - floor[1] >= need[1] - base[1]
+
+
+def _evict_args(**over):
+    """pkd_evict_args with made-up device addresses: for calls that fail before any launch."""
+    from paged_kv_decode_23_gb300 import cache
+    f = dict(k=4096, v=8192, ks=0, vs=0, pages=10, s0=4096, s1=256, s2=128, f0=0, f1=0, f2=0, ip=64, ix=64, nidx=9, batch=2,
+             dtype=1, hkv=2, d=128, ps=16, kscale=1.0, vscale=1.0, r=0, w=256, w0=32, w1=16, w2=1, lens=64, kept=0, moves=64,
+             status=0, budget=64, sinks=4, recent=8, r2=0)
+    f.update(over)
+    return cache._EVICT.pack(*f.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(budget=0), -1), (dict(budget=-3), -1), (dict(sinks=-1), -1), (dict(recent=-1), -1), (dict(sinks=60), -1),
+    (dict(recent=2 ** 31 - 1, sinks=2 ** 31 - 1), -1), (dict(w=0), -1), (dict(w=258), -1), (dict(w2=0), -1), (dict(w0=15), -1),
+    (dict(w1=-16), -1), (dict(w0=2 ** 62), -1), (dict(lens=0), -1), (dict(moves=0), -1), (dict(moves=68), -1), (dict(ip=0), -1),
+    (dict(ix=0), -1), (dict(k=0), -1), (dict(v=4096), -1), (dict(k=4100), -1), (dict(s1=100), -1), (dict(s0=128), -1),
+    (dict(dtype=3), -1), (dict(dtype=7), -5), (dict(d=96), -5), (dict(ps=12), -5), (dict(hkv=0), -1), (dict(batch=-1), -1),
+    (dict(pages=0), -1), (dict(batch=2 ** 20, hkv=2 ** 12), -1),
+])
+def test_evictions_that_are_refused(over, code):
+    from paged_kv_decode_23_gb300 import _lib as L
+    assert L.lib().pkd_evict(_evict_args(**over), None) == code, L.lib().pkd_last_error()
+
+
+def test_an_eviction_of_nothing_needs_no_gpu():
+    from paged_kv_decode_23_gb300 import _lib as L
+    assert L.lib().pkd_evict(None, None) == -1
+    assert L.lib().pkd_evict(_evict_args(batch=0), None) == 0
