@@ -607,7 +607,7 @@ int pkd_gather(const pkd_gather_args* args, void* stream);
  * means nothing to attention; ROPE_LLAMA, ALIBI and window_left, which count slots, do not go with it.
  *   kept   device [batch, num_kv_heads, budget] or NULL: the slot whose token now lies in each slot, -1
  *          behind the sequence's end.
- *   moves  device workspace of batch * num_kv_heads * (budget - S - R) pairs of int32, 8-byte aligned
+ *   moves  device workspace of 3 * batch * num_kv_heads * (budget - S - R) int32, 8-byte aligned
  *          (NULL if that is 0).
  * A sequence with a negative length, or more tokens than its pages hold, sets PKD_STATUS_BAD_TOKEN in
  * status (may be NULL), one whose page ids lie outside the pool PKD_STATUS_BAD_PAGE; it is left alone, its kept entries -1.

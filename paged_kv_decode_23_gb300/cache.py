@@ -300,7 +300,7 @@ def evict_paged_kv(paged_kv_cache, key_weights: torch.Tensor, kv_lens: torch.Ten
     weights = weight_views(key_weights, first.shape[0], hkv, ps, dev)
     heads, middle = batch * hkv, budget - sinks - recent
     kept = new_output((batch, hkv, budget), first, _INT32, stream) if return_kept else None
-    moves = new_output((heads * middle, 2), first, _INT32, stream)
+    moves = new_output((3 * heads * middle,), first, _INT32, stream)
     args = _EVICT.pack(*pool, *weights, lens, 0 if kept is None else kept.data_ptr(), moves.data_ptr(),
                        _status(status, dev), budget, sinks, recent, 0)
     _launch(L.lib().pkd_evict, dev, stream, args)

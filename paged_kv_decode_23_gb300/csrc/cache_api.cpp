@@ -252,6 +252,14 @@ extern "C" int pkd_evict(const pkd_evict_args* args, void* stream) {
         return bad("key_weights strides must be positive, within 2^60 elements");
     const int64_t st[3] = {a.weight_strides[0], a.weight_strides[2], a.weight_strides[1]};
     if (!rows_apart(a.pool, st, 1)) return bad("entries of key_weights overlap");
+    // (page and slot strides are held in 32 bits: of 16 bytes, of 4 for scales, of an element for weights)
+    const int64_t unit = dt == PKD_DTYPE_F16 || dt == PKD_DTYPE_BF16 ? 8 : 16;
+    for (int i = 0; i < 2; ++i) {
+      const int64_t entries = i == 0 ? a.pool.num_pages : a.pool.page_size;
+      if (entries > 1 && (a.pool.strides[i] / unit > UINT32_MAX || st[i] > UINT32_MAX ||
+                          (dt == PKD_DTYPE_E2M1 && a.pool.scale_strides[i] / 4 > UINT32_MAX)))
+        return bad("page or slot strides of more than 2^32 units");
+    }
     if (!a.moves && a.num_sink_tokens + a.num_recent < a.budget) return bad("moves is null");
     if (reinterpret_cast<uintptr_t>(a.moves) % 8) return bad("moves must be 8-byte aligned");
     return done(launch_evict(a, static_cast<cudaStream_t>(stream)), "evict kernel launch");
