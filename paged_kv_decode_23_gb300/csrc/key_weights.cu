@@ -15,39 +15,77 @@ namespace pkd {
 
 namespace {
 
-__global__ void __launch_bounds__(kKeyTileTokens) key_weights_kernel(const __grid_constant__ KeyWeightParams p) {
+constexpr int kThreads = kKeyTileTokens / 4;
+
+// Adds x to the four slots at w (16-byte aligned).
+__device__ __forceinline__ void add4(float* w, const float (&x)[4]) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(w), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3])
+               : "memory");
+}
+
+// A thread takes four consecutive keys, so that scores are read 16 bytes at a time (a row's scores are
+// laid out so that key t lies at a multiple of 16 bytes where t is one of 4, see KeyRow).
+__global__ void __launch_bounds__(kThreads) key_weights_kernel(const __grid_constant__ KeyWeightParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (a decode launch that gave up left scores out)
   if (*reinterpret_cast<const volatile uint32_t*>(p.status) & dev::kStatusTimeout) return;
   const int hkv = p.num_kv_heads, group = p.num_qo_heads / hkv;
-  const int64_t units = (int64_t)(p.tile_count ? *p.tile_count : p.num_tiles) * hkv;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int kvh = (int)(u % hkv);
-    const KeyTile tile = p.tiles[u / hkv];
-    const int t = tile.t0 + threadIdx.x;
+  const uint32_t units = (uint32_t)(p.tile_count ? *p.tile_count : p.num_tiles) * (uint32_t)hkv;
+  for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int kvh = (int)(u % (uint32_t)hkv);
+    const KeyTile tile = p.tiles[u / (uint32_t)hkv];
+    const int t = (tile.t0 & ~3) + 4 * threadIdx.x;
     if (t >= tile.t1) continue;
-    float sum = 0.f;
+    const uint32_t page = (uint32_t)__ldg(p.indices + tile.page_base + (t >> p.page_log));
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < p.q_len; ++j) {
       const int row = tile.req * p.q_len + j;
       const KeyRow kr = p.rows[row];
-      const bool sink = t < kr.sink;
-      if (t >= kr.n || (!sink && t < kr.win)) continue;
-      const float* s = p.scores + kr.base + (int64_t)kvh * group * kr.stride + t + (sink ? 0 : kr.shift);
+      bool in[4], any = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        in[i] = t + i < kr.sink || (t + i >= kr.win && t + i < kr.n);
+        any |= in[i];
+      }
+      if (!any) continue;
+      // (four keys of which some are sinks and some the window's: the two parts lie apart)
+      const bool both = t < kr.sink && t + 3 >= kr.win;
+      const float* s = p.scores + kr.base + (int64_t)kvh * group * kr.stride + t;
+      const float* at = s + (t < kr.sink ? 0 : kr.shift);
       const float2* st = p.stats + (int64_t)row * p.num_qo_heads + kvh * group;
 #pragma unroll 4
       for (int g = 0; g < group; ++g) {
         const float2 ml = st[g];
-        sum += dev::fast_exp2(s[(int64_t)g * kr.stride] - ml.x) * ml.y;
+        float4 x = *reinterpret_cast<const float4*>(at + (int64_t)g * kr.stride);
+        if (both) {
+          const float4 y = *reinterpret_cast<const float4*>(s + (int64_t)g * kr.stride + kr.shift);
+          x.y = t + 1 < kr.sink ? x.y : y.y;
+          x.z = t + 2 < kr.sink ? x.z : y.z;
+          x.w = t + 3 < kr.sink ? x.w : y.w;
+        }
+        sum[0] += in[0] ? dev::fast_exp2(x.x - ml.x) * ml.y : 0.f;
+        sum[1] += in[1] ? dev::fast_exp2(x.y - ml.x) * ml.y : 0.f;
+        sum[2] += in[2] ? dev::fast_exp2(x.z - ml.x) * ml.y : 0.f;
+        sum[3] += in[3] ? dev::fast_exp2(x.w - ml.x) * ml.y : 0.f;
       }
     }
-    const uint32_t page = (uint32_t)p.indices[tile.page_base + t / p.page_size];
-    if (page < p.num_pages)  // (the decode launch has reported other ids)
-      atomicAdd(p.weights + page * p.strides[0] + kvh * p.strides[1] + (t & (p.page_size - 1)) * p.strides[2], sum);
+    if (page >= p.num_pages) continue;  // (the decode launch has reported the id)
+    float* w = p.weights + page * p.strides[0] + kvh * p.strides[1] + (t & ((1 << p.page_log) - 1)) * p.strides[2];
+    if (p.quads && t >= tile.t0 && t + 4 <= tile.t1) {
+      add4(w, sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i >= tile.t0 && t + i < tile.t1) atomicAdd(w + i * p.strides[2], sum[i]);
+    }
   }
 }
 
 }  // namespace
 
-const void* key_weights_fn() { return reinterpret_cast<const void*>(&key_weights_kernel); }
+const void* key_weights_fn(int* threads) {
+  *threads = kThreads;
+  return reinterpret_cast<const void*>(&key_weights_kernel);
+}
 
 }  // namespace pkd

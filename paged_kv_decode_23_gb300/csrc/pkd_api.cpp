@@ -1099,25 +1099,28 @@ int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_b
     kp.num_pages = prm.num_pages;
     kp.num_qo_heads = h->num_qo_heads;
     kp.num_kv_heads = h->num_kv_heads;
-    kp.page_size = h->page_size;
+    kp.page_log = 31 - __builtin_clz((unsigned)h->page_size);
+    kp.quads = kw->strides[2] == 1 && kw->strides[0] % 4 == 0 && kw->strides[1] % 4 == 0 && aligned(kw->base, 16);
     kp.q_len = h->q_len;
     // units of (tile, kv head), at most as many CTAs as the GPU holds at once, which take them in turn;
     // CUDA-graph mode: that many for every plan
-    const int64_t units = (int64_t)h->n_key_tiles * h->num_kv_heads, most = (int64_t)h->num_sms * 8;
+    const int64_t units = (int64_t)h->n_key_tiles * h->num_kv_heads, most = (int64_t)h->num_sms * 16;
     const int64_t ctas = h->graph ? most : std::min(units, most);
     if (ctas > 0) {
       void* kargs[] = {&kp};
       cudaLaunchConfig_t cfg;
       std::memset(&cfg, 0, sizeof cfg);
       cfg.gridDim = dim3((unsigned)ctas);
-      cfg.blockDim = dim3(kKeyTileTokens);
+      int threads = 0;
+      const void* fn = key_weights_fn(&threads);
+      cfg.blockDim = dim3((unsigned)threads);
       cfg.stream = s;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       attr[0].val.programmaticStreamSerializationAllowed = h->pdl ? 1 : 0;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      e = cudaLaunchKernelExC(&cfg, key_weights_fn(), kargs);
+      e = cudaLaunchKernelExC(&cfg, fn, kargs);
       if (e != cudaSuccess) return cuda_fail(e, "key weights kernel launch");
     }
   }

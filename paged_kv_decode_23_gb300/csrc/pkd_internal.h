@@ -73,17 +73,19 @@ enum KernelKind { kCudaCore = 0, kTensorCore = 1 };
 
 // Plans with key weights.  Where the scores of one output row's attended keys lie: key t of qo head g
 // at base + g * stride + t for the sinks, t + shift for the window (both parts start at a page's first
-// slot, so that a warp's 16 keys fill whole 32-byte sectors).  The row attends t < sink and win <= t < n.
+// slot, so that a warp's 16 keys fill whole 32-byte sectors, and four keys from a multiple of 4 on 16
+// aligned bytes).  The row attends t < sink and win <= t < n.
 struct KeyRow {
   int64_t base;
   int32_t stride, sink, win, n, shift, pad;
 };
 static_assert(sizeof(KeyRow) == 32, "KeyRow is 8 int32");
-// Keys [t0, t1) of a request that at least one of its rows may attend, at most kKeyTileTokens of them.
+// Keys [t0, t1) of a request that its rows may attend, inside kKeyTileTokens from t0 rounded down to a
+// multiple of 4.
 struct KeyTile {
   int32_t req, t0, t1, page_base;
 };
-constexpr int kKeyTileTokens = 256;
+constexpr int kKeyTileTokens = 512;
 
 // Kernel parameters, passed by value as a __grid_constant__ so the tensor maps stay in
 // parameter space (where the TMA unit may read them).
@@ -141,9 +143,10 @@ struct KeyWeightParams {
   int64_t strides[3];  // of page, kv head, slot
   int num_tiles;
   uint32_t num_pages;
-  int num_qo_heads, num_kv_heads, page_size, q_len;
+  int num_qo_heads, num_kv_heads, page_log, q_len;
+  int quads;           // 1: four slots from a multiple of 4 on are 16 aligned bytes
 };
-const void* key_weights_fn();
+const void* key_weights_fn(int* threads);
 
 // The parameters of a kernel over a 4-bit cache: 5-D maps over the code pools (d, head and slot in
 // the layout's order, K/V, page) and the e4m3 scale of (page, slot, head, block) at base +

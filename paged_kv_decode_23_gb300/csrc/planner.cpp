@@ -813,9 +813,11 @@ void key_weight_lists(const PlanRequest& r, KeyRow* rows, KeyTile* tiles, int64_
     floats += stride * r.num_qo_heads;
   }
   auto add = [&](int req, int64_t from, int64_t to) {
-    for (int64_t t = from; t < to; t += kKeyTileTokens, ++n)
-      if (n < tiles_cap)
-        tiles[n] = {req, (int32_t)t, (int32_t)std::min<int64_t>(to, t + kKeyTileTokens), r.indptr[req]};
+    for (int64_t t = from; t < to; ++n) {
+      const int64_t e = std::min<int64_t>(to, t / 4 * 4 + kKeyTileTokens);
+      if (n < tiles_cap) tiles[n] = {req, (int32_t)t, (int32_t)e, r.indptr[req]};
+      t = e;
+    }
   };
   for (int i = 0; i < r.batch; ++i) {
     // the first row's window begins first and the last row's ends last; a row without a gap attends
