@@ -551,9 +551,11 @@ struct ScoreOut {
   float* base;
   int stride, sink, shift;
   bool live0, live1;
+  uint64_t policy;
   __device__ __forceinline__ ScoreOut(const DecodeParams& p, const BlockCoords& b, int col, int heads) {
     const KeyRow kr = p.key_rows[b.it.req];
     base = p.scores + kr.base + (int64_t)(b.g0 + col) * kr.stride;
+    policy = dev::policy_evict_last();
     stride = kr.stride;
     sink = kr.sink;
     shift = kr.shift;
@@ -563,8 +565,8 @@ struct ScoreOut {
   // the scores of key t
   __device__ __forceinline__ void put(int t, float s0, float s1) const {
     float* at = base + t + (t < sink ? 0 : shift);
-    if (live0) at[0] = s0;
-    if (live1) at[stride] = s1;
+    if (live0) dev::st_hint(at, s0, policy);
+    if (live1) dev::st_hint(at + stride, s1, policy);
   }
 };
 

@@ -23,12 +23,20 @@ __device__ __forceinline__ void add4(float* w, const float (&x)[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ float4 ld_first(const float* p, uint64_t policy) {
+  float4 v;
+  asm volatile("ld.global.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p), "l"(policy));
+  return v;
+}
+
 // A thread takes four consecutive keys, so that scores are read 16 bytes at a time (a row's scores are
 // laid out so that key t lies at a multiple of 16 bytes where t is one of 4, see KeyRow).
 __global__ void __launch_bounds__(kThreads) key_weights_kernel(const __grid_constant__ KeyWeightParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (a decode launch that gave up left scores out)
   if (*reinterpret_cast<const volatile uint32_t*>(p.status) & dev::kStatusTimeout) return;
+  const uint64_t pol = dev::policy_evict_first();
   const int hkv = p.num_kv_heads, group = p.num_qo_heads / hkv;
   const uint32_t units = (uint32_t)(p.tile_count ? *p.tile_count : p.num_tiles) * (uint32_t)hkv;
   for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -56,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) key_weights_kernel(const __grid_cons
 #pragma unroll 4
       for (int g = 0; g < group; ++g) {
         const float2 ml = st[g];
-        float4 x = *reinterpret_cast<const float4*>(at + (int64_t)g * kr.stride);
+        float4 x = ld_first(at + (int64_t)g * kr.stride, pol);
         if (both) {
           const float4 y = *reinterpret_cast<const float4*>(s + (int64_t)g * kr.stride + kr.shift);
           x.y = t + 1 < kr.sink ? x.y : y.y;
