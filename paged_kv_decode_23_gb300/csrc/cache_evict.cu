@@ -31,6 +31,7 @@ namespace cg = cooperative_groups;
 constexpr int kBins = 2048;  // of an 11-bit digit
 constexpr int kMaxRanks = 8;
 constexpr int kFew = 256;
+constexpr int kMostTokens = 1 << 30;  // (positions and steps past them stay in 32 bits)
 
 // Order of weights as unsigned numbers: NaN above all, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
   __shared__ int found[3];
   // to the cluster: counts of equal and of larger keys below B - R and not, tokens below; bad pages; keys in `few`
   __shared__ int said[7];
+  __shared__ int theirs[5][kMaxRanks];  // what the CTAs of the cluster said
   asm volatile("griddepcontrol.wait;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
   int32_t* kept = p.kept ? p.kept + (int64_t)unit * B : nullptr;
   const int64_t first = __ldg(p.indptr + seq), end = __ldg(p.indptr + seq + 1);
   const int64_t pages = ((int64_t)n + (1 << p.page_log) - 1) >> p.page_log;
-  const bool no_token = n < 0 || n > INT32_MAX - 4096 ||
+  const bool no_token = n < 0 || n > kMostTokens ||
                         (n > 0 && (first < 0 || first + pages > end || first + pages > p.num_indices));
   if (no_token || n <= B) {  // (the whole cluster)
     if (no_token && p.status && rank == 0 && tid == 0) atomicOr(p.status, PKD_STATUS_BAD_TOKEN);
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
   if constexpr (CLUSTER) {
     if (tid == 0) said[5] = bad;
     sync();
-    for (int r = 0; r < ranks; ++r) bad |= *of_rank(&said[5], r) != 0;
+    bad = __syncthreads_or(tid < ranks ? *of_rank(&said[5], tid) : 0);
   }
   if (bad) {
     if (p.status && rank == 0 && tid == 0) atomicOr(p.status, PKD_STATUS_BAD_PAGE);
@@ -304,13 +306,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
         }
         sync();
         if constexpr (CLUSTER) {  // those of all CTAs, into the histogram that is not in use
-          uint32_t* mine_all = reinterpret_cast<uint32_t*>(hist[~pass & 1]);
-          int base = 0;
-          for (int r = 0; r < ranks; ++r) {
-            const int c = *of_rank(&said[6], r);
-            const uint32_t* src = of_rank(few, r);
-            for (int i = tid; i < c; i += THREADS) mine_all[base + i] = src[i];
-            base += c;
+          uint32_t* list = reinterpret_cast<uint32_t*>(hist[~pass & 1]);
+          if (tid < ranks) theirs[0][tid] = *of_rank(&said[6], tid);
+          __syncthreads();
+          for (int i = tid; i < left; i += THREADS) {
+            int r = 0, j = i;
+            while (j >= theirs[0][r]) j -= theirs[0][r++];
+            list[i] = of_rank(few, r)[j];
           }
           __syncthreads();
         }
@@ -367,10 +369,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
       if (lane == 0 && x) atomicAdd(&said[i], x);
     }
     sync();
+    for (int i = tid; i < 5 * ranks; i += THREADS) theirs[i % 5][i / 5] = of_rank(said, i / 5)[i % 5];
+    __syncthreads();
     int eq_before = 0;
     n_moves = 0;
     for (int r = 0; r < ranks; ++r) {
-      const int* of = of_rank(said, r);
+      const int of[5] = {theirs[0][r], theirs[1][r], theirs[2][r], theirs[3][r], theirs[4][r]};
       const int lows = of[0], highs = of[1];
       const int take_low = max(0, min(lows, equal - eq_before)), take_high = max(0, min(highs, equal - eq_before - lows));
       if (r < rank) {
