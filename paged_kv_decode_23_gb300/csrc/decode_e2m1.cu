@@ -4,8 +4,8 @@
 namespace pkd {
 
 void register_decode_e2m1(std::vector<DecodeKernel>& out) {
-  register_e2m1_geometries<__half, false>(out, kF16);
-  register_e2m1_geometries<__nv_bfloat16, false>(out, kBF16);
+  register_e2m1_geometries<__half, kUnbounded>(out, kF16);
+  register_e2m1_geometries<__nv_bfloat16, kUnbounded>(out, kBF16);
 }
 
 }  // namespace pkd

@@ -188,7 +188,7 @@ struct PageWindow {
 };
 
 // ------------------------------------------------------------------------------ producer
-template <class G>
+template <class G, bool SINKS>
 __device__ __forceinline__ void produce_e2m1(const DecodeE2m1Params& p, const BlockCoords& b,
                                              uint32_t smem, uint32_t full0, uint32_t empty0,
                                              volatile int* abort_flag, int lane) {
@@ -204,32 +204,32 @@ __device__ __forceinline__ void produce_e2m1(const DecodeE2m1Params& p, const Bl
   // pages of up to 32 slots put a lane's tokens into one slot, tile after tile
   const int64_t lane_slot = (int64_t)(lane & (ps - 1)) * p.sf_stride[1];
   if (lane == 0) prefetch_tmap(&p.tmap_k);
-  const bool sinks = b.ns > 0;
-  int run0 = sinks ? b.it.sink_begin : b.it.chunk_tok0;  // first token of the window's run of pages
-  PageWindow win(p, b, run0, sinks ? b.it.sink_end : b.it.tok_end, (tile_span<TS>(b, 0).t0 - run0) / ps, lane);
+  int run0 = SINKS && b.ns > 0 ? b.it.sink_begin : b.it.chunk_tok0;  // first token of the run of pages
+  TileRun<SINKS, TS> run(b);
+  PageWindow win(p, b, run0, run.hi(b), (run.t0(b, 0) - run0) / ps, lane);
   int issued = 0, s = 0;
   uint32_t phase = 1;
   bool ok = true, bad_page = false;
   for (int i = 0; i < b.ntiles; ++i) {
-    const TileSpan ts = tile_span<TS>(b, i);
-    const int t0 = ts.t0;
-    if (sinks && i == b.ns) {  // from the sinks to the window
+    const bool moved = run.move(p, b, i);
+    const int t0 = run.t0(b, i);
+    if (moved) {  // from the sinks to the window
       run0 = b.it.chunk_tok0;
-      win = PageWindow(p, b, run0, b.it.tok_end, (t0 - run0) / ps, lane);
+      win = PageWindow(p, b, run0, run.hi(b), (t0 - run0) / ps, lane);
     }
     const int tile0 = t0 - run0;
     const int bt0 = t0 + lane * br;
-    const bool need = lane < boxes && bt0 < ts.hi && bt0 + br > ts.lo;
+    const bool need = lane < boxes && bt0 < run.hi(b) && bt0 + br > run.lo(b);
     win.move(tile0 >> ps_log, lane);
     const int pid = win.id((tile0 + lane * br) >> ps_log);  // (lanes past the boxes: any page)
-    const bool whole = t0 >= ts.lo && t0 + TS <= ts.hi;
+    const bool whole = t0 >= run.lo(b) && t0 + TS <= run.hi(b);
     const uint8_t* src[TS / 32];
     bool valid[TS / 32];
 #pragma unroll
     for (int k = 0; k < TS / 32; ++k) {
       const int j = lane + 32 * k;
       const uint32_t id = (uint32_t)win.id((tile0 + j) >> ps_log);
-      valid[k] = id < p.num_pages && (whole || (t0 + j >= ts.lo && t0 + j < ts.hi));
+      valid[k] = id < p.num_pages && (whole || (t0 + j >= run.lo(b) && t0 + j < run.hi(b)));
       src[k] = ksf + (valid[k] ? id : 0u) * p.sf_stride[0] +
                (ps <= 32 ? lane_slot : (int64_t)((tile0 + j) & (ps - 1)) * p.sf_stride[1]);
     }
@@ -362,7 +362,7 @@ __device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t s, bool high) {
   return *reinterpret_cast<const uint32_t*>(&z);
 }
 
-template <typename TQ, class G, bool SCORES>
+template <typename TQ, class G, bool SINKS, bool SCORES>
 __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const BlockCoords& b,
                                              uint32_t smem, uint32_t full0, uint32_t empty0,
                                              volatile int* abort_flag, int warp, int lane,
@@ -410,16 +410,17 @@ __device__ __forceinline__ void consume_e2m1(const DecodeE2m1Params& p, const Bl
 
   int s = 0;
   uint32_t phase = 0;
+  TileRun<SINKS, TS> run(b);
   for (int i = 0; i < b.ntiles; ++i) {
-    const TileSpan ts = tile_span<TS>(b, i);
-    const int t_w = ts.t0 + warp * 16;  // first token of slice 0
+    run.move(p, b, i);
+    const int t_w = run.t0(b, i) + warp * 16;  // first token of slice 0
     if (!__all_sync(~0u, mbar_wait(full0 + 8 * s, phase, abort_flag, p.wait_ns))) {
       *abort_flag = 1;  // warp-uniform: the warp leaves the loop together
       atomicOr(p.status, kStatusTimeout);
       break;
     }
     // attended tokens [lo, hi), counted from t_w
-    const int lo = ts.lo - t_w, hi = ts.hi - t_w;
+    const int lo = run.lo(b) - t_w, hi = run.hi(b) - t_w;
     const uint32_t st = stage_after_wait(smem + s * G::STAGE_BYTES);
     bool work = hi > 0 && lo < 16;
 #pragma unroll
@@ -644,7 +645,7 @@ __device__ __forceinline__ void stash_e2m1(const EpiView<G::D>& e, int warp, int
 }
 
 // ------------------------------------------------------------------------------ kernel
-template <typename TQ, class G, int CTAS, bool SCORES>
+template <typename TQ, class G, int CTAS, int BOUNDED>
 __global__ void __launch_bounds__(G::THREADS, CTAS)
     decode_e2m1_kernel(const __grid_constant__ DecodeE2m1Params p) {
   using namespace dev;
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(G::THREADS, CTAS)
   // upload, everything else is touched only after the previous kernel has finished.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (p.task_count != nullptr && (int)blockIdx.x >= *p.task_count) return;
-  const BlockCoords b = task_coords<G::TS, G::HEADS>(p);
+  const BlockCoords b = task_coords<G::TS, G::HEADS, BOUNDED != kUnbounded>(p);
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int s = 0; s < NSTAGES; ++s) {
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(G::THREADS, CTAS)
   if (abort_flag_s) return;  // an earlier launch timed out: touch nothing
 
   if (warp == G::NW) {
-    produce_e2m1<G>(p, b, smem, full0, empty0, abort_flag, lane);
+    produce_e2m1<G, BOUNDED != kUnbounded>(p, b, smem, full0, empty0, abort_flag, lane);
     return;
   }
   const EpiView<D> epi(smem_p, G::NW);
@@ -690,16 +691,16 @@ __global__ void __launch_bounds__(G::THREADS, CTAS)
   float acc[G::ACC][4];
 #pragma unroll
   for (int mb = 0; mb < G::ACC; ++mb) acc[mb][0] = acc[mb][1] = acc[mb][2] = acc[mb][3] = 0.f;
-  consume_e2m1<TQ, G, SCORES>(p, b, smem, full0, empty0, abort_flag, warp, lane, m2, lsum, acc);
+  consume_e2m1<TQ, G, BOUNDED != kUnbounded, BOUNDED == kScores>(p, b, smem, full0, empty0, abort_flag, warp, lane, m2, lsum, acc);
   // every consumer is done with the stages; one shared decision whether any wait gave up
   if (named_bar_or(1, G::NCONS, *abort_flag != 0)) return;
   stash_e2m1<G>(epi, warp, lane, m2, lsum, acc);
   named_bar_sync(1, G::NCONS);
-  store_task<TQ, D, G::NW>(p, b, epi, threadIdx.x);
-  if (b.it.out_slot >= 0) merge_unit<TQ, D, G::NCONS>(p, b, threadIdx.x, &merge_last_s);
+  store_task<TQ, D, G::NW, BOUNDED == kScores>(p, b, epi, threadIdx.x);
+  if (b.it.out_slot >= 0) merge_unit<TQ, D, G::NCONS, BOUNDED == kScores>(p, b, threadIdx.x, &merge_last_s);
 }
 
-template <typename TQ, class G, int CTAS, bool SCORES>
+template <typename TQ, class G, int CTAS, int BOUNDED>
 DecodeKernel make_decode_e2m1(int q_dtype) {
   DecodeKernel k;
   k.kind = kTensorCore;
@@ -707,8 +708,9 @@ DecodeKernel make_decode_e2m1(int q_dtype) {
   k.kv_dtype = kE2M1;
   k.head_dim = G::D;
   k.heads_per_cta = G::HEADS;
-  k.fn = reinterpret_cast<const void*>(&decode_e2m1_kernel<TQ, G, CTAS, SCORES>);
-  k.scores = SCORES ? 1 : 0;
+  k.fn = reinterpret_cast<const void*>(&decode_e2m1_kernel<TQ, G, CTAS, BOUNDED>);
+  k.sinks = BOUNDED != kUnbounded ? 1 : 0;
+  k.scores = BOUNDED == kScores ? 1 : 0;
   k.threads = G::THREADS;
   k.smem_bytes = G::SMEM_BYTES;
   k.tile_tokens = G::TS;
@@ -722,15 +724,15 @@ DecodeKernel make_decode_e2m1(int q_dtype) {
 // The geometries that are built, for tasks of up to 4 or up to 8 qo heads: 4 where a kv head has no
 // more.  Groups of 4 heads through the 8-head instance took 52.1 us for 45.4 (64 contexts of 512 to
 // 4,096, head_dim 128), and 123 for 113 (4 of 131,072).  At head_dim 64 these cases take 30.3 and 75.9 us.
-template <typename TQ, bool SCORES>
+template <typename TQ, int BOUNDED>
 void register_e2m1_geometries(std::vector<DecodeKernel>& out, int q) {
   //                                  D  heads warps slices stages  CTAs per SM
-  out.push_back(make_decode_e2m1<TQ, E2m1Geom<64, 4, 4, 2, 5>, 4, SCORES>(q));
-  out.push_back(make_decode_e2m1<TQ, E2m1Geom<128, 4, 4, 2, 3>, 4, SCORES>(q));
-  out.push_back(make_decode_e2m1<TQ, E2m1Geom<256, 4, 4, 2, 3>, 2, SCORES>(q));
-  out.push_back(make_decode_e2m1<TQ, E2m1Geom<64, 8, 4, 2, 4>, 4, SCORES>(q));
-  out.push_back(make_decode_e2m1<TQ, E2m1Geom<128, 8, 4, 2, 4>, 3, SCORES>(q));
-  out.push_back(make_decode_e2m1<TQ, E2m1Geom<256, 8, 4, 2, 3>, 2, SCORES>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<64, 4, 4, 2, 5>, 4, BOUNDED>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<128, 4, 4, 2, 3>, 4, BOUNDED>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<256, 4, 4, 2, 3>, 2, BOUNDED>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<64, 8, 4, 2, 4>, 4, BOUNDED>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<128, 8, 4, 2, 4>, 3, BOUNDED>(q));
+  out.push_back(make_decode_e2m1<TQ, E2m1Geom<256, 8, 4, 2, 3>, 2, BOUNDED>(q));
 }
 
 }  // namespace pkd

@@ -78,6 +78,13 @@ struct RopeGeom {
   static_assert(ROW >= 128, "the row swizzle flips bit 6 of an offset inside the row");
 };
 
+// What a tensor-core instance can do beside plain decode: nothing; sinks; sinks and leaving scores.  The
+// CUDA-core and the rotating kernels have one instance, which takes sinks.
+enum Bounded { kUnbounded = 0, kSinks = 1, kScores = 2 };
+__host__ __device__ constexpr bool takes_sinks(int kind, bool rope, int bounded) {
+  return kind != kTensorCore || rope || bounded != kUnbounded;
+}
+
 struct BlockCoords {
   DecodeTask it;
   int kvh;    // kv head
@@ -85,22 +92,42 @@ struct BlockCoords {
   int gcnt;   // qo heads of this task
   int gs;     // which slice of the kv head's qo-head group
   int ns;     // tiles of the task's sinks, before those of its window
-  int main0;  // token of tile 0, were the window's tiles counted back to it
+  int j0;     // the window's first tile (relative to the chunk start)
   int ntiles;
 };
 
-// Tile i of a task: its first token and the attended tokens [lo, hi) around it.
-struct TileSpan {
-  int t0, lo, hi;
+// Where a task's tiles lie: tile i begins at token t0(b, i), and [lo(b), hi(b)) are the attended tokens
+// around it.  SINKS: the tiles of the task's sinks come first; move(i), called for every tile in order,
+// goes on to the window's (whose tokens are read again: the registers hold one run's).
+// Kernels for plans without sinks are instances of their own: a test per tile cost those at the edge of
+// their registers 0.5 to 2.3 % (4 bits), the others 0.1 to 0.3 %.
+template <bool SINKS, int TS>
+struct TileRun {
+  int base, lo_, hi_;
+  __device__ __forceinline__ explicit TileRun(const BlockCoords& b)
+      : base(b.ns > 0 ? b.it.sink_begin : b.it.chunk_tok0 + b.j0 * TS),
+        lo_(b.ns > 0 ? b.it.sink_begin : b.it.tok_begin), hi_(b.ns > 0 ? b.it.sink_end : b.it.tok_end) {}
+  __device__ __forceinline__ bool move(const DecodeParams& p, const BlockCoords& b, int i) {
+    if (i != b.ns || i == 0) return false;
+    const DecodeTask* t = p.tasks + blockIdx.x;
+    base = t->chunk_tok0 + (b.j0 - b.ns) * TS;
+    lo_ = t->tok_begin;
+    hi_ = t->tok_end;
+    return true;
+  }
+  __device__ __forceinline__ int t0(const BlockCoords&, int i) const { return base + i * TS; }
+  __device__ __forceinline__ int lo(const BlockCoords&) const { return lo_; }
+  __device__ __forceinline__ int hi(const BlockCoords&) const { return hi_; }
 };
 template <int TS>
-__device__ __forceinline__ TileSpan tile_span(const BlockCoords& b, int i) {
-  const bool sink = i < b.ns;
-  return {(sink ? b.it.sink_begin : b.main0) + i * TS, sink ? b.it.sink_begin : b.it.tok_begin,
-          sink ? b.it.sink_end : b.it.tok_end};
-}
-
-template <int TS, int HEADS>
+struct TileRun<false, TS> {
+  __device__ __forceinline__ explicit TileRun(const BlockCoords&) {}
+  __device__ __forceinline__ bool move(const DecodeParams&, const BlockCoords&, int) { return false; }
+  __device__ __forceinline__ int t0(const BlockCoords& b, int i) const { return b.it.chunk_tok0 + (b.j0 + i) * TS; }
+  __device__ __forceinline__ int lo(const BlockCoords& b) const { return b.it.tok_begin; }
+  __device__ __forceinline__ int hi(const BlockCoords& b) const { return b.it.tok_end; }
+};
+template <int TS, int HEADS, bool SINKS>
 __device__ __forceinline__ BlockCoords task_coords(const DecodeParams& p) {
   BlockCoords b;
   b.it = p.tasks[blockIdx.x];
@@ -108,19 +135,19 @@ __device__ __forceinline__ BlockCoords task_coords(const DecodeParams& p) {
   b.gs = b.it.gs;
   b.g0 = b.kvh * p.group + b.gs * HEADS;
   b.gcnt = min(HEADS, p.group - b.gs * HEADS);
-  b.ns = (b.it.sink_end - b.it.sink_begin + TS - 1) / TS;
-  b.main0 = 0;
-  b.ntiles = 0;
+  b.ns = SINKS ? (b.it.sink_end - b.it.sink_begin + TS - 1) / TS : 0;
   if (b.it.tok_end > b.it.tok_begin) {
-    const int j0 = (b.it.tok_begin - b.it.chunk_tok0) / TS;  // the window's first tile in the chunk
-    b.main0 = b.it.chunk_tok0 + (j0 - b.ns) * TS;
-    b.ntiles = (b.it.tok_end - b.it.chunk_tok0 + TS - 1) / TS - j0 + b.ns;
+    b.j0 = (b.it.tok_begin - b.it.chunk_tok0) / TS;
+    b.ntiles = (b.it.tok_end - b.it.chunk_tok0 + TS - 1) / TS - b.j0 + b.ns;
+  } else {
+    b.j0 = 0;
+    b.ntiles = 0;
   }
   return b;
 }
 
 // ------------------------------------------------------------------------------ producer
-template <class G, int TS, int NSTAGES>
+template <class G, int TS, int NSTAGES, bool SINKS>
 __device__ __forceinline__ void produce(const DecodeParams& p, const BlockCoords& b, uint32_t smem,
                                         uint32_t full0, uint32_t empty0, volatile int* abort_flag,
                                         int lane) {
@@ -136,6 +163,7 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const BlockCoords
   }
   int issued = 0;
   bool ok = true, bad_page = false;
+  TileRun<SINKS, TS> run(b);
   for (int i = 0; i < b.ntiles; ++i) {
     const int s = i % NSTAGES;
     // one decision per warp: a lane that gave up takes the whole warp out of the loop
@@ -144,9 +172,9 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const BlockCoords
       ok = false;
       break;
     }
-    const TileSpan ts = tile_span<TS>(b, i);
-    const int bt0 = ts.t0 + lane * br;
-    const bool need = lane < boxes && bt0 < ts.hi && bt0 + br > ts.lo;
+    run.move(p, b, i);
+    const int bt0 = run.t0(b, i) + lane * br;
+    const bool need = lane < boxes && bt0 < run.hi(b) && bt0 + br > run.lo(b);
     int pid = 0;
     if (need) pid = __ldg(p.indices + b.it.page_base + bt0 / ps);
     bad_page |= need && (uint32_t)pid >= p.num_pages;
@@ -201,8 +229,9 @@ struct EpiView {
   }
 };
 
-// Combines every warp's state and writes the task's final o / lse, or its fp32 partial.
-template <typename TQ, int D, int NW>
+// Combines every warp's state and writes the task's final o / lse, or its fp32 partial.  STATS: a final
+// row's softmax statistics as well.
+template <typename TQ, int D, int NW, bool STATS>
 __device__ __forceinline__ void store_task(const DecodeParams& p, const BlockCoords& b,
                                            const EpiView<D>& e, int tid) {
   using namespace dev;
@@ -241,7 +270,7 @@ __device__ __forceinline__ void store_task(const DecodeParams& p, const BlockCoo
       TQ* dst = reinterpret_cast<TQ*>(p.o) + ((size_t)b.it.req * p.num_qo_heads + qo) * D + d0;
       *reinterpret_cast<uint4*>(dst) = v;
       if (d0 == 0 && p.lse) p.lse[(size_t)b.it.req * p.num_qo_heads + qo] = lse2 * kLn2;
-      if (d0 == 0 && p.stats)
+      if (STATS && d0 == 0)
         p.stats[(size_t)b.it.req * p.num_qo_heads + qo] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
     } else {
       float* dst = p.part_o + ((size_t)b.it.out_slot * kSlotHeads + g) * D + d0;
@@ -257,7 +286,7 @@ __device__ __forceinline__ void store_task(const DecodeParams& p, const BlockCoo
 // o = sum w_c o_c / sum w_c, lse = M + log2 sum w_c.  Writers publish their partial with a
 // fence before counting; the last one fences again, reads the partials from L2 and resets the
 // counter for the next run of the plan.  No CTA waits for another.
-template <typename TQ, int D, int NCONS>
+template <typename TQ, int D, int NCONS, bool STATS>
 __device__ __forceinline__ void merge_unit(const DecodeParams& p, const BlockCoords& b, int tid,
                                            volatile int* last_flag) {
   using namespace dev;
@@ -337,7 +366,7 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, const BlockCoo
     *reinterpret_cast<uint4*>(dst) = v;
     if (d0 == 0 && p.lse)
       p.lse[(size_t)me.req * hq + qo] = L > 0.f ? (M + log2f(L)) * kLn2 : kNegInf;
-    if (d0 == 0 && p.stats) p.stats[(size_t)me.req * hq + qo] = make_float2(M, inv);
+    if (STATS && d0 == 0) p.stats[(size_t)me.req * hq + qo] = make_float2(M, inv);
   }
 }
 
@@ -574,7 +603,7 @@ struct ScoreOut {
 // (the two halves of a rotation pair are k steps kk and kk + D/32 of the same lane), in fp16
 // arithmetic, so QK runs in fp16; P*V keeps V's type.
 // SCORES: every attended key's score is left in p.scores as well.
-template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, bool ROPE = false, bool SCORES = false>
+template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, bool ROPE, bool SINKS, bool SCORES>
 __device__ __forceinline__ void consume_tc(const DecodeParams& p, const BlockCoords& b, uint32_t smem,
                                            uint32_t full0, uint32_t empty0, volatile int* abort_flag,
                                            int warp, int lane, float (&m2)[2], float (&lsum)[2],
@@ -623,10 +652,11 @@ __device__ __forceinline__ void consume_tc(const DecodeParams& p, const BlockCoo
     }
   }
 
+  TileRun<SINKS, TS> run(b);
   for (int i = 0; i < b.ntiles; ++i) {
     const int s = i % NSTAGES;
-    const TileSpan ts = tile_span<TS>(b, i);
-    const int t_w = ts.t0 + warp * 16;  // first token of my slice
+    run.move(p, b, i);
+    const int t_w = run.t0(b, i) + warp * 16;  // first token of my slice
     // ROPE: the slice's q rotation, while the stage may still be loading
     if constexpr (ROPE)
       rope_build_e<D, KV_FP8>(rope_e + (i & 1) * RG::ROW, rope_rates, (float)(b.it.q_pos - t_w), lane);
@@ -635,8 +665,8 @@ __device__ __forceinline__ void consume_tc(const DecodeParams& p, const BlockCoo
       atomicOr(p.status, kStatusTimeout);
       break;
     }
-    const int vlo = max(0, ts.lo - t_w);
-    const int vhi = min(16, ts.hi - t_w);
+    const int vlo = max(0, run.lo(b) - t_w);
+    const int vhi = min(16, run.hi(b) - t_w);
     const uint32_t ktile = stage_after_wait(smem + s * G::STAGE_BYTES);
     uint32_t vtile = ktile + G::TILE_BYTES;
     const int r0 = warp * 16;  // first tile row of my slice
@@ -1158,10 +1188,11 @@ __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoo
     lsum_h[j] = 0.f;
   }
 
+  TileRun<true, TS> run(b);
   for (int i = 0; i < b.ntiles; ++i) {
     const int s = i % NSTAGES;
-    const TileSpan ts = tile_span<TS>(b, i);
-    const int t_w = ts.t0 + warp * 16;  // first token of my slice
+    run.move(p, b, i);
+    const int t_w = run.t0(b, i) + warp * 16;  // first token of my slice
     if constexpr (ROPE)
       cc_rotate_q<TQ, KV_FP8, D, GP, G::NW>(p, b, qr, (float)(b.it.q_pos - t_w - 8), lane);
     if (!__all_sync(~0u, mbar_wait(full0 + 8 * s, (i / NSTAGES) & 1, abort_flag, p.wait_ns))) {
@@ -1169,8 +1200,8 @@ __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoo
       atomicOr(p.status, kStatusTimeout);
       break;
     }
-    const int vlo = max(0, ts.lo - t_w);
-    const int vhi = min(16, ts.hi - t_w);
+    const int vlo = max(0, run.lo(b) - t_w);
+    const int vhi = min(16, run.hi(b) - t_w);
     const uint32_t ktile = stage_after_wait(smem + s * G::STAGE_BYTES);
     const uint32_t vtile = ktile + G::TILE_BYTES;
     if (vlo < vhi) {  // warp-uniform
@@ -1370,9 +1401,9 @@ __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoo
 
 // ------------------------------------------------------------------------------ kernel
 // KIND: kTensorCore (HEADS = 8 qo heads per task) or kCudaCore (HEADS = GP).  ROPE: ROPE_LLAMA
-// applied to q and K.  SCORES: see consume_tc.  CTA blockIdx.x runs task blockIdx.x.
+// applied to q and K.  BOUNDED: what the instance is for beside plain plans.  CTA blockIdx.x runs task blockIdx.x.
 template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int KIND, int GP, bool ROPE = false,
-          bool SCORES = false>
+          int BOUNDED = kUnbounded>
 __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREADS,
                                   KIND == kTensorCore ? 2 : 1)
     __maxnreg__((KIND == kTensorCore ? 255
@@ -1381,6 +1412,7 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
   using namespace dev;
   using G = DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>;
   constexpr int HEADS = KIND == kTensorCore ? 8 : GP;
+  constexpr bool SINKS = takes_sinks(KIND, ROPE, BOUNDED);
   __shared__ __align__(8) uint64_t bars[2 * NSTAGES];
   __shared__ int abort_flag_s;
   __shared__ int merge_last_s;
@@ -1402,7 +1434,7 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
   // kernel may still run.  CUDA-graph mode: the grid is cut for a fixed work-list capacity;
   // CTAs past this plan's tasks have nothing to do (the whole CTA leaves at once).
   if (p.task_count != nullptr && (int)blockIdx.x >= *p.task_count) return;
-  const BlockCoords b = task_coords<TS, HEADS>(p);
+  const BlockCoords b = task_coords<TS, HEADS, SINKS>(p);
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int s = 0; s < NSTAGES; ++s) {
@@ -1420,7 +1452,7 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
   if (abort_flag_s) return;  // an earlier launch timed out: touch nothing
 
   if (warp == G::NW) {
-    produce<G, TS, NSTAGES>(p, b, smem, full0, empty0, abort_flag, lane);
+    produce<G, TS, NSTAGES, SINKS>(p, b, smem, full0, empty0, abort_flag, lane);
     return;
   }
   const EpiView<D> epi(smem_p, G::NW);
@@ -1434,7 +1466,7 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
     float acc[D / 16][4];
 #pragma unroll
     for (int mb = 0; mb < D / 16; ++mb) acc[mb][0] = acc[mb][1] = acc[mb][2] = acc[mb][3] = 0.f;
-    consume_tc<TQ, KV_FP8, D, TS, NSTAGES, ROPE, SCORES>(p, b, smem, full0, empty0, abort_flag, warp,
+    consume_tc<TQ, KV_FP8, D, TS, NSTAGES, ROPE, SINKS, BOUNDED == kScores>(p, b, smem, full0, empty0, abort_flag, warp,
                                                  lane, m2, lsum, acc);
     // every consumer is done with the stages; one shared decision whether any wait gave up
     if (named_bar_or(1, G::NCONS, *abort_flag != 0)) return;
@@ -1447,13 +1479,13 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
       return;
   }
   named_bar_sync(1, G::NCONS);
-  store_task<TQ, D, G::NW>(p, b, epi, threadIdx.x);
-  if (b.it.out_slot >= 0) merge_unit<TQ, D, G::NCONS>(p, b, threadIdx.x, &merge_last_s);
+  store_task<TQ, D, G::NW, BOUNDED == kScores>(p, b, epi, threadIdx.x);
+  if (b.it.out_slot >= 0) merge_unit<TQ, D, G::NCONS, BOUNDED == kScores>(p, b, threadIdx.x, &merge_last_s);
 }
 
 // ------------------------------------------------------------------------------ registry
 template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int KIND, int GP, bool ROPE = false,
-          bool SCORES = false>
+          int BOUNDED = kUnbounded>
 DecodeKernel make_decode_kernel(int q_dtype, int kv_dtype) {
   using G = DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>;
   DecodeKernel k;
@@ -1463,9 +1495,10 @@ DecodeKernel make_decode_kernel(int q_dtype, int kv_dtype) {
   k.head_dim = D;
   k.heads_per_cta = KIND == kTensorCore ? 8 : GP;
   k.fn = reinterpret_cast<const void*>(
-      &decode_paged_kernel<TQ, KV_FP8, D, TS, NSTAGES, KIND, GP, ROPE, SCORES>);
+      &decode_paged_kernel<TQ, KV_FP8, D, TS, NSTAGES, KIND, GP, ROPE, BOUNDED>);
   k.rope = ROPE ? 1 : 0;
-  k.scores = SCORES ? 1 : 0;
+  k.sinks = takes_sinks(KIND, ROPE, BOUNDED) ? 1 : 0;
+  k.scores = BOUNDED == kScores ? 1 : 0;
   k.nstages = NSTAGES;
   k.threads = G::THREADS;
   k.smem_bytes = G::SMEM_BYTES + (KIND == kTensorCore

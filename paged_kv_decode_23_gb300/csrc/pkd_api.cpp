@@ -50,8 +50,10 @@ void init_registry() {
     register_decode_rope_cc(g_decode);
     register_decode_rope_cc_e4m3(g_decode);
     register_decode_e2m1(g_decode);
-    register_decode_weights(g_decode);
-    register_decode_e2m1_weights(g_decode);
+    register_decode_sinks(g_decode);
+    register_decode_scores(g_decode);
+    register_decode_e2m1_sinks(g_decode);
+    register_decode_e2m1_scores(g_decode);
     register_mla(g_mla);
     register_mla_tc(g_mla);
   });
@@ -64,12 +66,13 @@ const MlaKernel* find_mla(int dtype, int variant) {
   return nullptr;
 }
 
+// (kernels that take sinks come after those that do not, where there are both)
 const DecodeKernel* find_decode(int kind, int q_dtype, int kv_dtype, int head_dim, int heads,
-                                int rope, int scores) {
+                                int rope, bool sinks, bool scores) {
   init_registry();
   for (const auto& k : g_decode)
     if (k.kind == kind && k.q_dtype == q_dtype && k.kv_dtype == kv_dtype &&
-        k.head_dim == head_dim && k.heads_per_cta == heads && k.rope == rope && k.scores == scores)
+        k.head_dim == head_dim && k.heads_per_cta == heads && k.rope == rope && k.sinks >= (int)sinks && k.scores == (int)scores)
       return &k;
   return nullptr;
 }
@@ -155,7 +158,8 @@ struct pkd_handle {
   size_t tmap_next = 0;
   int gslices = 1;
   int64_t n_tasks = 0;
-  bool key_weights = false;  // the plan's runs sum their keys' weights
+  bool sinks = false;        // the plan's kernel takes sinks
+  bool key_weights = false;  // its runs sum their keys' weights
   KeyWsLayout klayout{};
   int n_key_tiles = 0;
 
@@ -675,6 +679,9 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
       return fail(PKD_ERR_INVALID_ARG, "CUDA-graph mode: the handle holds MLA plans");
     if (h->g_batch >= 0 && key_weights != h->key_weights)
       return fail(PKD_ERR_INVALID_ARG, "CUDA-graph mode: key_weights is fixed by the first plan");
+    if (h->g_batch >= 0 && args->num_sink_tokens > 0 && !h->sinks)
+      return fail(PKD_ERR_INVALID_ARG,
+                  "CUDA-graph mode: the first plan had no sinks, so captured runs take none");
   }
 
   PlanRequest r;
@@ -686,9 +693,10 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   const char* err = "";
   rc = decode_geometry(r, &sch, &err);
   if (rc) return fail(rc, err);
+  // (CUDA-graph mode: the first plan's choice, which captured runs hold)
+  const bool sinks = h->graph && h->g_batch >= 0 ? h->sinks : r.num_sinks > 0 || key_weights;
   const DecodeKernel* k =
-      find_decode(sch.kind, q_dtype, kv_dtype, head_dim, sch.heads_per_cta, r.rope,
-                  key_weights ? 1 : 0);
+      find_decode(sch.kind, q_dtype, kv_dtype, head_dim, sch.heads_per_cta, r.rope, sinks, key_weights);
   if (!k) return fail(PKD_ERR_UNSUPPORTED, "no decode kernel built for this dtype / head_dim");
   cudaError_t e = set_smem_limit_once(k, h->device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
@@ -824,6 +832,7 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   h->cap = logits_soft_cap > 0.f ? logits_soft_cap : 0.f;
   h->indices = h->graph ? h->g_indices : indices_dev;
   h->dlayout = lay;
+  h->sinks = sinks;
   h->key_weights = key_weights;
   h->klayout = klay;
   h->n_key_tiles = (int)n_key_tiles;

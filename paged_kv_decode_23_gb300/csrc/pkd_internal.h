@@ -176,6 +176,7 @@ struct DecodeKernel {
   int nstages;      // pipeline stages
   int max_ctas = kDecodeCtasPerSm;  // CTAs per SM it is sized for
   int box_rows = 0;                 // rows of a tensor-map box at most; 0: tile_tokens
+  int sinks = 0;                    // 1: takes tasks with sinks
   int scores = 0;                   // 1: leaves the attended keys' scores (plans with key weights)
 };
 
@@ -187,8 +188,10 @@ void register_decode_rope(std::vector<DecodeKernel>& out);
 void register_decode_rope_cc(std::vector<DecodeKernel>& out);
 void register_decode_rope_cc_e4m3(std::vector<DecodeKernel>& out);
 void register_decode_e2m1(std::vector<DecodeKernel>& out);
-void register_decode_weights(std::vector<DecodeKernel>& out);
-void register_decode_e2m1_weights(std::vector<DecodeKernel>& out);
+void register_decode_sinks(std::vector<DecodeKernel>& out);
+void register_decode_scores(std::vector<DecodeKernel>& out);
+void register_decode_e2m1_sinks(std::vector<DecodeKernel>& out);
+void register_decode_e2m1_scores(std::vector<DecodeKernel>& out);
 
 // MLA decode kernel parameters (pkd_mla_run -> mla_decode_kernel).
 struct MlaParams {

@@ -144,3 +144,16 @@ def test_a_captured_run_with_sinks_replays_across_plans():
         torch.cuda.synchronize()
         assert dec.check_status() == 0
         assert_decode(q, o, lse, decode_ref(part, pool64, q, window=window, sinks=sinks), pool64, 4000, what=str(step))
+
+
+def test_captured_runs_without_sinks_take_none_later():
+    from paged_kv_decode_23_gb300 import CUDAGraphBatchDecodePagedKV, PkdError
+    i32 = dict(dtype=torch.int32, device="cuda")
+    dec = CUDAGraphBatchDecodePagedKV(torch.zeros(64 << 20, dtype=torch.uint8, device="cuda"), torch.zeros(2, **i32),
+                                      torch.zeros(64, **i32), torch.zeros(1, **i32), "NHD")
+    pg = Pages([900], 16, 2, 128, "same", "NHD", seed=9)
+    args = (torch.from_numpy(pg.host_indptr), pg.indices, torch.from_numpy(pg.last), 8, 2, 128, 16)
+    dec.plan(*args, q_data_type=BF16, window_left=100)
+    with pytest.raises(PkdError, match="no sinks"):
+        dec.plan(*args, q_data_type=BF16, window_left=100, num_sink_tokens=4)
+    dec.plan(*args, q_data_type=BF16, window_left=50)
