@@ -16,6 +16,13 @@
 // before it; then all move rows.  A row that moves into [S, B - R) overwrites nothing that is read; the
 // newest are shifted down once those rows are read, in tiles that are read whole before they are written
 // (a tile's sources lie above every earlier tile's destinations), each CTA a part of the rows' columns.
+//
+// Bound: the moves are a copy's traffic, what comes before them is waiting (three dependent loads, then
+// exchanges between the CTAs of a cluster, some 2 us each).  64 sequences of 2,049 to 2,064 tokens to 2,048, 8
+// heads of 128, 16 bits: 18 us (80 MB, 12 us at a copy's rate), 9 of them selection; 4 of 60,000 to 131,072 to
+// 8,192: 94 us (270 MB, 40), 35 of them selection and 45 the moves.  In the first, instructions counted: places worked out once a
+// row and passed by shuffles, and strides in 32 bits, took a quarter of the 17.8 M warp instructions of
+// 64-bit arithmetic per piece (38 us).  Fetching the newest rows into L2 ahead changed nothing.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -30,6 +37,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kBins = 2048;  // of an 11-bit digit
 constexpr int kMaxRanks = 8;
+// Where at most so many keys share the digits found so far, they are compared with each other instead of
+// going through the next digits (without that 512 units of 2,064 tokens take 1.5 to 3 us more).
 constexpr int kFew = 256;
 constexpr int kMostTokens = 1 << 30;  // (positions and steps past them stay in 32 bits)
 
@@ -64,7 +73,6 @@ struct EvictParams {
   int pieces_log;  // 16-byte pieces of a row, K and V together: 1 << pieces_log
   int words;       // 4-byte words of a row's scales, K (or V) alone
   int cap;         // keys that a CTA's shared memory holds; the others are read again
-  int ahead;       // of the newest, rows that are fetched into L2 while the others are chosen
 };
 
 // One (sequence, kv head): where its rows lie.
@@ -208,16 +216,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
       if (j + 1 >= v0 && j + 1 < v1) atomicAdd(&hist[0][k.y >> 21], 1);
       if (j + 2 >= v0 && j + 2 < v1) atomicAdd(&hist[0][k.z >> 21], 1);
       if (j + 3 >= v0 && j + 3 < v1) atomicAdd(&hist[0][k.w >> 21], 1);
-    }
-  }
-  // the newest's rows will be read whatever is chosen
-  {
-    const int line_log = max(p.pieces_log - 3, 1);  // 128-byte lines of a row: K's, then V's (shorter rows: one each)
-    for (int x = me; x < p.ahead << line_log; x += all) {
-      const int t = n - 1 - (x >> line_log);
-      if (known(at.page(t)))
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            at.piece_at(at.offset(t), (x & ((1 << line_log) - 1)) << (p.pieces_log - line_log))));
     }
   }
   // (the pages of the sinks and of the newest)
@@ -582,17 +580,21 @@ cudaError_t launch_evict(const pkd_evict_args& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // The lengths are on the device; the pages that a sequence owns on average stand for them.  CTAs a
-  // (sequence, kv head): as many as fill the GPU twice, but none for fewer than 1,024 tokens.
+  // (sequence, kv head): as many as the GPU holds of 512 threads, two an SM, but none for fewer than some
+  // 1,100 tokens, where the exchanges take longer than what they save (us for 1, 2, 4, 8 CTAs, 8 heads of 128):
+  // 1 sequence of 2,064 tokens 10.4, 12.4, 12.4, 14.5; 8 of 4,096 28.7, 22.5, 23.3, 46.4; 1 of 16,000 55, 37,
+  // 24.6, 22.6; 4 of 60,000 to 131,072 744, 392, 188, 94; 33 of 500 to 9,000 (2 heads of 256) 46, 38, 30, 52.
   const int units = c.batch * c.num_kv_heads;
   p.places = 2 * (int64_t)units * (a.budget - a.num_sink_tokens - a.num_recent);
   const int64_t tokens = c.num_indices * c.page_size / c.batch;
   int ranks = 1;
-  while (ranks < kMaxRanks && (int64_t)units * ranks * 2 <= 2 * sms && tokens / (ranks * 2) >= 1024) ranks *= 2;
+  while (ranks < kMaxRanks && (int64_t)units * ranks * 2 <= 2 * sms && tokens / (ranks * 2) >= 1100) ranks *= 2;
   p.cap = 1024;  // room for the average and a half of it, at most 64 KiB
   while (p.cap < 16 << 10 && p.cap < tokens / ranks + tokens / ranks / 2) p.cap *= 2;
-  const int64_t room = (int64_t(48) << 20) / ((int64_t)units * row * 2);  // rows of every unit that L2 takes
-  p.ahead = (int)std::min<int64_t>(a.num_recent, room);
-  return ranks == 1 ? launch<256, 4, false, 2>(p, units, 1, s) : launch<512, 2, true, 4>(p, units, ranks, s);
+  // One CTA each: of 512 threads while all of those are resident at once, else of 256, four an SM (us with 512
+  // and 256 threads: 256 units of 4,096 tokens 65.8, 71.7; 512 of 2,064 25, 18; 1,024 of 1,040 55, 44).
+  if (ranks > 1) return launch<512, 2, true, 4>(p, units, ranks, s);
+  return units > 2 * sms ? launch<256, 4, false, 2>(p, units, 1, s) : launch<512, 2, false, 2>(p, units, 1, s);
 }
 
 }  // namespace pkd
