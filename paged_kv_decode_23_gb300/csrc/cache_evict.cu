@@ -19,10 +19,10 @@
 //
 // Bound: the moves are a copy's traffic, what comes before them is waiting (three dependent loads, then
 // exchanges between the CTAs of a cluster, some 2 us each).  64 sequences of 2,049 to 2,064 tokens to 2,048, 8
-// heads of 128, 16 bits: 18 us (80 MB, 12 us at a copy's rate), 9 of them selection; 4 of 60,000 to 131,072 to
-// 8,192: 94 us (270 MB, 40), 35 of them selection and 45 the moves.  In the first, instructions counted: places worked out once a
+// heads of 128, 16 bits: 26 us (80 MB, 12 us at a copy's rate; 18 us with the rows in L2), 9 of them selection;
+// 4 of 60,000 to 131,072 to 8,192: 92 us (270 MB, 40), 35 of them selection and 45 the moves.  In the first, instructions counted: places worked out once a
 // row and passed by shuffles, and strides in 32 bits, took a quarter of the 17.8 M warp instructions of
-// 64-bit arithmetic per piece (38 us).  Fetching the newest rows into L2 ahead changed nothing.
+// 64-bit arithmetic per piece (38 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -73,6 +73,7 @@ struct EvictParams {
   int pieces_log;  // 16-byte pieces of a row, K and V together: 1 << pieces_log
   int words;       // 4-byte words of a row's scales, K (or V) alone
   int cap;         // keys that a CTA's shared memory holds; the others are read again
+  int ahead;       // of the newest, rows that are fetched into L2 while the others are chosen
 };
 
 // One (sequence, kv head): where its rows lie.
@@ -216,6 +217,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
       if (j + 1 >= v0 && j + 1 < v1) atomicAdd(&hist[0][k.y >> 21], 1);
       if (j + 2 >= v0 && j + 2 < v1) atomicAdd(&hist[0][k.z >> 21], 1);
       if (j + 3 >= v0 && j + 3 < v1) atomicAdd(&hist[0][k.w >> 21], 1);
+    }
+  }
+  // the newest's rows will be read whatever is chosen (before the keys' loads this was no gain)
+  {
+    const int line_log = max(p.pieces_log - 3, 1);  // 128-byte lines of a row: K's, then V's (shorter rows: one each)
+    for (int x = me; x < p.ahead << line_log; x += all) {
+      const int t = n - 1 - (x >> line_log);
+      if (known(at.page(t)))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            at.piece_at(at.offset(t), (x & ((1 << line_log) - 1)) << (p.pieces_log - line_log))));
     }
   }
   // (the pages of the sinks and of the newest)
@@ -593,6 +604,10 @@ cudaError_t launch_evict(const pkd_evict_args& a, cudaStream_t s) {
   while (p.cap < 16 << 10 && p.cap < tokens / ranks + tokens / ranks / 2) p.cap *= 2;
   // One CTA each: of 512 threads while all of those are resident at once, else of 256, four an SM (us with 512
   // and 256 threads: 256 units of 4,096 tokens 65.8, 71.7; 512 of 2,064 25, 18; 1,024 of 1,040 55, 44).
+  // 64 sequences of 2,064 tokens with 128 newest, not in L2: 26.0 us for 28.4; up to what L2 holds beside
+  // the rest, no gain elsewhere.
+  const int64_t room = (int64_t(48) << 20) / ((int64_t)units * row * 2);
+  p.ahead = (int)std::min<int64_t>(a.num_recent, room);
   if (ranks > 1) return launch<512, 2, true, 4>(p, units, ranks, s);
   return units > 2 * sms ? launch<256, 4, false, 2>(p, units, 1, s) : launch<512, 2, false, 2>(p, units, 1, s);
 }
