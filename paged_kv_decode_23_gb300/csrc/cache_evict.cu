@@ -18,11 +18,12 @@
 // (a tile's sources lie above every earlier tile's destinations), each CTA a part of the rows' columns.
 //
 // Bound: the moves are a copy's traffic, what comes before them is waiting (three dependent loads, then
-// exchanges between the CTAs of a cluster, some 2 us each).  64 sequences of 2,049 to 2,064 tokens to 2,048, 8
-// heads of 128, 16 bits: 26 us (80 MB, 12 us at a copy's rate; 18 us with the rows in L2), 9 of them selection;
-// 4 of 60,000 to 131,072 to 8,192: 92 us (270 MB, 40), 35 of them selection and 45 the moves.  In the first, instructions counted: places worked out once a
-// row and passed by shuffles, and strides in 32 bits, took a quarter of the 17.8 M warp instructions of
-// 64-bit arithmetic per piece (38 us).
+// exchanges between the CTAs of a cluster, some 2 us each) and, where a CTA holds thousands of keys, instructions.
+// 64 sequences of 2,049 to 2,064 tokens to 2,048, 8 heads of 128, 16 bits: 24.5 us (80 MB, 12 us at a copy's
+// rate; 17 us with the rows in L2), 9 of them selection; 4 of 60,000 to 131,072 to 8,192: 83 us (270 MB, 40), some
+// 27 of them selection and 45 the moves.  Places worked out once a row and passed by shuffles, and strides in 32
+// bits, took 9 M of 17.8 M warp instructions away (38 -> 25 us in the first); loops over keys that are known to
+// lie in shared memory 9 us in the second.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -250,174 +251,181 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
   // where most slots take their tokens from; the moves below change what they change
   if (kept)
     for (int j = me; j < B; j += all) kept[j] = j < B - R ? j : j + n - B;
-  auto key = [&](int i) { return i < p.cap ? keys[i] : order_key(*at.weight(lo + i)); };
-
-  // ---- the m-th largest key T among the candidates, and how many of those equal to it are chosen
-  uint32_t T = 0xffffffffu;
-  int equal = 0;  // (m = 0: nothing is chosen)
-  if (m > 0) {
-    T = 0;
-    equal = m;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      int* h = hist[pass & 1];
-      if (pass > 0) {
-        for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<int4*>(h)[i] = make_int4(0, 0, 0, 0);
-        __syncthreads();
-#pragma unroll 4
-        for (int i = v0 + tid; i < v1; i += THREADS) {
-          const uint32_t k = key(i);
-          if (k >> (shift + bits) == T) atomicAdd(&h[(k >> shift) & ((1 << bits) - 1)], 1);
-        }
-        sync();
-      }
-      // threads take E bins each, from the highest down, summed over the cluster
-      const int top = kBins - 1 - tid * E;
-      int sum[E], mine = 0;
-#pragma unroll
-      for (int i = 0; i < E; ++i) sum[i] = 0;
-#pragma unroll
-      for (int r = 0; r < (CLUSTER ? kMaxRanks : 1); ++r)
-        if (r < ranks) {
-          const int4* hr = reinterpret_cast<const int4*>(of_rank(h, r)) + (top >> 2);
-#pragma unroll
-          for (int i = 0; i < E; i += 4) {
-            const int4 v = hr[-(i >> 2)];
-            sum[i] += v.w; sum[i + 1] += v.z; sum[i + 2] += v.y; sum[i + 3] += v.x;
-          }
-        }
-#pragma unroll
-      for (int i = 0; i < E; ++i) mine += sum[i];
-      int all_keys;
-      int above = block_prefix<THREADS>(mine, part[0], all_keys);
-      if (above < equal && equal <= above + mine) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          if (above < equal && equal <= above + sum[i]) {
-            found[0] = top - i;
-            found[1] = above;
-            found[2] = sum[i];
-          }
-          above += sum[i];
-        }
-      }
-      __syncthreads();
-      T = T << bits | (uint32_t)found[0];
-      equal -= found[1];
-      const int left = found[2];
-      __syncthreads();  // (found is written again)
-      if (pass < 2 && left <= kFew) {
-        // few keys begin with T: each is compared with all of them
-        for (int i = v0 + tid; i < v1; i += THREADS) {
-          const uint32_t k = key(i);
-          if (k >> shift == T) few[atomicAdd(&said[6], 1)] = k;
-        }
-        sync();
-        if constexpr (CLUSTER) {  // those of all CTAs, into the histogram that is not in use
-          uint32_t* list = reinterpret_cast<uint32_t*>(hist[~pass & 1]);
-          if (tid < ranks) theirs[0][tid] = *of_rank(&said[6], tid);
-          __syncthreads();
-          for (int i = tid; i < left; i += THREADS) {
-            int r = 0, j = i;
-            while (j >= theirs[0][r]) j -= theirs[0][r++];
-            list[i] = of_rank(few, r)[j];
-          }
-          __syncthreads();
-        }
-        const uint32_t* list = CLUSTER ? reinterpret_cast<const uint32_t*>(hist[~pass & 1]) : few;
-        for (int i = tid; i < left; i += THREADS) {
-          const uint32_t k = list[i];
-          int greater = 0, same = 0;
-          for (int j = 0; j < left; ++j) {
-            greater += list[j] > k;
-            same += list[j] == k;
-          }
-          if (greater < equal && equal <= greater + same) {  // (of equal keys, all say the same)
-            found[0] = (int)k;
-            found[1] = greater;
-          }
-        }
-        __syncthreads();
-        T = (uint32_t)found[0];
-        equal -= found[1];
-        break;
-      }
-    }
-  }
-
-  // ---- counts of each thread's run; the chosen among equal keys are the first of them.  (Runs of an
-  // odd length keep the threads of a warp in different banks.)
-  const int run = ((v1 - v0 + THREADS - 1) / THREADS) | 1;
-  const int i0 = min(v0 + tid * run, v1), i1 = min(i0 + run, v1);
-  const int edge = min(max(B - R - lo, i0), i1);  // [i0, edge) lies in [S, B - R)
-  int gt_low = 0, gt_high = 0, eq_low = 0, eq_high = 0;
-#pragma unroll 4
-  for (int i = i0; i < edge; ++i) {
-    const uint32_t k = key(i);
-    gt_low += k > T;
-    eq_low += k == T;
-  }
-#pragma unroll 4
-  for (int i = edge; i < i1; ++i) {
-    const uint32_t k = key(i);
-    gt_high += k > T;
-    eq_high += k == T;
-  }
-  // Equal keys before this thread's, and with them what it leaves free and moves; then both before it.
-  // A CTA's tokens below B - R come before its others, so its sums of five counts say how many of its
-  // equal keys are chosen on either side: one exchange between the CTAs.
-  int total;
-  int eq_base = block_prefix<THREADS>(eq_low + eq_high, part[1], total);
-  int free_base = 0, move_base = 0, n_moves;
-  if constexpr (CLUSTER) {
-    const int five[5] = {eq_low, eq_high, gt_low, gt_high, edge - i0};
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      const int x = __reduce_add_sync(~0u, five[i]);
-      if (lane == 0 && x) atomicAdd(&said[i], x);
-    }
-    sync();
-    for (int i = tid; i < 5 * ranks; i += THREADS) theirs[i % 5][i / 5] = of_rank(said, i / 5)[i % 5];
-    __syncthreads();
-    int eq_before = 0;
-    n_moves = 0;
-    for (int r = 0; r < ranks; ++r) {
-      const int of[5] = {theirs[0][r], theirs[1][r], theirs[2][r], theirs[3][r], theirs[4][r]};
-      const int lows = of[0], highs = of[1];
-      const int take_low = max(0, min(lows, equal - eq_before)), take_high = max(0, min(highs, equal - eq_before - lows));
-      if (r < rank) {
-        eq_base += lows + highs;
-        free_base += of[4] - of[2] - take_low;
-        move_base += of[3] + take_high;
-      }
-      n_moves += of[3] + take_high;
-      eq_before += lows + highs;
-    }
-  }
-  eq_low = max(0, min(eq_low, equal - eq_base));
-  eq_high = max(0, min(eq_high, equal - eq_base - eq_low));
-  free_base += block_prefix<THREADS>(edge - i0 - gt_low - eq_low, part[0], total);
-  move_base += block_prefix<THREADS>(gt_high + eq_high, part[1], total);
-  if constexpr (!CLUSTER) n_moves = total;
-
-  // ---- the lists: the i-th free slot of [S, B - R) takes the i-th chosen above it, its weight with it
   int2* moves = reinterpret_cast<int2*>(p.moves) + (int64_t)unit * m;
   int32_t* places = p.moves + p.places + (int64_t)unit * m;
-  {
-    int left = equal - eq_base;  // equal keys still to choose
-    for (int i = i0; i < edge; ++i) {
-      const uint32_t k = key(i);
-      if (!(k > T || (k == T && left-- > 0))) places[free_base++] = lo + i;
-    }
-    for (int i = edge; i < i1; ++i) {
-      const uint32_t k = key(i);
-      if (k > T || (k == T && left-- > 0)) {
-        const bool plain = k != 0xffffffffu && k != 0x80000000u;
-        moves[move_base++] = make_int2(lo + i, __float_as_int(plain ? weight_of(k) : *at.weight(lo + i)));
+  int n_moves = 0;
+  auto choose = [&](auto key) {
+    // ---- the m-th largest key T among the candidates, and how many of those equal to it are chosen
+    uint32_t T = 0xffffffffu;
+    int equal = 0;  // (m = 0: nothing is chosen)
+    if (m > 0) {
+      T = 0;
+      equal = m;
+#pragma unroll 1
+      for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        int* h = hist[pass & 1];
+        if (pass > 0) {
+          for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<int4*>(h)[i] = make_int4(0, 0, 0, 0);
+          __syncthreads();
+#pragma unroll 4
+          for (int i = v0 + tid; i < v1; i += THREADS) {
+            const uint32_t k = key(i);
+            if (k >> (shift + bits) == T) atomicAdd(&h[(k >> shift) & ((1 << bits) - 1)], 1);
+          }
+          sync();
+        }
+        // threads take E bins each, from the highest down, summed over the cluster
+        const int top = kBins - 1 - tid * E;
+        int sum[E], mine = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum[i] = 0;
+#pragma unroll
+        for (int r = 0; r < (CLUSTER ? kMaxRanks : 1); ++r)
+          if (r < ranks) {
+            const int4* hr = reinterpret_cast<const int4*>(of_rank(h, r)) + (top >> 2);
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+              const int4 v = hr[-(i >> 2)];
+              sum[i] += v.w; sum[i + 1] += v.z; sum[i + 2] += v.y; sum[i + 3] += v.x;
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < E; ++i) mine += sum[i];
+        int all_keys;
+        int above = block_prefix<THREADS>(mine, part[0], all_keys);
+        if (above < equal && equal <= above + mine) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            if (above < equal && equal <= above + sum[i]) {
+              found[0] = top - i;
+              found[1] = above;
+              found[2] = sum[i];
+            }
+            above += sum[i];
+          }
+        }
+        __syncthreads();
+        T = T << bits | (uint32_t)found[0];
+        equal -= found[1];
+        const int left = found[2];
+        __syncthreads();  // (found is written again)
+        if (pass < 2 && left <= kFew) {
+          // few keys begin with T: each is compared with all of them
+          for (int i = v0 + tid; i < v1; i += THREADS) {
+            const uint32_t k = key(i);
+            if (k >> shift == T) few[atomicAdd(&said[6], 1)] = k;
+          }
+          sync();
+          if constexpr (CLUSTER) {  // those of all CTAs, into the histogram that is not in use
+            uint32_t* list = reinterpret_cast<uint32_t*>(hist[~pass & 1]);
+            if (tid < ranks) theirs[0][tid] = *of_rank(&said[6], tid);
+            __syncthreads();
+            for (int i = tid; i < left; i += THREADS) {
+              int r = 0, j = i;
+              while (j >= theirs[0][r]) j -= theirs[0][r++];
+              list[i] = of_rank(few, r)[j];
+            }
+            __syncthreads();
+          }
+          const uint32_t* list = CLUSTER ? reinterpret_cast<const uint32_t*>(hist[~pass & 1]) : few;
+          for (int i = tid; i < left; i += THREADS) {
+            const uint32_t k = list[i];
+            int greater = 0, same = 0;
+            for (int j = 0; j < left; ++j) {
+              greater += list[j] > k;
+              same += list[j] == k;
+            }
+            if (greater < equal && equal <= greater + same) {  // (of equal keys, all say the same)
+              found[0] = (int)k;
+              found[1] = greater;
+            }
+          }
+          __syncthreads();
+          T = (uint32_t)found[0];
+          equal -= found[1];
+          break;
+        }
       }
     }
-  }
+
+    // ---- counts of each thread's run; the chosen among equal keys are the first of them.  (Runs of an
+    // odd length keep the threads of a warp in different banks.)
+    const int run = ((v1 - v0 + THREADS - 1) / THREADS) | 1;
+    const int i0 = min(v0 + tid * run, v1), i1 = min(i0 + run, v1);
+    const int edge = min(max(B - R - lo, i0), i1);  // [i0, edge) lies in [S, B - R)
+    int gt_low = 0, gt_high = 0, eq_low = 0, eq_high = 0;
+#pragma unroll 4
+    for (int i = i0; i < edge; ++i) {
+      const uint32_t k = key(i);
+      gt_low += k > T;
+      eq_low += k == T;
+    }
+#pragma unroll 4
+    for (int i = edge; i < i1; ++i) {
+      const uint32_t k = key(i);
+      gt_high += k > T;
+      eq_high += k == T;
+    }
+    // Equal keys before this thread's, and with them what it leaves free and moves; then both before it.
+    // A CTA's tokens below B - R come before its others, so its sums of five counts say how many of its
+    // equal keys are chosen on either side: one exchange between the CTAs.
+    int total;
+    int eq_base = block_prefix<THREADS>(eq_low + eq_high, part[1], total);
+    int free_base = 0, move_base = 0;
+    if constexpr (CLUSTER) {
+      const int five[5] = {eq_low, eq_high, gt_low, gt_high, edge - i0};
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const int x = __reduce_add_sync(~0u, five[i]);
+        if (lane == 0 && x) atomicAdd(&said[i], x);
+      }
+      sync();
+      for (int i = tid; i < 5 * ranks; i += THREADS) theirs[i % 5][i / 5] = of_rank(said, i / 5)[i % 5];
+      __syncthreads();
+      int eq_before = 0;
+      n_moves = 0;
+      for (int r = 0; r < ranks; ++r) {
+        const int of[5] = {theirs[0][r], theirs[1][r], theirs[2][r], theirs[3][r], theirs[4][r]};
+        const int lows = of[0], highs = of[1];
+        const int take_low = max(0, min(lows, equal - eq_before));
+        const int take_high = max(0, min(highs, equal - eq_before - lows));
+        if (r < rank) {
+          eq_base += lows + highs;
+          free_base += of[4] - of[2] - take_low;
+          move_base += of[3] + take_high;
+        }
+        n_moves += of[3] + take_high;
+        eq_before += lows + highs;
+      }
+    }
+    eq_low = max(0, min(eq_low, equal - eq_base));
+    eq_high = max(0, min(eq_high, equal - eq_base - eq_low));
+    free_base += block_prefix<THREADS>(edge - i0 - gt_low - eq_low, part[0], total);
+    move_base += block_prefix<THREADS>(gt_high + eq_high, part[1], total);
+    if constexpr (!CLUSTER) n_moves = total;
+
+    // ---- the lists: the i-th free slot of [S, B - R) takes the i-th chosen above it, its weight with it
+    {
+      int left = equal - eq_base;  // equal keys still to choose
+#pragma unroll 4
+      for (int i = i0; i < edge; ++i) {
+        const uint32_t k = key(i);
+        if (k <= T && !(k == T && left-- > 0)) places[free_base++] = lo + i;
+      }
+#pragma unroll 4
+      for (int i = edge; i < i1; ++i) {
+        const uint32_t k = key(i);
+        if (k >= T && (k > T || left-- > 0)) {
+          const bool plain = k != 0xffffffffu && k != 0x80000000u;
+          moves[move_base++] = make_int2(lo + i, __float_as_int(plain ? weight_of(k) : *at.weight(lo + i)));
+        }
+      }
+    }
+  };
+  // (a run that shared memory does not hold goes through the same steps, its last keys read again)
+  if (v1 <= p.cap) choose([&](int i) { return keys[i]; });
+  else choose([&](int i) { return i < p.cap ? keys[i] : order_key(*at.weight(lo + i)); });
   sync();
 
   // ---- candidates' slots that no token is left in

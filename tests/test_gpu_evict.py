@@ -98,6 +98,8 @@ CASES = [
     ("e2m1", "NHD", 1, 256, 128, [700], 130, 128, 1),
     ("same", "NHD", 2, 64, 16, [40000, 30000], 9000, 4, 1000),
     ("same", "HND", 2, 128, 16, [1025] * 5, 1024, 4, 1000),           # one token more, each
+    ("same", "NHD", 2, 64, 16, [40000] + [9] * 40, 9000, 4, 100),     # far longer than the others
+    ("e4m3", "HND", 1, 128, 8, [70000, 8, 8], 300, 0, 7),             # and over several CTAs
 ]
 
 
