@@ -119,6 +119,21 @@ struct TileRun {
   __device__ __forceinline__ int lo(const BlockCoords&) const { return lo_; }
   __device__ __forceinline__ int hi(const BlockCoords&) const { return hi_; }
 };
+// TileRun<true> without state: which run tile i belongs to is asked every time.
+template <int TS>
+struct TileOf {
+  bool sink;
+  __device__ __forceinline__ explicit TileOf(const BlockCoords& b) : sink(b.ns > 0) {}
+  __device__ __forceinline__ bool move(const DecodeParams&, const BlockCoords& b, int i) {
+    sink = i < b.ns;
+    return i == b.ns && i > 0;
+  }
+  __device__ __forceinline__ int t0(const BlockCoords& b, int i) const {
+    return (sink ? b.it.sink_begin : b.it.chunk_tok0 + (b.j0 - b.ns) * TS) + i * TS;
+  }
+  __device__ __forceinline__ int lo(const BlockCoords& b) const { return sink ? b.it.sink_begin : b.it.tok_begin; }
+  __device__ __forceinline__ int hi(const BlockCoords& b) const { return sink ? b.it.sink_end : b.it.tok_end; }
+};
 template <int TS>
 struct TileRun<false, TS> {
   __device__ __forceinline__ explicit TileRun(const BlockCoords&) {}
