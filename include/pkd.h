@@ -610,11 +610,14 @@ int pkd_gather(const pkd_gather_args* args, void* stream);
  *          behind the sequence's end.
  *   moves  device workspace of 3 * batch * num_kv_heads * (budget - S - R) int32, 8-byte aligned
  *          (NULL if that is 0).
- * A sequence with a negative length, more than 2^30 tokens or more than its pages hold, sets PKD_STATUS_BAD_TOKEN
- * in status (may be NULL), one whose page ids lie outside the pool PKD_STATUS_BAD_PAGE; it is left alone, its kept entries -1.
+ * budget: in [1, 2^30].  A sequence with a negative length, more than 2^30 tokens or more than its pages
+ * hold, sets PKD_STATUS_BAD_TOKEN in status (may be NULL), one whose page ids lie outside the pool
+ * PKD_STATUS_BAD_PAGE; it is left alone, its kept entries -1.
  * Sequences must not share pages of tokens that move or whose places are taken (none that are evicted
- * should: see pkd_pages_fork).  The pool's rows must not overlap, nor key_weights' entries (strides of
- * page, head, slot in elements).  k_scale and v_scale are not used.
+ * should: see pkd_pages_fork), and nothing that the call reads may change while it runs.  The pool's rows
+ * must not overlap, nor key_weights' entries (strides of page, head, slot in elements); page and slot
+ * strides are below 2^32 units (of 16 bytes, 4 for scales, an element for weights).  k_scale and v_scale
+ * are not used.
  */
 typedef struct pkd_evict_args {
   pkd_paged_pool pool;

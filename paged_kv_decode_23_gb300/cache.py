@@ -293,9 +293,9 @@ def evict_paged_kv(paged_kv_cache, key_weights: torch.Tensor, kv_lens: torch.Ten
     pool, hkv, _ = _pool_fields(paged_kv_cache, kv_block_scales, kv_indptr, kv_indices, kv_layout, None, None, dev, io)
     batch, ps = pool[14], pool[18]
     budget, sinks, recent = int(budget), int(num_sink_tokens), int(num_recent)
-    if not (1 <= budget < 2 ** 31 and 0 <= sinks and 0 <= recent and sinks + recent <= budget):
-        raise ValueError("budget must be a positive 32-bit number, num_sink_tokens and num_recent must be "
-                         ">= 0 and fit it together")
+    if not (1 <= budget <= 2 ** 30 and 0 <= sinks and 0 <= recent and sinks + recent <= budget):
+        raise ValueError("budget must lie in [1, 2^30], num_sink_tokens and num_recent must be >= 0 and fit "
+                         "it together")
     lens = _index(kv_lens, "kv_lens", dev, batch)
     weights = weight_views(key_weights, first.shape[0], hkv, ps, dev)
     heads, middle = batch * hkv, budget - sinks - recent

@@ -239,7 +239,7 @@ extern "C" int pkd_evict(const pkd_evict_args* args, void* stream) {
     const int dt = a.pool.dtype;
     if (int rc = check_pool(a.pool, dt == PKD_DTYPE_BF16 ? PKD_DTYPE_BF16 : PKD_DTYPE_F16, true)) return rc;
     if (int rc = check_written(a.pool)) return rc;
-    if (a.budget < 1) return bad("budget must be >= 1");
+    if (a.budget < 1 || a.budget > 1 << 30) return bad("budget must lie in [1, 2^30]");
     if (a.num_sink_tokens < 0 || a.num_recent < 0 || (int64_t)a.num_sink_tokens + a.num_recent > a.budget)
       return bad("num_sink_tokens and num_recent must be >= 0 and fit the budget together");
     if (a.pool.batch == 0) return done(cudaSuccess, "");

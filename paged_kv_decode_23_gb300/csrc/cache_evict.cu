@@ -314,7 +314,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
           // few keys begin with T: each is compared with all of them
           for (int i = v0 + tid; i < v1; i += THREADS) {
             const uint32_t k = key(i);
-            if (k >> shift == T) few[atomicAdd(&said[6], 1)] = k;
+            if (k >> shift == T) {
+              const int x = atomicAdd(&said[6], 1);
+              if (x < kFew) few[x] = k;
+            }
           }
           sync();
           if constexpr (CLUSTER) {  // those of all CTAs, into the histogram that is not in use
@@ -323,8 +326,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
             __syncthreads();
             for (int i = tid; i < left; i += THREADS) {
               int r = 0, j = i;
-              while (j >= theirs[0][r]) j -= theirs[0][r++];
-              list[i] = of_rank(few, r)[j];
+              while (r + 1 < ranks && j >= theirs[0][r]) j -= theirs[0][r++];
+              list[i] = of_rank(few, r)[j & (kFew - 1)];
             }
             __syncthreads();
           }
@@ -411,22 +414,25 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
 #pragma unroll 4
       for (int i = i0; i < edge; ++i) {
         const uint32_t k = key(i);
-        if (k <= T && !(k == T && left-- > 0)) places[free_base++] = lo + i;
+        if (k <= T && !(k == T && left-- > 0) && free_base < m) places[free_base++] = lo + i;
       }
 #pragma unroll 4
       for (int i = edge; i < i1; ++i) {
         const uint32_t k = key(i);
-        if (k >= T && (k > T || left-- > 0)) {
+        if (k >= T && (k > T || left-- > 0) && move_base < m) {
           const bool plain = k != 0xffffffffu && k != 0x80000000u;
           moves[move_base++] = make_int2(lo + i, __float_as_int(plain ? weight_of(k) : *at.weight(lo + i)));
         }
       }
     }
   };
-  // (a run that shared memory does not hold goes through the same steps, its last keys read again)
+  // (A run that shared memory does not hold goes through the same steps, its last keys read again.  Were they
+  // to change meanwhile, what is chosen would mean nothing; that lists and rows stay in their bounds all the
+  // same is what the tests of free_base, move_base and of the places below are for.)
   if (v1 <= p.cap) choose([&](int i) { return keys[i]; });
   else choose([&](int i) { return i < p.cap ? keys[i] : order_key(*at.weight(lo + i)); });
   sync();
+  n_moves = min(n_moves, m);
 
   // ---- candidates' slots that no token is left in
   const int W = 2 * p.words;
@@ -448,8 +454,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_kernel(const __grid_const
     const int rows = min(per_warp, n_moves - r0);
     uint64_t from = 0, to = 0;
     if (lane < rows) {
-      const int2 mv = __ldcg(moves + r0 + lane);
-      const int place = __ldcg(places + r0 + lane);
+      int2 mv = __ldcg(moves + r0 + lane);
+      int place = __ldcg(places + r0 + lane);
+      if (mv.x < B - R || mv.x >= n - R) mv.x = B - R;
+      if (place < S || place >= B - R) place = S;
       from = at.offset(mv.x);
       to = at.offset(place);
       if (kept) kept[place] = mv.x;

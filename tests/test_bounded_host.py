@@ -183,7 +183,7 @@ def _evict_args(**over):
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(budget=0), -1), (dict(budget=-3), -1), (dict(sinks=-1), -1), (dict(recent=-1), -1), (dict(sinks=60), -1),
+    (dict(budget=0), -1), (dict(budget=-3), -1), (dict(budget=2 ** 30 + 1), -1), (dict(budget=2 ** 31 - 1), -1), (dict(sinks=-1), -1), (dict(recent=-1), -1), (dict(sinks=60), -1),
     (dict(recent=2 ** 31 - 1, sinks=2 ** 31 - 1), -1), (dict(w=0), -1), (dict(w=258), -1), (dict(w2=0), -1), (dict(w0=15), -1),
     (dict(w1=-16), -1), (dict(w0=2 ** 62), -1), (dict(lens=0), -1), (dict(moves=0), -1), (dict(moves=68), -1), (dict(ip=0), -1),
     (dict(ix=0), -1), (dict(k=0), -1), (dict(v=4096), -1), (dict(k=4100), -1), (dict(s1=100), -1), (dict(s0=128), -1),

@@ -156,6 +156,22 @@ def test_pairs_strides_and_no_kept():
     assert (wide[:, :, 0] == 5).all() and (wide[..., :16] == 5).all() and (wide[..., 144:] == 5).all()
 
 
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_weights_whose_address_is_no_multiple_of_16(off):
+    from paged_kv_decode_23_gb300 import evict_paged_kv
+    lens = [500, 77, 2000]
+    pg = Pages(lens, 8, 3, 64, "e4m3", "HND", seed=off)
+    w = _weights(pg, lens, seed=off)
+    before, w0 = _pools(pg), w.clone()
+    flat = torch.full((w.numel() + 8,), 3.0, device="cuda")
+    mine = flat[off:off + w.numel()].view(w.shape)
+    mine.copy_(w)
+    kept = evict_paged_kv(pg.pool, mine, torch.tensor(lens, dtype=torch.int32, device="cuda"), pg.indptr, pg.indices, 70,
+                          "HND", num_sink_tokens=off, num_recent=9, return_kept=True)
+    check_evicted(pg, lens, before, w0, _pools(pg), mine, kept, 70, off, 9)
+    assert (flat[:off] == 3).all() and (flat[off + w.numel():] == 3).all()
+
+
 def test_sequences_that_cannot_be_evicted_are_left_alone():
     from paged_kv_decode_23_gb300 import _lib as L
     lens = [300, 200, 250, 100]
@@ -232,7 +248,7 @@ def test_refusals():
     pg = Pages(lens, 16, 2, 128, "same", "NHD", seed=5)
     w = _weights(pg, lens)
     before, w0 = _pools(pg), w.clone()
-    for budget, sinks, recent in ((0, 0, 0), (-1, 0, 0), (10, 11, 0), (10, 5, 6), (10, -1, 0), (10, 0, -1), (2 ** 31, 0, 0),
+    for budget, sinks, recent in ((0, 0, 0), (-1, 0, 0), (10, 11, 0), (10, 5, 6), (10, -1, 0), (10, 0, -1), (2 ** 31, 0, 0), (2 ** 30 + 1, 0, 0),
                                   (10, 2 ** 31 - 1, 2 ** 31 - 1)):
         with pytest.raises(ValueError):
             _evict(pg, lens, w, budget, sinks, recent)

@@ -99,6 +99,11 @@ def test_lse_may_be_left_out_and_weights_may_have_strides():
     b.zero_()
     dec.run(q, pg.pool, key_weights=b)
     assert torch.equal(a, b) and (big[:, :, 0] == 7).all() and (big[:, :, 3:] == 7).all()
+    for off in (1, 2, 3):  # an address that is no multiple of 16
+        flat = torch.zeros(a.numel() + 8, device="cuda")
+        mine = flat[off:off + a.numel()].view(a.shape)
+        dec.run(q, pg.pool, key_weights=mine)
+        assert torch.equal(a, mine) and (flat[:off] == 0).all() and (flat[off + a.numel():] == 0).all()
     k, v = pg.pool[:, 0].contiguous(), pg.pool[:, 1].contiguous()
     c = torch.zeros_like(a)
     dec.run(q, (k, v), key_weights=c)
