@@ -217,6 +217,7 @@ int pkd_run_scaled(pkd_handle* h, const pkd_scaled_run* run, void* stream);
  * no row attends are left as they are.  Sums are taken in 32 bits in the order of rows and heads; a page
  * that several requests share takes their sums in no fixed order, which may change the last bit.  A key whose page id
  * lies outside the pool has no entry (PKD_STATUS_BAD_PAGE); nothing is added after PKD_STATUS_TIMEOUT.
+ * The scores lie in the handle's workspace, as split partials do: runs of one handle must not overlap.
  */
 typedef struct pkd_key_weights_run {
   pkd_scaled_run run;

@@ -349,7 +349,8 @@ class BatchDecodePagedKV:
         A plan with ``key_weights=True`` takes ``key_weights``, float32 ``[pages, num_kv_heads,
         page_size]`` in either layout, and adds to each attended key's entry its softmax weight, summed
         over the query heads of its kv head and the request's query tokens.  Other entries are left as
-        they are; a page that several requests share takes all their sums (in no fixed order)."""
+        they are; a page that several requests share takes all their sums (in no fixed order).  Clear
+        the entries of a page before new tokens enter it (``evict_paged_kv`` clears what it frees)."""
         a = self._plan_args
         if a is None:
             raise RuntimeError("plan() must be called before run()")
