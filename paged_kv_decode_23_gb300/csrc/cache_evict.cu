@@ -616,16 +616,21 @@ cudaError_t launch_evict(const pkd_evict_args& a, cudaStream_t s) {
   const int64_t tokens = c.num_indices * c.page_size / c.batch;
   int ranks = 1;
   while (ranks < kMaxRanks && (int64_t)units * ranks * 2 <= 2 * sms && tokens / (ranks * 2) >= 1100) ranks *= 2;
-  p.cap = 1024;  // room for the average and a half of it, at most 64 KiB
-  while (p.cap < 16 << 10 && p.cap < tokens / ranks + tokens / ranks / 2) p.cap *= 2;
-  // One CTA each: of 512 threads while all of those are resident at once, else of 256, four an SM (us with 512
-  // and 256 threads: 256 units of 4,096 tokens 65.8, 71.7; 512 of 2,064 25, 18; 1,024 of 1,040 55, 44).
+  // One CTA each: of 512 threads while all of those are resident at once, else of 256, four an SM, but for long
+  // sequences (us with 512 and 256 threads: 256 units of 4,096 tokens 65.8, 71.7; 512 of 2,064 28.6, 25.0; of
+  // 5,000 161, 159; of 9,000 184, 217; of 16,000 225, 311; 1,024 of 1,040 55, 44).
+  const bool small = units > 2 * sms && tokens <= 6000;
+  // room for the average and a half of it, up to what leaves the SM its CTAs: 32 KiB and 64 KiB (512 units of
+  // 2,064 tokens in a page table four times as long take 26.6 us, with 64 KiB 29.6)
+  const int most = small ? 8 << 10 : 16 << 10;
+  p.cap = 1024;
+  while (p.cap < most && p.cap < tokens / ranks + tokens / ranks / 2) p.cap *= 2;
   // 64 sequences of 2,064 tokens with 128 newest, not in L2: 26.0 us for 28.4; up to what L2 holds beside
   // the rest, no gain elsewhere.
   const int64_t room = (int64_t(48) << 20) / ((int64_t)units * row * 2);
   p.ahead = (int)std::min<int64_t>(a.num_recent, room);
   if (ranks > 1) return launch<512, 2, true, 4>(p, units, ranks, s);
-  return units > 2 * sms ? launch<256, 4, false, 2>(p, units, 1, s) : launch<512, 2, false, 2>(p, units, 1, s);
+  return small ? launch<256, 4, false, 2>(p, units, 1, s) : launch<512, 2, false, 2>(p, units, 1, s);
 }
 
 }  // namespace pkd
