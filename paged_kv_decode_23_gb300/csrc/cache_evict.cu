@@ -19,7 +19,7 @@
 //
 // Bound: the moves are a copy's traffic, what comes before them is waiting (three dependent loads, then
 // exchanges between the CTAs of a cluster, some 2 us each) and, where a CTA holds thousands of keys, instructions.
-// 64 sequences of 2,049 to 2,064 tokens to 2,048, 8 heads of 128, 16 bits: 24.5 us (80 MB, 12 us at a copy's
+// 64 sequences of 2,049 to 2,064 tokens to 2,048, 8 heads of 128, 16 bits: 25 us (80 MB, 12 us at a copy's
 // rate; 17 us with the rows in L2), 9 of them selection; 4 of 60,000 to 131,072 to 8,192: 83 us (270 MB, 40), some
 // 27 of them selection and 45 the moves.  Places worked out once a row and passed by shuffles, and strides in 32
 // bits, took 9 M of 17.8 M warp instructions away (38 -> 25 us in the first); loops over keys that are known to
@@ -621,7 +621,7 @@ cudaError_t launch_evict(const pkd_evict_args& a, cudaStream_t s) {
   // 5,000 161, 159; of 9,000 184, 217; of 16,000 225, 311; 1,024 of 1,040 55, 44).
   const bool small = units > 2 * sms && tokens <= 6000;
   // room for the average and a half of it, up to what leaves the SM its CTAs: 32 KiB and 64 KiB (512 units of
-  // 2,064 tokens in a page table four times as long take 26.6 us, with 64 KiB 29.6)
+  // 2,064 tokens, 256 threads each: 26.6 us with 32 KiB, 29.6 with 64)
   const int most = small ? 8 << 10 : 16 << 10;
   p.cap = 1024;
   while (p.cap < most && p.cap < tokens / ranks + tokens / ranks / 2) p.cap *= 2;
