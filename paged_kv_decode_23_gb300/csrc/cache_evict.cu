@@ -41,6 +41,7 @@ constexpr int kMaxRanks = 8;
 // Where at most so many keys share the digits found so far, they are compared with each other instead of
 // going through the next digits (without that 512 units of 2,064 tokens take 1.5 to 3 us more).
 constexpr int kFew = 256;
+constexpr int kMostKeys = 16 << 10;  // that a CTA holds
 constexpr int kMostTokens = 1 << 30;  // (positions and steps past them stay in 32 bits)
 
 // Order of weights as unsigned numbers: NaN above all, -0 as 0.
@@ -538,7 +539,8 @@ cudaError_t launch(const EvictParams& p, int units, int ranks, cudaStream_t s) {
   const int smem = p.cap * 4;
   const void* fn = reinterpret_cast<const void*>(&evict_kernel<THREADS, CTAS, CLUSTER, LOADS>);
   if (smem > 16 << 10) {  // with what the kernel has besides, more than a launch may take unasked
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (always the same limit: calls on other threads, and captured ones, must not find it lowered)
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kMostKeys);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -622,7 +624,7 @@ cudaError_t launch_evict(const pkd_evict_args& a, cudaStream_t s) {
   const bool small = units > 2 * sms && tokens <= 6000;
   // room for the average and a half of it, up to what leaves the SM its CTAs: 32 KiB and 64 KiB (512 units of
   // 2,064 tokens, 256 threads each: 26.6 us with 32 KiB, 29.6 with 64)
-  const int most = small ? 8 << 10 : 16 << 10;
+  const int most = small ? kMostKeys / 2 : kMostKeys;
   p.cap = 1024;
   while (p.cap < most && p.cap < tokens / ranks + tokens / ranks / 2) p.cap *= 2;
   // 64 sequences of 2,064 tokens with 128 newest, not in L2: 26.0 us for 28.4; up to what L2 holds beside

@@ -242,6 +242,39 @@ def test_two_streams():
         check_evicted(pg, lens, before, w0, _pools(pg), w, k, 200, 4, 50)
 
 
+def test_calls_of_different_sizes_from_two_threads():
+    """Calls that ask for more and less shared memory, at the same time."""
+    import threading
+    sets = []
+    for i, n in enumerate((30000, 3500)):
+        lens = [n] * (2 if i == 0 else 6)
+        pg = Pages(lens, 16, 2, 64, "same", "NHD", seed=20 + i)
+        w = _weights(pg, lens, seed=i)
+        sets.append((pg, lens, w, _pools(pg), w.clone(), pg.pool.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(pg, lens, w, before, w0, pool0, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(40):
+                    pg.pool.copy_(pool0)
+                    w.copy_(w0)
+                    _evict(pg, lens, w, 1000, 4, 100)
+        except Exception as e:  # pragma: no cover
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=s) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for pg, lens, w, before, w0, _, _ in sets:
+        check_evicted(pg, lens, before, w0, _pools(pg), w, None, 1000, 4, 100)
+
+
 def test_refusals():
     from paged_kv_decode_23_gb300 import PkdError, evict_paged_kv
     lens = [300, 40]
