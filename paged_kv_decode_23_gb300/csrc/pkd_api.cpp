@@ -158,8 +158,7 @@ struct pkd_handle {
   size_t tmap_next = 0;
   int gslices = 1;
   int64_t n_tasks = 0;
-  bool sinks = false;        // the plan's kernel takes sinks
-  bool key_weights = false;  // its runs sum their keys' weights
+  bool key_weights = false;  // the plan's runs sum their keys' weights
   KeyWsLayout klayout{};
   int n_key_tiles = 0;
 
@@ -679,7 +678,7 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
       return fail(PKD_ERR_INVALID_ARG, "CUDA-graph mode: the handle holds MLA plans");
     if (h->g_batch >= 0 && key_weights != h->key_weights)
       return fail(PKD_ERR_INVALID_ARG, "CUDA-graph mode: key_weights is fixed by the first plan");
-    if (h->g_batch >= 0 && args->num_sink_tokens > 0 && !h->sinks)
+    if (h->g_batch >= 0 && args->num_sink_tokens > 0 && !h->kernel->sinks)
       return fail(PKD_ERR_INVALID_ARG,
                   "CUDA-graph mode: the first plan had no sinks, so captured runs take none");
   }
@@ -694,7 +693,7 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   rc = decode_geometry(r, &sch, &err);
   if (rc) return fail(rc, err);
   // (CUDA-graph mode: the first plan's choice, which captured runs hold)
-  const bool sinks = h->graph && h->g_batch >= 0 ? h->sinks : r.num_sinks > 0 || key_weights;
+  const bool sinks = h->graph && h->g_batch >= 0 ? h->kernel->sinks != 0 : r.num_sinks > 0;
   const DecodeKernel* k =
       find_decode(sch.kind, q_dtype, kv_dtype, head_dim, sch.heads_per_cta, r.rope, sinks, key_weights);
   if (!k) return fail(PKD_ERR_UNSUPPORTED, "no decode kernel built for this dtype / head_dim");
@@ -832,7 +831,6 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   h->cap = logits_soft_cap > 0.f ? logits_soft_cap : 0.f;
   h->indices = h->graph ? h->g_indices : indices_dev;
   h->dlayout = lay;
-  h->sinks = sinks;
   h->key_weights = key_weights;
   h->klayout = klay;
   h->n_key_tiles = (int)n_key_tiles;

@@ -157,3 +157,8 @@ def test_captured_runs_without_sinks_take_none_later():
     with pytest.raises(PkdError, match="no sinks"):
         dec.plan(*args, q_data_type=BF16, window_left=100, num_sink_tokens=4)
     dec.plan(*args, q_data_type=BF16, window_left=50)
+    # the CUDA-core kernel takes them anyway
+    dec = CUDAGraphBatchDecodePagedKV(torch.zeros(64 << 20, dtype=torch.uint8, device="cuda"), torch.zeros(2, **i32),
+                                      torch.zeros(64, **i32), torch.zeros(1, **i32), "NHD", use_tensor_cores=False)
+    dec.plan(*args, q_data_type=BF16, window_left=100)
+    dec.plan(*args, q_data_type=BF16, window_left=100, num_sink_tokens=4)
