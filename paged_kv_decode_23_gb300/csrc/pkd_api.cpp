@@ -72,7 +72,8 @@ const DecodeKernel* find_decode(int kind, int q_dtype, int kv_dtype, int head_di
   init_registry();
   for (const auto& k : g_decode)
     if (k.kind == kind && k.q_dtype == q_dtype && k.kv_dtype == kv_dtype &&
-        k.head_dim == head_dim && k.heads_per_cta == heads && k.rope == rope && k.sinks >= (int)sinks && k.scores == (int)scores)
+        k.head_dim == head_dim && k.heads_per_cta == heads && k.rope == rope &&
+        k.sinks >= (int)sinks && k.scores == (int)scores)
       return &k;
   return nullptr;
 }
@@ -951,8 +952,8 @@ bool entries_apart(const int64_t strides[3], const int64_t n[3]) {
 // pkd_run_timed (sf and kw null), pkd_run_scaled and pkd_run_key_weights.
 int run_decode(pkd_handle* h, const void* q, const void* k_base, const void* v_base,
                int64_t num_pages, const int64_t kv_strides[3], const ScalePools* sf,
-               const WeightPool* kw, float q_scale, float k_scale, float v_scale, void* o, float* lse, void* stream, void* ev_start,
-               void* ev_end) {
+               const WeightPool* kw, float q_scale, float k_scale, float v_scale, void* o, float* lse,
+               void* stream, void* ev_start, void* ev_end) {
   if (!h) return fail(PKD_ERR_INVALID_ARG, "handle is null");
   if (!h->planned || h->mla)
     return fail(PKD_ERR_NOT_PLANNED, "pkd_run called before a successful pkd_plan");
