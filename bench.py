@@ -50,7 +50,7 @@ MEASURED_TRAFFIC = {
 
 # The files that decide what the decode kernel reads and writes: its device code and the
 # planner that cuts its work list (host API and no-allocation code are left out).
-KERNEL_SOURCES = ("decode_kernels.cuh", "pkd_device.cuh", "pkd_internal.h", "decode_f16.cu",
+KERNEL_SOURCES = ("decode_kernels.cuh", "decode_geometries.cuh", "pkd_device.cuh", "pkd_internal.h", "decode_f16.cu",
                   "decode_bf16.cu", "decode_e4m3.cu", "planner.cpp")
 
 

@@ -19,11 +19,12 @@ LIB = os.path.join(BUILD, "libpkd.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["decode_f16.cu", "decode_bf16.cu", "decode_e4m3.cu", "decode_rope.cu",
            "decode_rope_cc.cu", "decode_rope_cc_e4m3.cu", "mla.cu",
+           "decode_sinks_rope_cc.cu", "decode_sinks_rope_cc_e4m3.cu", "decode_sinks_cc.cu",
            "decode_e2m1.cu", "decode_sinks.cu", "decode_scores.cu", "decode_e2m1_sinks.cu",
            "decode_e2m1_scores.cu", "key_weights.cu", "cache_append.cu", "cache_gather.cu", "cache_evict.cu",
            "cache_copy.cu", "cache_api.cpp",
            "mla_tc.cu", "planner.cpp", "pkd_api.cpp", "noalloc.cu"]
-HEADERS = ["pkd_internal.h", "pkd_device.cuh", "decode_kernels.cuh",
+HEADERS = ["pkd_internal.h", "pkd_device.cuh", "decode_kernels.cuh", "decode_geometries.cuh",
            "decode_e2m1_kernels.cuh", "cache_ops.cuh", "cache_rows.cuh",
            "mla_kernels.cuh", "mla_tc_kernels.cuh"]
 

@@ -80,12 +80,8 @@ struct RopeGeom {
   static_assert(ROW >= 128, "the row swizzle flips bit 6 of an offset inside the row");
 };
 
-// What a tensor-core instance can do beside plain decode: nothing; sinks; sinks and leaving scores.  The
-// CUDA-core and the rotating kernels have one instance, which takes sinks.
+// What an instance can do beside plain decode: nothing; sinks; sinks and leaving scores.
 enum Bounded { kUnbounded = 0, kSinks = 1, kScores = 2 };
-__host__ __device__ constexpr bool takes_sinks(int kind, bool rope, int bounded) {
-  return kind != kTensorCore || rope || bounded != kUnbounded;
-}
 
 struct BlockCoords {
   DecodeTask it;
@@ -1156,7 +1152,7 @@ __device__ __forceinline__ void cc_rotate_q(const DecodeParams& p, const BlockCo
 // row - 8 from there (the partner dims of a rotation pair are on lane ^ 16): the logit
 // depends only on the difference of the two positions.
 // Returns false when a pipeline wait gave up (the CTA's consumers then leave together).
-template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int GP, bool ROPE>
+template <typename TQ, bool KV_FP8, int D, int TS, int NSTAGES, int GP, bool ROPE, bool SINKS>
 __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoords& b,
                                            uint32_t smem, uint8_t* smem_p, uint32_t full0,
                                            uint32_t empty0, volatile int* abort_flag, int warp,
@@ -1208,7 +1204,7 @@ __device__ __forceinline__ bool consume_cc(const DecodeParams& p, const BlockCoo
     lsum_h[j] = 0.f;
   }
 
-  TileRun<true, TS> run(b);
+  TileRun<SINKS, TS> run(b);
   for (int i = 0; i < b.ntiles; ++i) {
     const int s = i % NSTAGES;
     run.move(p, b, i);
@@ -1432,7 +1428,7 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
   using namespace dev;
   using G = DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>;
   constexpr int HEADS = KIND == kTensorCore ? 8 : GP;
-  constexpr bool SINKS = takes_sinks(KIND, ROPE, BOUNDED);
+  constexpr bool SINKS = BOUNDED != kUnbounded;
   __shared__ __align__(8) uint64_t bars[2 * NSTAGES];
   __shared__ int abort_flag_s;
   __shared__ int merge_last_s;
@@ -1494,7 +1490,7 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
   } else {
     cc_setup<TQ, KV_FP8, D, GP, G::NW, ROPE>(p, b, smem_p + G::PIPE_BYTES, threadIdx.x, G::NCONS);
     named_bar_sync(2, G::NCONS);
-    if (!consume_cc<TQ, KV_FP8, D, TS, NSTAGES, GP, ROPE>(p, b, smem, smem_p, full0, empty0,
+    if (!consume_cc<TQ, KV_FP8, D, TS, NSTAGES, GP, ROPE, SINKS>(p, b, smem, smem_p, full0, empty0,
                                                           abort_flag, warp, lane, epi))
       return;
   }
@@ -1517,7 +1513,7 @@ DecodeKernel make_decode_kernel(int q_dtype, int kv_dtype) {
   k.fn = reinterpret_cast<const void*>(
       &decode_paged_kernel<TQ, KV_FP8, D, TS, NSTAGES, KIND, GP, ROPE, BOUNDED>);
   k.rope = ROPE ? 1 : 0;
-  k.sinks = takes_sinks(KIND, ROPE, BOUNDED) ? 1 : 0;
+  k.sinks = BOUNDED != kUnbounded ? 1 : 0;
   k.scores = BOUNDED == kScores ? 1 : 0;
   k.nstages = NSTAGES;
   k.threads = G::THREADS;

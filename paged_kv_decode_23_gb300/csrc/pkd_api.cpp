@@ -51,6 +51,9 @@ void init_registry() {
     register_decode_rope_cc_e4m3(g_decode);
     register_decode_e2m1(g_decode);
     register_decode_sinks(g_decode);
+    register_decode_sinks_cc(g_decode);
+    register_decode_sinks_rope_cc(g_decode);
+    register_decode_sinks_rope_cc_e4m3(g_decode);
     register_decode_scores(g_decode);
     register_decode_e2m1_sinks(g_decode);
     register_decode_e2m1_scores(g_decode);
@@ -693,8 +696,10 @@ int plan_with(pkd_handle* h, const pkd_plan_args* args, void* stream) {
   const char* err = "";
   rc = decode_geometry(r, &sch, &err);
   if (rc) return fail(rc, err);
-  // (CUDA-graph mode: the first plan's choice, which captured runs hold)
-  const bool sinks = h->graph && h->g_batch >= 0 ? h->kernel->sinks != 0 : r.num_sinks > 0;
+  // (CUDA-graph mode: the first plan's choice, which captured runs hold; on the CUDA cores and with
+  // ROPE_LLAMA later plans may have sinks whatever the first has)
+  const bool sinks = r.num_sinks > 0 || (h->graph && (sch.kind == kCudaCore || r.rope)) ||
+                     (h->graph && h->g_batch >= 0 && h->kernel->sinks != 0);
   const DecodeKernel* k =
       find_decode(sch.kind, q_dtype, kv_dtype, head_dim, sch.heads_per_cta, r.rope, sinks, key_weights);
   if (!k) return fail(PKD_ERR_UNSUPPORTED, "no decode kernel built for this dtype / head_dim");

@@ -189,6 +189,9 @@ void register_decode_rope_cc(std::vector<DecodeKernel>& out);
 void register_decode_rope_cc_e4m3(std::vector<DecodeKernel>& out);
 void register_decode_e2m1(std::vector<DecodeKernel>& out);
 void register_decode_sinks(std::vector<DecodeKernel>& out);
+void register_decode_sinks_cc(std::vector<DecodeKernel>& out);
+void register_decode_sinks_rope_cc(std::vector<DecodeKernel>& out);
+void register_decode_sinks_rope_cc_e4m3(std::vector<DecodeKernel>& out);
 void register_decode_scores(std::vector<DecodeKernel>& out);
 void register_decode_e2m1_sinks(std::vector<DecodeKernel>& out);
 void register_decode_e2m1_scores(std::vector<DecodeKernel>& out);

@@ -162,3 +162,20 @@ def test_captured_runs_without_sinks_take_none_later():
                                       torch.zeros(64, **i32), torch.zeros(1, **i32), "NHD", use_tensor_cores=False)
     dec.plan(*args, q_data_type=BF16, window_left=100)
     dec.plan(*args, q_data_type=BF16, window_left=100, num_sink_tokens=4)
+
+
+@pytest.mark.parametrize("pos", ["NONE", "ROPE_LLAMA"])
+@pytest.mark.parametrize("kv,d", [("same", 64), ("same", 128), ("same", 256), ("e4m3", 128), ("e4m3", 256)])
+def test_instances_with_and_without_sinks_agree(kv, d, pos):
+    """A plan whose sinks leave no gap runs an instance that takes sinks, one without them (mostly) another:
+    the same bits, for every group of query heads of either kernel."""
+    for dtype in (BF16, F16):
+        pg = Pages([900, 1, 40, 0, 1333], 16, 2, d, kv, "NHD", seed=12, dtype=dtype)
+        for group, tc in ((1, False), (2, False), (3, False), (8, False), (4, True)):
+            q = _q(5, 2 * group, d, dtype)
+            got = []
+            for opt in (dict(num_sink_tokens=5), {}):
+                dec = decoder(pg, 2 * group, dtype, use_tensor_cores=tc, pos_encoding_mode=pos, **opt)
+                got.append(dec.run(q, pg.pool, return_lse=True))
+                assert dec.check_status() == 0
+            assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]), (dtype, group, tc)
