@@ -214,7 +214,7 @@ int pkd_run_scaled(pkd_handle* h, const pkd_scaled_run* run, void* stream);
  * (two launches; ev_end is recorded behind the second).  run's k_scales and v_scales are NULL unless
  * the cache is E2M1.  key_weights: device float32, element (page, head, slot) at page*weight_strides[0]
  * + head*weight_strides[1] + slot*weight_strides[2]; entries must not overlap.  Entries of slots that
- * no row attends are left as they are.  Sums are taken in 32 bits in the order of rows and heads; a page
+ * no row attends are left as they are; a row whose every score is -inf (o = 0, lse = -inf) adds 0.  Sums are taken in 32 bits in the order of rows and heads; a page
  * that several requests share takes their sums in no fixed order, which may change the last bit.  A key whose page id
  * lies outside the pool has no entry (PKD_STATUS_BAD_PAGE); nothing is added after PKD_STATUS_TIMEOUT.
  * The scores lie in the handle's workspace, as split partials do: runs of one handle must not overlap.

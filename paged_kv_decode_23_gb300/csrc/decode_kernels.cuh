@@ -242,6 +242,12 @@ struct EpiView {
   }
 };
 
+// The softmax statistics of a final row, for its keys' weights 2^(s - M) / L.  A row whose every score is -inf
+// has L = 0 and no weights (its M must not meet its scores: -inf - -inf).
+__device__ __forceinline__ float2 row_stats(float M, float inv_l) {
+  return make_float2(M == kNegInf ? 0.f : M, inv_l);
+}
+
 // Combines every warp's state and writes the task's final o / lse, or its fp32 partial.  STATS: a final
 // row's softmax statistics as well.
 template <typename TQ, int D, int NW, bool STATS>
@@ -284,7 +290,7 @@ __device__ __forceinline__ void store_task(const DecodeParams& p, const BlockCoo
       *reinterpret_cast<uint4*>(dst) = v;
       if (d0 == 0 && p.lse) p.lse[(size_t)b.it.req * p.num_qo_heads + qo] = lse2 * kLn2;
       if (STATS && d0 == 0)
-        p.stats[(size_t)b.it.req * p.num_qo_heads + qo] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
+        p.stats[(size_t)b.it.req * p.num_qo_heads + qo] = row_stats(M, L > 0.f ? 1.f / L : 0.f);
     } else {
       float* dst = p.part_o + ((size_t)b.it.out_slot * kSlotHeads + g) * D + d0;
       reinterpret_cast<float4*>(dst)[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
@@ -379,7 +385,7 @@ __device__ __forceinline__ void merge_unit(const DecodeParams& p, const BlockCoo
     *reinterpret_cast<uint4*>(dst) = v;
     if (d0 == 0 && p.lse)
       p.lse[(size_t)me.req * hq + qo] = L > 0.f ? (M + log2f(L)) * kLn2 : kNegInf;
-    if (STATS && d0 == 0) p.stats[(size_t)me.req * hq + qo] = make_float2(M, inv);
+    if (STATS && d0 == 0) p.stats[(size_t)me.req * hq + qo] = row_stats(M, inv);
   }
 }
 

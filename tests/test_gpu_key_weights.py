@@ -143,6 +143,28 @@ def test_dominant_and_far_keys():
     assert_weights(pg, got, before, decode_ref(pg, values(pg.pool), q)[3])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_rows_of_infinitely_low_scores_have_no_weights(dtype):
+    """Requests whose every score is -inf (one task, and split into several), and one with some such keys: no
+    weight and no NaN is added for them."""
+    lens = [40, 9000, 300]
+    pg = Pages(lens, 16, 2, 128, "same", "NHD", seed=21, dtype=dtype)
+    low = {0: range(40), 1: range(9000), 2: (0, 17, 18, 299)}
+    for b, tokens in low.items():
+        page, slot = pg.where(np.full(len(tokens), b), np.array(tokens))
+        pg.pool[torch.from_numpy(page).long().cuda(), 0, torch.from_numpy(slot).long().cuda(), :, 0] = -float("inf")
+    q = _q(3, 8, 128, dtype)
+    q[..., 0] = 1.0
+    dec = decoder(pg, 8, dtype, key_weights=True)
+    before = _weights(pg)
+    got = before.clone()
+    o, lse = dec.run(q, pg.pool, key_weights=got, return_lse=True)
+    assert dec.check_status() == 0
+    assert (o[:2] == 0).all() and torch.isneginf(lse[:2]).all() and torch.isfinite(lse[2]).all()
+    ref = decode_ref(pg, values(pg.pool), q)
+    assert_weights(pg, got, before, {2: ref[3][2]})
+
+
 def test_bad_pages_have_no_weights():
     pg = Pages([100, 30], 16, 2, 128, "same", "NHD", seed=4)
     ids = pg.host_indices.copy()
