@@ -398,9 +398,12 @@ class BatchDecodePagedKV:
     def _run_scaled(self, q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse, stream,
                     timing_events, enable_pdl, weights=None):
         """run() on a plan with a 4-bit cache or with key weights; q's shape and dtype are checked."""
-        if (torch.is_grad_enabled() and (q.requires_grad or (weights is not None and weights.requires_grad))
+        kv, second = cache if isinstance(cache, (tuple, list)) else (cache, None)
+        if (torch.is_grad_enabled() and (q.requires_grad or kv.requires_grad or (second is not None and second.requires_grad)
+                                         or (weights is not None and weights.requires_grad))
                 ) or forward_ad._current_level >= 0:
-            refuse_gradients("decode over a 4-bit cache" if weights is None else "decode with key weights", q, weights)
+            refuse_gradients("decode over a 4-bit cache" if weights is None else "decode with key weights", q, kv, second,
+                             weights)
         a = self._plan_args
         rows, hq, d, ps, hkv = a["rows"], a["num_qo_heads"], a["head_dim"], a["page_size"], a["num_kv_heads"]
         dev = q.get_device()
@@ -408,7 +411,6 @@ class BatchDecodePagedKV:
             with torch.cuda.device(dev):
                 return self._run_scaled(q, cache, scales, q_scale, k_scale, v_scale, out, lse, return_lse,
                                         stream, timing_events, enable_pdl, weights)
-        kv = cache[0] if isinstance(cache, (tuple, list)) else cache
         k_ptr, v_ptr, strides, kv_ps, kv_hkv = pool_views(cache, self.kv_layout)
         pages = kv.shape[0]
         if scales is None:

@@ -308,3 +308,17 @@ def test_workspace_bytes_are_enough():
         # every row with a key adds a weight of 1 per qo head (4 of them a kv head)
         rows = 3 * opt.get("q_len_per_req", 1)
         assert abs(float(w.double().sum()) - rows * 8) < 1e-4 * rows * 8
+
+
+def test_a_cache_whose_gradient_would_be_lost_is_refused():
+    pg = Pages([300, 40], 16, 2, 128, "same", "NHD", seed=10)
+    q = _q(2, 8, 128, BF16)
+    w = torch.zeros(pg.num_pages, 2, 16, device="cuda")
+    dec = decoder(pg, 8, BF16, key_weights=True)
+    k, v = pg.pool[:, 0].contiguous(), pg.pool[:, 1].contiguous()
+    for cache in (pg.pool.clone().requires_grad_(), (k.clone().requires_grad_(), v), (k, v.clone().requires_grad_())):
+        with pytest.raises(NotImplementedError, match="no backward pass"):
+            dec.run(q, cache, key_weights=w)
+        with torch.no_grad():
+            dec.run(q, cache, key_weights=torch.zeros_like(w))
+    assert (w == 0).all()
