@@ -131,7 +131,8 @@ def new_output(shape, like, dtype, stream):
 
 def _plan_args(*fields) -> bytes:
     try:
-        return _PLAN.pack(*fields)
+        # (fields 4 to 7 are 32-bit floats: one that does not fit is infinite, which the plan refuses)
+        return _PLAN.pack(*fields[:4], *(ctypes.c_float(x).value for x in fields[4:8]), *fields[8:])
     except struct.error as e:
         raise ValueError(f"a number of the plan does not fit 32 bits ({e})") from None
 

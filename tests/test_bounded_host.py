@@ -199,3 +199,16 @@ def test_an_eviction_of_nothing_needs_no_gpu():
     from paged_kv_decode_23_gb300 import _lib as L
     assert L.lib().pkd_evict(None, None) == -1
     assert L.lib().pkd_evict(_evict_args(batch=0), None) == 0
+
+
+@pytest.mark.parametrize("at,name", [(4, "sm_scale"), (5, "logits_soft_cap"), (6, "rope_scale"), (7, "rope_theta")])
+def test_numbers_past_32_bits_reach_the_plan_as_infinite(at, name):
+    """(which refuses them, as one call of pkd_plan with 32-bit arguments did)"""
+    import struct
+    from paged_kv_decode_23_gb300 import decode
+    fields = [0] * 4 + [0.5, 1.0, 2.0, 1e4] + [1] * 16
+    fields[at] = 1e300
+    got = struct.unpack("@3Pq4f16i", decode._plan_args(*fields))
+    assert got[at] == float("inf") and got[:at] == tuple(fields[:at]) and got[at + 1:] == tuple(fields[at + 1:])
+    with pytest.raises(ValueError, match="32 bits"):
+        decode._plan_args(*fields[:8], 2 ** 31, *fields[9:])

@@ -322,3 +322,12 @@ def test_a_cache_whose_gradient_would_be_lost_is_refused():
         with torch.no_grad():
             dec.run(q, cache, key_weights=torch.zeros_like(w))
     assert (w == 0).all()
+
+
+@pytest.mark.parametrize("opt", [dict(sm_scale=1e300), dict(logits_soft_cap=1e39), dict(pos_encoding_mode="ROPE_LLAMA", rope_theta=1e39),
+                                 dict(pos_encoding_mode="ROPE_LLAMA", rope_scale=float("inf"))])
+def test_infinite_numbers_are_refused(opt):
+    from paged_kv_decode_23_gb300 import PkdError
+    pg = Pages([30], 16, 2, 128, "same", "NHD", seed=11)
+    with pytest.raises(PkdError, match="finite"):
+        decoder(pg, 8, BF16, **opt)
