@@ -410,3 +410,48 @@ def test_a_bounded_cache_step_after_step(kv):
         for i in range(n):
             used[t[i // page], i % page] = True
     assert (weights.cpu().transpose(1, 2)[~used] == 0).all()  # slots without a token hold no weight
+
+
+def _many(heads, extra=2):
+    """So many sequences of `heads` kv heads that a (sequence, kv head) of each would fill two CTAs an SM, and `extra`."""
+    return 2 * torch.cuda.get_device_properties(0).multi_processor_count // heads + extra
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties", "odd"])
+@pytest.mark.parametrize("kv,layout", [("same", "NHD"), ("e4m3", "HND"), ("e2m1", "NHD")])
+def test_more_sequences_than_the_gpu_holds(kv, layout, kind):
+    """CTAs of 256 threads, one a (sequence, kv head): ragged lengths, one sequence past the keys that a CTA can
+    hold (8,192) and many past those that it does hold for the average length."""
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 700, _many(8)).tolist()
+    lens[0], lens[1], lens[7], lens[-1] = 9500, 8200, 2300, 3000
+    pg = Pages(lens, 16, 8, 64, kv, layout, seed=30)
+    w = _weights(pg, lens, seed=31, kind=kind)
+    before, w0 = _pools(pg), w.clone()
+    kept = _evict(pg, lens, w, 256, 4, 37, return_kept=True)
+    check_evicted(pg, lens, before, w0, _pools(pg), w, kept, 256, 4, 37)
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties"])
+def test_many_sequences_cut_back_after_a_few_steps(kind):
+    """The same CTAs, their keys all in shared memory."""
+    lens = np.random.default_rng(2).integers(2049, 2065, _many(8)).tolist()
+    pg = Pages(lens, 16, 8, 64, "same", "NHD", seed=32)
+    w = _weights(pg, lens, seed=33, kind=kind)
+    before, w0 = _pools(pg), w.clone()
+    kept = _evict(pg, lens, w, 2048, 4, 128, return_kept=True)
+    check_evicted(pg, lens, before, w0, _pools(pg), w, kept, 2048, 4, 128)
+
+
+def test_more_long_sequences_than_the_gpu_holds():
+    """Above 6,000 tokens a sequence (by the pages that the table lists) CTAs of 512 threads, in several waves."""
+    from paged_kv_decode_23_gb300 import evict_paged_kv
+    lens = np.random.default_rng(3).integers(0, 700, _many(8, 200)).tolist()
+    lens[3] = 9000
+    pg = Pages(lens, 16, 8, 64, "same", "HND", seed=34)
+    w = _weights(pg, lens, seed=35)
+    before, w0 = _pools(pg), w.clone()
+    indices = torch.cat([pg.indices, torch.zeros(6100 * len(lens) // 16, dtype=torch.int32, device="cuda")])
+    kept = evict_paged_kv(pg.pool, w, torch.tensor(lens, dtype=torch.int32, device="cuda"), pg.indptr, indices, 200, "HND",
+                          num_sink_tokens=3, num_recent=30, return_kept=True)
+    check_evicted(pg, lens, before, w0, _pools(pg), w, kept, 200, 3, 30)
