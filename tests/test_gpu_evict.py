@@ -455,3 +455,41 @@ def test_more_long_sequences_than_the_gpu_holds():
     kept = evict_paged_kv(pg.pool, w, torch.tensor(lens, dtype=torch.int32, device="cuda"), pg.indptr, indices, 200, "HND",
                           num_sink_tokens=3, num_recent=30, return_kept=True)
     check_evicted(pg, lens, before, w0, _pools(pg), w, kept, 200, 3, 30)
+
+
+def test_calls_of_one_kernel_that_need_less_and_more_shared_memory_from_two_threads(monkeypatch):
+    """Both take the CTAs of a cluster, with 32 and 64 KiB of keys: more than a launch may ask for before its
+    kernel's limit is raised, so that a call that lowered it would fail the other's launch.  The threads make the
+    library's call alone, over and over, so that the calls meet (sequences inside the budget: nothing moves)."""
+    import threading
+    from paged_kv_decode_23_gb300 import _lib as L, cache
+    sets, packed = [], []
+    for i, n in enumerate((30000, 60000)):
+        pg = Pages([n], 16, 2, 64, "same", "NHD", seed=40 + i)
+        w = _weights(pg, [n], seed=i)
+        sets.append((pg, n, w, _pools(pg), w.clone(), torch.tensor([1000], dtype=torch.int32, device="cuda")))
+        with monkeypatch.context() as m:
+            m.setattr(cache, "_launch", lambda call, dev, stream, *args: packed.append(args))
+            cache.evict_paged_kv(pg.pool, w, sets[-1][-1], pg.indptr, pg.indices, 1000, num_sink_tokens=4, num_recent=100)
+    torch.cuda.synchronize()
+    failed = []
+    start = threading.Barrier(len(sets))
+
+    def work(args, stream):
+        start.wait()
+        for _ in range(20000):
+            if L.lib().pkd_evict(*args, stream.cuda_stream):
+                failed.append(L.lib().pkd_last_error())
+                return
+
+    threads = [threading.Thread(target=work, args=(a, torch.cuda.Stream())) for a in packed]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for pg, n, w, before, w0, _ in sets:
+        assert torch.equal(w, w0) and all(torch.equal(x, y) for x, y in zip(before, _pools(pg)))
+        _evict(pg, [n], w, 1000, 4, 100)
+        check_evicted(pg, [n], before, w0, _pools(pg), w, None, 1000, 4, 100)
