@@ -331,3 +331,44 @@ def test_infinite_numbers_are_refused(opt):
     pg = Pages([30], 16, 2, 128, "same", "NHD", seed=11)
     with pytest.raises(PkdError, match="finite"):
         decoder(pg, 8, BF16, **opt)
+
+
+def test_more_keys_than_the_second_kernels_grid_holds():
+    """So many (tile of keys, kv head)s that its CTAs (16 an SM at most) take several, with and without sinks; and
+    the same plan in CUDA-graph mode, replayed."""
+    from paged_kv_decode_23_gb300 import CUDAGraphBatchDecodePagedKV, graph_workspace_bytes
+    hkv, hq, d, page = 8, 16, 64, 8
+    ctas = 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    batch = 2 * ctas // hkv + 10  # a tile each at least
+    lens = np.random.default_rng(5).integers(1, 65, batch)
+    lens[5], lens[-1], lens[17] = 1700, 2000, 0
+    pg = Pages(lens.tolist(), page, hkv, d, "same", "NHD", seed=12, dtype=F16)
+    pool64 = values(pg.pool)
+    q = _q(batch, hq, d, F16)
+    for opt in ({}, dict(window_left=9, num_sink_tokens=5)):
+        ref = decode_ref(pg, pool64, q, window=opt.get("window_left", -1), sinks=opt.get("num_sink_tokens", 0))
+        before = _weights(pg)
+        got = before.clone()
+        dec = decoder(pg, hq, F16, key_weights=True, **opt)
+        dec.run(q, pg.pool, key_weights=got)
+        assert dec.check_status() == 0
+        assert_weights(pg, got, before, ref[3])
+        i32 = dict(dtype=torch.int32, device="cuda")
+        items, pages = batch + 2 * 152, len(pg.host_indices)
+        fb, ib = graph_workspace_bytes(items, hq, hkv, d, key_weights_pages=pages, page_size=page, max_batch=batch)
+        dec = CUDAGraphBatchDecodePagedKV(torch.zeros(fb, dtype=torch.uint8, device="cuda"), torch.zeros(batch + 1, **i32),
+                                          torch.zeros(pages, **i32), torch.zeros(batch, **i32), "NHD", max_items=items,
+                                          int_workspace_buffer=torch.zeros(ib, dtype=torch.uint8, device="cuda"))
+        dec.plan(torch.from_numpy(pg.host_indptr), pg.indices, torch.from_numpy(pg.last), hq, hkv, d, page, q_data_type=F16,
+                 key_weights=True, **opt)
+        o, w = torch.zeros_like(q), before.clone()
+        dec.run(q, pg.pool, out=o, key_weights=w)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            dec.run(q, pg.pool, out=o, key_weights=w)
+        w.copy_(before)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dec.check_status() == 0
+        assert_weights(pg, w, before, ref[3], what="replayed")
