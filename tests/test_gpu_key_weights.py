@@ -372,3 +372,25 @@ def test_more_keys_than_the_second_kernels_grid_holds():
         torch.cuda.synchronize()
         assert dec.check_status() == 0
         assert_weights(pg, w, before, ref[3], what="replayed")
+
+
+def test_a_run_that_timed_out_adds_nothing():
+    """Waits that give up at once, over keys that are not in L2: the status says so, and no entry changes."""
+    from paged_kv_decode_23_gb300 import _lib as L
+    pg = Pages([3000, 17, 2000, 4000, 1000, 700, 0, 2500] * 4, 16, 2, 128, "same", "NHD", seed=13)
+    dec = decoder(pg, 8, BF16, key_weights=True, fixed_split_size=8)
+    q = _q(32, 8, 128, BF16)
+    before = _weights(pg)
+    want = before.clone()
+    dec.run(q, pg.pool, key_weights=want)
+    assert dec.check_status() == 0
+    got = before.clone()
+    dec.set_wait_limit(0)
+    torch.zeros(300 << 20, dtype=torch.uint8, device="cuda")
+    dec.run(q, pg.pool, key_weights=got)
+    dec.set_wait_limit(2 * 10 ** 9)
+    dec.run(q, pg.pool, key_weights=got)  # (the word is still set)
+    assert dec.check_status() & L.STATUS_TIMEOUT
+    assert torch.equal(got, before)
+    dec.run(q, pg.pool, key_weights=got)
+    assert dec.check_status() == 0 and torch.equal(got, want)
