@@ -131,8 +131,9 @@ def new_output(shape, like, dtype, stream):
 
 def _plan_args(*fields) -> bytes:
     try:
-        # (fields 4 to 7 are 32-bit floats: one that does not fit is infinite, which the plan refuses)
-        return _PLAN.pack(*fields[:4], *(ctypes.c_float(x).value for x in fields[4:8]), *fields[8:])
+        return _PLAN.pack(*fields)
+    except OverflowError:  # fields 4 to 7: a number that no 32-bit float holds is infinite, which the plan refuses
+        return _plan_args(*fields[:4], *(ctypes.c_float(x).value for x in fields[4:8]), *fields[8:])
     except struct.error as e:
         raise ValueError(f"a number of the plan does not fit 32 bits ({e})") from None
 
