@@ -362,7 +362,8 @@ int pkd_workspace_bytes(const int32_t* indptr_host, const int32_t* last_page_len
  *                    t >= p - window_left.  Keys in between are not read: their pages may be freed
  *                    and their entries of `indices` may hold anything.  Positions (ALiBi, RoPE)
  *                    stay the tokens' own.  No effect with window_left < 0.  CUDA-graph mode: later
- *                    plans may have sinks where the first one has (> 0), or has key weights.
+ *                    plans may have sinks where the first one has (> 0) or has key weights, and
+ *                    on the CUDA-core kernel and with ROPE_LLAMA whatever the first one has.
  *   key_weights      1: the plan's runs are pkd_run_key_weights, which also adds every key's softmax
  *                    weight to a pool of sums.  The workspaces then hold the scores of all attended
  *                    keys (4 bytes a key, row and qo head) as well.  Tensor-core kernel, without

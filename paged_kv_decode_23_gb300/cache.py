@@ -266,8 +266,9 @@ def evict_paged_kv(paged_kv_cache, key_weights: torch.Tensor, kv_lens: torch.Ten
     """Cut every sequence back to ``budget`` tokens, in place (pkd_evict): each kv head keeps its first
     ``num_sink_tokens``, its newest ``num_recent`` and the tokens with the largest ``key_weights``
     (float32 ``[pages, num_kv_heads, page_size]``, what ``BatchDecodePagedKV.run`` adds to).
-    ``kv_lens`` (device int32 ``[batch]``) are the sequences' lengths; afterwards they are
-    ``min(kv_lens, budget)``, and the pages behind may be freed (``PageAllocator.free``).
+    ``kv_lens`` (device int32 ``[batch]``) are the sequences' lengths, which the call reads and leaves as
+    they are; the new ones are ``min(kv_lens, budget)``, and the pages behind may be freed
+    (``PageAllocator.free``).
 
     The first tokens stay in place, the newest lie at the end in order, the others in any slots
     between (those that can stay do), so append later keys with ``rope_positions`` of their own and

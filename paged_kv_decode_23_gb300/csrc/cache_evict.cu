@@ -623,7 +623,8 @@ cudaError_t launch_evict(const pkd_evict_args& a, cudaStream_t s) {
   // 5,000 161, 159; of 9,000 184, 217; of 16,000 225, 311; 1,024 of 1,040 55, 44).
   const bool small = units > 2 * sms && tokens <= 6000;
   // room for the average and a half of it, up to what leaves the SM its CTAs: 32 KiB and 64 KiB (512 units of
-  // 2,064 tokens, 256 threads each: 26.6 us with 32 KiB, 29.6 with 64)
+  // 2,064 tokens, 256 threads each: 26.6 us with 32 KiB, 29.6 with 64).  Sequences longer than that read the rest
+  // of their keys again in every pass
   const int most = small ? kMostKeys / 2 : kMostKeys;
   p.cap = 1024;
   while (p.cap < most && p.cap < tokens / ranks + tokens / ranks / 2) p.cap *= 2;

@@ -264,7 +264,8 @@ class BatchDecodePagedKV:
 
         ``key_weights=True``: runs of this plan take a ``key_weights`` pool and add every key's
         softmax weight to it (tensor-core kernel, without ROPE_LLAMA).  The float workspace then also
-        holds the attended keys' scores, 4 bytes a key, row and query head (``workspace_bytes``)."""
+        holds the attended keys' scores, 4 bytes a key, row and query head (``workspace_bytes``; 539 MB
+        for 32 rows of 131,072 keys and 32 heads)."""
         if block_tables is not None or seq_lens is not None:
             raise NotImplementedError("block_tables / seq_lens (the trtllm-gen backend's page "
                                       "table form) are not built; pass indptr / indices / "

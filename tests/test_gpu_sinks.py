@@ -179,3 +179,31 @@ def test_instances_with_and_without_sinks_agree(kv, d, pos):
                 got.append(dec.run(q, pg.pool, return_lse=True))
                 assert dec.check_status() == 0
             assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]), (dtype, group, tc)
+
+
+@pytest.mark.parametrize("tc,pos", [(False, "NONE"), (False, "ROPE_LLAMA"), (True, "ROPE_LLAMA")])
+def test_runs_captured_without_sinks_take_them_later_on_these_kernels(tc, pos):
+    from paged_kv_decode_23_gb300 import CUDAGraphBatchDecodePagedKV
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pg = Pages([900, 133], 16, 2, 128, "same", "NHD", seed=14)
+    dec = CUDAGraphBatchDecodePagedKV(torch.zeros(64 << 20, dtype=torch.uint8, device="cuda"), torch.zeros(3, **i32),
+                                      torch.zeros(128, **i32), torch.zeros(2, **i32), "NHD", use_tensor_cores=tc)
+    q = _q(2, 8, 128, BF16)
+    o, lse = torch.zeros_like(q), torch.zeros(2, 8, device="cuda")
+    graph = None
+    for opt in ({}, dict(window_left=100, num_sink_tokens=9), dict(window_left=50), dict(window_left=300, num_sink_tokens=200)):
+        dec.plan(torch.from_numpy(pg.host_indptr), pg.indices, torch.from_numpy(pg.last), 8, 2, 128, 16, q_data_type=BF16,
+                 pos_encoding_mode=pos, **opt)
+        if graph is None:
+            dec.run(q, pg.pool, out=o, lse=lse)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                dec.run(q, pg.pool, out=o, lse=lse)
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dec.check_status() == 0
+        ref = decode_ref(pg, values(pg.pool), q, window=opt.get("window_left", -1), sinks=opt.get("num_sink_tokens", 0),
+                         pos=None if pos == "NONE" else pos)
+        assert_decode(q, o, lse, ref, values(pg.pool), 900, rope=pos != "NONE", what=str(opt))
