@@ -1488,16 +1488,16 @@ __global__ void __launch_bounds__(DecodeGeom<TQ, KV_FP8, D, TS, NSTAGES>::THREAD
     float acc[D / 16][4];
 #pragma unroll
     for (int mb = 0; mb < D / 16; ++mb) acc[mb][0] = acc[mb][1] = acc[mb][2] = acc[mb][3] = 0.f;
-    consume_tc<TQ, KV_FP8, D, TS, NSTAGES, ROPE, SINKS, BOUNDED == kScores>(p, b, smem, full0, empty0, abort_flag, warp,
-                                                 lane, m2, lsum, acc);
+    consume_tc<TQ, KV_FP8, D, TS, NSTAGES, ROPE, SINKS, BOUNDED == kScores>(p, b, smem, full0, empty0, abort_flag,
+                                                                            warp, lane, m2, lsum, acc);
     // every consumer is done with the stages; one shared decision whether any wait gave up
     if (named_bar_or(1, G::NCONS, *abort_flag != 0)) return;
     stash_tc<D, KV_FP8>(epi, warp, lane, m2, lsum, acc);
   } else {
     cc_setup<TQ, KV_FP8, D, GP, G::NW, ROPE>(p, b, smem_p + G::PIPE_BYTES, threadIdx.x, G::NCONS);
     named_bar_sync(2, G::NCONS);
-    if (!consume_cc<TQ, KV_FP8, D, TS, NSTAGES, GP, ROPE, SINKS>(p, b, smem, smem_p, full0, empty0,
-                                                          abort_flag, warp, lane, epi))
+    if (!consume_cc<TQ, KV_FP8, D, TS, NSTAGES, GP, ROPE, SINKS>(p, b, smem, smem_p, full0, empty0, abort_flag,
+                                                                 warp, lane, epi))
       return;
   }
   named_bar_sync(1, G::NCONS);
